@@ -23,6 +23,7 @@
 #include "../../include/leyline.h"
 #include "host_common.h"
 #include "leyline_internal.h"
+#include "pool_internal.h"
 #include "rows_internal.h"
 #include "alloc_internal.h"
 
@@ -52,117 +53,15 @@ const char* last_error() { return g_error.c_str(); }
 
 namespace {
 
+using ll::align_up;
+using ll::ceil_div;
+using ll::DeviceGuard;
 using ll::fail;
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-// Lowest-free-first page allocator over a bitmap (bit set = free).
-class FreePages {
- public:
-  void init(int64_t n) {
-    n_ = n;
-    words_.assign(static_cast<size_t>(ceil_div(n, 64)), ~0ull);
-    if (n % 64) words_.back() = (1ull << (n % 64)) - 1;
-    count_ = n;
-    hint_ = 0;
-  }
-  int64_t count() const { return count_; }
-  bool is_free(int64_t p) const { return (words_[p >> 6] >> (p & 63)) & 1ull; }
-  void take(int64_t p) {
-    words_[p >> 6] &= ~(1ull << (p & 63));
-    --count_;
-  }
-  void give(int64_t p) {
-    words_[p >> 6] |= 1ull << (p & 63);
-    ++count_;
-    hint_ = std::min<int64_t>(hint_, p >> 6);
-  }
-  // The k lowest free pages, in increasing order (not taken).
-  void lowest(int64_t k, std::vector<int32_t>& out) const {
-    out.clear();
-    out.reserve(static_cast<size_t>(k));
-    for (size_t w = static_cast<size_t>(hint_); w < words_.size() && static_cast<int64_t>(out.size()) < k; ++w) {
-      uint64_t bits = words_[w];
-      while (bits && static_cast<int64_t>(out.size()) < k) {
-        const int b = __builtin_ctzll(bits);
-        out.push_back(static_cast<int32_t>(w * 64 + b));
-        bits &= bits - 1;
-      }
-    }
-  }
-  // Pages marked in `bits` return to the free set, in one pass; false if one
-  // of them was free already or is not a page (the caller then treats the
-  // set as broken).
-  bool give_bits_checked(const uint64_t* bits) {
-    const size_t n = words_.size();
-    if (n && (bits[n - 1] & ~tail_mask())) return false;
-    // branch-free: freed words come in any order of zero and non-zero
-    uint64_t clash = 0;
-    int64_t added = 0;
-    for (size_t w = 0; w < n; ++w) {
-      const uint64_t b = bits[w];
-      clash |= b & words_[w];
-      words_[w] |= b;
-      added += __builtin_popcountll(b);
-    }
-    size_t first = 0;
-    while (first < n && !bits[first]) ++first;
-    count_ += added;
-    hint_ = std::min<int64_t>(hint_, static_cast<int64_t>(first));
-    return clash == 0;
-  }
-  // Pages marked in `bits` (all taken now) return to the free set.
-  void give_bits(const uint64_t* bits) {
-    for (size_t w = 0; w < words_.size(); ++w) {
-      if (!bits[w]) continue;
-      count_ += __builtin_popcountll(bits[w] & ~words_[w]);
-      words_[w] |= bits[w];
-      hint_ = std::min<int64_t>(hint_, static_cast<int64_t>(w));
-    }
-  }
-  size_t num_words() const { return words_.size(); }
-  // The bitmap words (bit set = free), for the device's page plan.
-  void copy_words(uint64_t* out) const { std::memcpy(out, words_.data(), words_.size() * sizeof(uint64_t)); }
-  void advance_hint() {
-    while (hint_ < static_cast<int64_t>(words_.size()) && words_[hint_] == 0) ++hint_;
-  }
-
- private:
-  // bits of the last word that are pages
-  uint64_t tail_mask() const { return n_ % 64 ? (1ull << (n_ % 64)) - 1 : ~0ull; }
-
-  int64_t n_ = 0, count_ = 0, hint_ = 0;
-  std::vector<uint64_t> words_;
-};
-
-struct SeqState {
-  bool used = false;
-  int64_t len = 0;
-  int64_t next_pos = 0;
-  std::vector<int32_t> pages;
-  // pages is out of date: the device page-table row (written by an eviction
-  // the device planned) holds the sequence's table; copied back on demand
-  bool stale = false;
-};
-
-// The region of the staging ring one call fills on the host and sends to the
-// device with one copy (pinned host memory and device memory at the same
-// offsets).
-struct Staging {
-  char* host = nullptr;
-  char* dev = nullptr;
-  size_t start = 0;
-  size_t cap = 0;
-  size_t used = 0;
-};
-
-// A region still in use by device work, and the event that marks its end.
-struct RingRegion {
-  size_t start, end;
-  hipEvent_t done;
-};
+using ll::kMaxDispatchItems;
+using ll::ProfRec;
+using ll::RingRegion;
+using ll::SeqState;
+using ll::Staging;
 
 // The staging ring starts this large and doubles when one call needs more.
 constexpr size_t kRingBytes = size_t{16} << 20;
@@ -170,39 +69,11 @@ constexpr size_t kRingBytes = size_t{16} << 20;
 // run while earlier work still occupies the caller's stream.
 constexpr size_t kCopyStreamBytes = size_t{16} << 10;
 
-struct ProfRec {
-  hipEvent_t start, stop;
-  int64_t bytes;
-};
-
-// Current-device guard.
-class DeviceGuard {
- public:
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&old_) != hipSuccess) old_ = -1;
-    if (old_ != dev) ok_ = hipSetDevice(dev) == hipSuccess;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (old_ >= 0 && hipGetDevice(&cur) == hipSuccess && cur != old_) (void)hipSetDevice(old_);
-  }
-  bool ok() const { return ok_; }
-
- private:
-  int old_ = -1;
-  bool ok_ = true;
-};
-
-}  // namespace
-
-namespace {
-
 // A dispatch packet counts its work-items in 32 bits.  A row kernel whose
 // grid would pass that (every layer of a batch that moves more than 2^32
 // 16-byte chunks in all) is issued as several dispatches in order on one
 // stream, each over a range of whole page tasks and every layer; the
 // page-table rewrites ride in the last one.
-constexpr int64_t kMaxDispatchItems = int64_t{0xFFFFFFFF};
 
 // Page tasks per dispatch: `units_per_task` units of each task in each of
 // `planes` planes, `units_per_block` units per block of `block_threads`
@@ -220,76 +91,6 @@ ll::Stamp part_stamp(const ll::Stamp& t, bool first, bool last) {
 }
 
 }  // namespace
-
-struct ll_pool {
-  ll_pool_desc desc{};       // GQA pools: kv_lora_rank 0, rope_dim = rotary_dim
-  int page_shift = 0;
-  int64_t P = 1;
-  bool gqa = false;          // K and V planes with per-head RoPE bands
-  int32_t num_planes = 0;    // MLA: num_layers; GQA: 2 * num_layers (K then V)
-  int64_t row_bytes = 0;     // one row of one plane
-  int64_t band_bytes = 0;    // RoPE bytes of one row of a rotated plane
-  int32_t heads = 0, head_chunks = 0, rot_shift = 0;  // GQA row shape
-  std::vector<void*> layer_ptrs;  // the planes
-  void** d_layers = nullptr;
-  // chunks from one plane to the next when every plane's base is the first
-  // one's plus a multiple of one fixed stride (one caller allocation), else 0
-  int64_t plane_stride_chunks = 0;
-  std::vector<SeqState> seqs;
-  FreePages free;
-  // staging ring: one pinned + one device buffer; calls take consecutive
-  // regions and a region is reused once its call's event has fired
-  char* ring_host = nullptr;
-  char* ring_dev = nullptr;
-  size_t ring_cap = 0;
-  size_t ring_head = 0;
-  std::deque<RingRegion> ring_inflight;
-  std::vector<hipEvent_t> ring_events;  // idle events for new regions
-  Staging cur;                          // region of the call in progress
-  hipEvent_t upload_ev = nullptr;
-  // eviction scratch: device [counts | reuse | src_of_dst], pinned readback
-  float* d_rowtab = nullptr;    // per-row cos/sin tables of ll_rope_rows
-  size_t rowtab_cap = 0;        // floats
-  char* d_scratch = nullptr;
-  size_t scratch_cap = 0;
-  char* h_readback = nullptr;
-  size_t readback_cap = 0;
-  hipEvent_t readback_ev = nullptr;
-  hipStream_t copy_stream = nullptr;
-  hipEvent_t last_done = nullptr;  // end of the last call's device work
-  hipStream_t last_stream = nullptr;  // the stream that work ran on
-  // Calls that take no staging (splices planned on the device) record no
-  // event: last_done then lags, and last_work() records lazy_ev on
-  // last_stream when a later step needs the end of all work issued so far.
-  bool unevented = false;
-  hipEvent_t lazy_ev = nullptr;
-  int32_t splice_planner = LL_SPLICE_PLAN_AUTO;
-  bool page_reuse = true;       // false: every new page of a rewritten sequence is fresh
-  int64_t dispatch_items = kMaxDispatchItems;  // work-items one row-kernel dispatch may hold
-  char* d_direct = nullptr;     // tasks, tables and rotation tables of device-planned splices
-  size_t direct_cap = 0;
-  bool poisoned = false;
-  std::vector<double> theta;    // RoPE frequencies of the pool's band (float64)
-  ll_plan_stats last{};
-  int32_t prof_every = 0;       // time every n-th launch of each kernel (0: none)
-  int64_t prof_tick[3] = {0, 0, 0};
-  std::vector<ProfRec> prof[3];  // row-moving kernel, keep scan, per-row rotation
-  std::vector<hipEvent_t> spare_events;
-  std::vector<int32_t> page_slot;  // per physical page: scratch marks of ll_seq_set_pages
-  std::vector<int32_t> table_rows;     // host copy of device page-table rows (stale tables)
-  // An eviction at page size 1 (no page is ever fresh): the call returns at
-  // once and the host learns its result -- new lengths and the bitmap of
-  // freed pages -- from a small readback that the next call on the pool
-  // applies (settles) first.
-  struct PendingEvict {
-    bool active = false;
-    hipEvent_t done = nullptr;   // the readback has landed
-    std::vector<int32_t> seq_ids;
-    size_t off_info = 0, off_freed = 0;  // in h_readback (counts at 0)
-    int64_t n_words = 0;         // words of the freed bitmap
-    int64_t prof_index = -1;     // prof[0] entry whose bytes are known only then
-  } pending;
-};
 
 namespace {
 
@@ -346,6 +147,7 @@ ll_status apply_evict(ll_pool* p, const int32_t* seq_ids, size_t n_seqs, const i
     SeqState& s = p->seqs[seq_ids[i]];
     s.len = counts[i];
     s.stale = true;
+    s.gen = ++p->epoch;
     stats.table_entries += ceil_div(counts[i], P);
   }
   stats.alg_bytes = p->num_planes * 2 * p->row_bytes * stats.rows_moved;
@@ -907,6 +709,7 @@ ll_status evict_device_plan(ll_pool* p, const int32_t* seq_ids, int32_t n, const
     ll_pool::PendingEvict& pe = p->pending;
     pe.active = true;
     pe.seq_ids.assign(seq_ids, seq_ids + n);
+    for (int32_t i = 0; i < n; ++i) p->seqs[seq_ids[i]].gen = ++p->epoch;
     pe.off_info = off_info;
     pe.off_freed = off_freed;
     pe.n_words = n_words;
@@ -1030,6 +833,20 @@ ll_status validate_directives(const ll_pool* p, const ll_directive* dirs, int32_
 }
 
 }  // namespace
+
+namespace ll {
+
+ll_status pool_check(const ll_pool* p) { return check_pool(p); }
+ll_status pool_enter(ll_pool* p) { return enter(p); }
+ll_status pool_host_exception(ll_pool* p) noexcept { return host_exception(p); }
+ll_status pool_device_fail(ll_pool* p, hipError_t e, const char* what) { return device_fail(p, e, what); }
+ll_status pool_begin_call(ll_pool* p, hipStream_t st) { return begin_call(p, st); }
+ll_status pool_end_call(ll_pool* p, Staging* s, hipStream_t st) { return end_call(p, s, st); }
+ll_status pool_stage(ll_pool* p, size_t bytes, Staging** out) { return stage_acquire(p, bytes, out); }
+ll_status pool_fresh_tables(ll_pool* p, const int32_t* seqs, size_t n) { return fresh_tables(p, seqs, n); }
+ll_status pool_wait_idle(ll_pool* p) { return wait_idle(p); }
+
+}  // namespace ll
 
 // =================================================================== C ABI ==
 
@@ -1214,6 +1031,7 @@ ll_status ll_pool_create_gqa(const ll_gqa_pool_desc* desc, ll_pool** out) try {
 void ll_pool_destroy(ll_pool* p) try {
   if (!p) return;
   DeviceGuard g(p->desc.device);
+  for (ll_pool** o : p->step_owners) *o = nullptr;  // its steps refuse every later call
   {
     hipError_t e;
     hipEvent_t ev = last_work(p, &e);
@@ -1305,6 +1123,7 @@ ll_status ll_seq_alloc(ll_pool* p, int64_t n_tokens, int32_t* seq_id_out, void* 
   s.used = true;
   s.len = n_tokens;
   s.next_pos = n_tokens;
+  s.gen = ++p->epoch;
   s.pages = std::move(pages);
   *seq_id_out = seq;
   return LL_OK;
@@ -1365,6 +1184,7 @@ ll_status ll_seq_set_pages(ll_pool* p, int32_t seq, const int32_t* pages, int64_
   s.used = true;
   s.len = n_tokens;
   s.next_pos = n_tokens;
+  s.gen = ++p->epoch;
   s.pages = std::move(t);
   return LL_OK;
 } catch (...) {
@@ -1379,6 +1199,7 @@ ll_status ll_seq_free(ll_pool* p, int32_t seq) try {
   SeqState& s = p->seqs[seq];
   for (int32_t pg : s.pages) p->free.give(pg);
   s = SeqState();
+  s.gen = ++p->epoch;
   return LL_OK;
 } catch (...) {
   return host_exception(p);
@@ -1806,6 +1627,7 @@ static ll_status splice_impl(ll_pool* p, const ll_directive* dirs, int32_t n, vo
     s.pages = std::move(new_tables[i]);
     s.len = plans[i].n_new;
     s.next_pos = plans[i].next_pos;
+    s.gen = ++p->epoch;
   }
   p->last = stats;
   return LL_OK;
@@ -1900,6 +1722,7 @@ ll_status ll_ptable_reindex(ll_pool* p, int32_t seq, const int32_t* keep_pages, 
   stats.table_entries = n_keep;
   s.pages = std::move(nt);
   s.len = new_len;
+  s.gen = ++p->epoch;
   p->last = stats;
   return LL_OK;
 } catch (...) {
