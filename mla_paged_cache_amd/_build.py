@@ -4,8 +4,9 @@ The library holds the HIP kernels (csrc/kernels.hip for MLA pools,
 csrc/kernels_gqa.hip for GQA / MHA pools, csrc/kernels_kvs.hip for the
 KV-streams trainer mask, csrc/kernels_rows.hip for the per-row-angle
 rotation, csrc/kernels_alloc.hip for the eviction's device-side page
-allocator, helpers in csrc/device_common.h) and the C++ host
-side and C ABI (csrc/pool.cpp, csrc/kvs_mask.cpp).  Flags:
+allocator, csrc/kernels_step.hip and csrc/kernels_attend.hip for the serving
+step, helpers in csrc/device_common.h) and the C++ host side and C ABI
+(csrc/pool.cpp, csrc/step.cpp, csrc/kvs_mask.cpp).  Flags:
   * --offload-arch=gfx950 only (MI355X);
   * -ffp-contract=off so the delta-rotation keeps its separately rounded
     float32 products (the kernels also say so with a pragma);
@@ -27,7 +28,8 @@ LIB_NAME = "libleyline.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = [os.path.join(CSRC, n) for n in ("kernels.hip", "kernels_gqa.hip", "kernels_kvs.hip", "kernels_rows.hip",
-                                           "kernels_alloc.hip", "pool.cpp", "kvs_mask.cpp")]
+                                           "kernels_alloc.hip", "kernels_step.hip", "kernels_attend.hip", "pool.cpp",
+                                           "step.cpp", "kvs_mask.cpp")]
 
 FLAGS = [
     "--offload-arch=gfx950",

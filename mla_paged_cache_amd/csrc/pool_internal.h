@@ -241,6 +241,7 @@ ll_status pool_device_fail(ll_pool* p, hipError_t e, const char* what);
 ll_status pool_begin_call(ll_pool* p, hipStream_t st);
 ll_status pool_end_call(ll_pool* p, Staging* s, hipStream_t st);
 ll_status pool_stage(ll_pool* p, size_t bytes, Staging** out);
+ll_status pool_upload(ll_pool* p, Staging* s, hipStream_t st);
 ll_status pool_fresh_tables(ll_pool* p, const int32_t* seqs, size_t n);
 ll_status pool_wait_idle(ll_pool* p);
 

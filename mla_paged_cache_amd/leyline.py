@@ -1,4 +1,5 @@
-"""Python binding of libleyline.so (include/leyline.h): argument marshalling only.
+"""Python binding of libleyline.so (include/leyline.h, include/leyline_step.h):
+argument marshalling only.
 
 Every step of the splice / evict path runs in the library's HIP kernels and
 C++ host planner; this module turns torch tensors into device pointers and
@@ -34,6 +35,10 @@ EXPORTS = (
     "ll_rope_rows", "ll_pool_set_splice_planner", "ll_pool_set_page_reuse", "ll_last_plan_bytes", "ll_seq_lengths",
     "leyline_splice_noalloc", "ll_pool_set_dispatch_limit",
 )
+
+
+# Every symbol include/leyline_step.h declares.
+STEP_EXPORTS = ("ll_step_create", "ll_step_destroy", "ll_step_begin", "ll_step_append", "ll_step_attend")
 
 
 class LeylineError(RuntimeError):
@@ -114,6 +119,57 @@ class _PlanStats(ctypes.Structure):
     ]
 
 
+class _StepDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_heads", ctypes.c_int32),
+        ("max_seqs", ctypes.c_int32),
+        ("max_tokens", ctypes.c_int32),
+    ]
+
+
+class _AppendDesc(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("layer", ctypes.c_int32),
+        ("norm_type", ctypes.c_int32),
+        ("a", ctypes.c_void_p),
+        ("a_token_stride", ctypes.c_int64),
+        ("a_head_stride", ctypes.c_int64),
+        ("b", ctypes.c_void_p),
+        ("b_token_stride", ctypes.c_int64),
+        ("b_head_stride", ctypes.c_int64),
+        ("norm", ctypes.c_void_p),
+        ("q", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p),
+        ("q_out_token_stride", ctypes.c_int64),
+        ("q_out_head_stride", ctypes.c_int64),
+        ("q_norm", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class _AttendDesc(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("layer", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("q", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("q_pe", ctypes.c_void_p),
+        ("q_pe_token_stride", ctypes.c_int64),
+        ("q_pe_head_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("out_token_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("lse", ctypes.c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with mla_paged_cache_amd._build.build() "
@@ -148,6 +204,11 @@ def _load():
         "kvs_death_times": (i32, [vp, P(_KvsRolloutLog), i32, i64, vp, vp, vp, vp]),
         "kvs_block_mask": (i32, [vp, vp, i32, i64, i32, i32, vp, vp, vp, vp, vp]),
         "kvs_dense_mask": (i32, [vp, vp, i32, i64, vp, vp]),
+        "ll_step_create": (i32, [vp, P(_StepDesc), P(vp)]),
+        "ll_step_destroy": (None, [vp]),
+        "ll_step_begin": (i32, [vp, vp, vp, i32, i32, vp]),
+        "ll_step_append": (i32, [vp, P(_AppendDesc), vp]),
+        "ll_step_attend": (i32, [vp, P(_AttendDesc), vp]),
         "ll_last_error": (ctypes.c_char_p, []),
         "ll_status_str": (ctypes.c_char_p, [i32]),
     }
@@ -404,6 +465,12 @@ class Pool:
                                  ptr, stride, _stream_handle(stream, self._dev)))
         return out
 
+    def step(self, heads: int, max_seqs: int | None = None, max_tokens: int = 8192) -> "Step":
+        """A serving step of this pool for `heads` query heads: up to max_seqs
+        sequences (None: all the pool can hold) with up to max_tokens new
+        tokens together."""
+        return Step(self, heads, self.max_seqs if max_seqs is None else max_seqs, max_tokens)
+
     def ptable_reindex(self, seq: int, keep_pages, stream=None) -> None:
         arr, ptr = _i32_array(keep_pages)
         _check(_lib.ll_ptable_reindex(self._h, int(seq), ptr, len(arr), _stream_handle(stream, self._dev)))
@@ -625,3 +692,159 @@ class KvsMask:
         _require(out, "out", torch.int32, (n, n_pad, n_pad // 32), self._tdev)
         _check(_lib.kvs_dense_mask(self._h, death.data_ptr(), n, n_pad, out.data_ptr(), _stream_handle(stream, self.device)))
         return out
+
+
+class Step:
+    """The serving step of a pool (include/leyline_step.h): begin() names the
+    sequences and how many tokens each brings, then append() and attend() run
+    once per layer.  The tokens of a step are the first sequence's in order, then
+    the second's, ...; tensors hold one row per token, or more (the first ones are
+    used; under graph capture they hold max_tokens rows).
+
+    Inputs may be views (e.g. of one projection's output): the last axis is dense,
+    the other strides are multiples of 8 values and the data is 16-byte aligned."""
+
+    def __init__(self, pool: Pool, heads: int, max_seqs: int, max_tokens: int):
+        d = _StepDesc(int(heads), int(max_seqs), int(max_tokens))
+        h = ctypes.c_void_p()
+        _check(_lib.ll_step_create(pool._h, ctypes.byref(d), ctypes.byref(h)))
+        self._h = h
+        self._pool = pool
+        self.gqa, self.heads, self.max_seqs, self.max_tokens = pool.gqa, int(heads), int(max_seqs), int(max_tokens)
+        self.device, self._dev = pool.device, pool._dev
+        self.tokens = 0
+        # widths of a query as attend takes it, of its rotated part, of a result
+        self._dq, self._dr, self._dv = (pool.head_dim,) * 3 if pool.gqa else (ROW, ROPE_DIM, KV_LORA_RANK)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            _lib.ll_step_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def begin(self, seqs, counts, grow: bool = True, stream=None) -> int:
+        """counts[i] tokens of sequence seqs[i].  grow=True: new ones, every
+        sequence grows by them; grow=False: the last ones it already holds.
+        Returns the number of tokens of the step."""
+        s_arr, s_ptr = _i32_array(seqs)
+        c_arr, c_ptr = _i32_array(counts)
+        if len(s_arr) != len(c_arr):
+            raise ValueError(f"{len(s_arr)} sequences but {len(c_arr)} token counts")
+        _check(_lib.ll_step_begin(self._h, s_ptr, c_ptr, len(s_arr), 1 if grow else 0,
+                                  _stream_handle(stream, self._dev)))
+        self.tokens = int(c_arr.sum())
+        return self.tokens
+
+    def _rows(self, t, name: str, *tail, dtype=None):
+        """Token count of a [tokens][*tail] tensor on the pool's device."""
+        import torch
+        if not isinstance(t, torch.Tensor) or t.dtype != (dtype or torch.bfloat16) or t.device != self.device \
+                or t.dim() != 1 + len(tail) or tuple(t.shape[1:]) != tail or t.stride(-1) != 1:
+            raise ValueError(f"{name}: need a {dtype or torch.bfloat16} tensor [tokens]{list(tail)} on {self.device} "
+                             f"with a dense last axis")
+        return t.shape[0]
+
+    def _weight(self, w, name: str, n: int):
+        import torch
+        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.bfloat16, torch.float32) or w.device != self.device \
+                or tuple(w.shape) != (n,) or w.stride(0) != 1:
+            raise ValueError(f"{name}: need a dense bf16 or float32 tensor [{n}] on {self.device}")
+        return w.data_ptr()
+
+    def append(self, layer: int, a=None, b=None, norm=None, q=None, q_out=None, q_norm=None, eps: float = 1e-6,
+               stream=None):
+        """Write one layer's new rows and prepare its queries (ll_step_append).
+
+        MLA: a = c_kv [T][512], b = k_pe [T][64], q = the rotated part of the
+        queries [T][heads][64]; GQA: a = K, b = V [T][kv_heads][head_dim], q =
+        [T][heads][head_dim].  norm / q_norm: RMS-norm weights (bf16 or float32) of
+        c_kv or the K heads / the query heads (GQA).  Returns q_out (new when not
+        given; q itself turns the queries in place), or None without q."""
+        import torch
+        d = _AppendDesc(layer=int(layer), eps=eps)
+        rows = []
+        if (a is None) != (b is None):
+            raise ValueError("a and b go together")
+        if a is not None:
+            if self.gqa:
+                shape = (self._pool.heads, self._pool.head_dim)
+                rows += [self._rows(a, "a", *shape), self._rows(b, "b", *shape)]
+                d.a_token_stride, d.a_head_stride, _ = a.stride()
+                d.b_token_stride, d.b_head_stride, _ = b.stride()
+            else:
+                rows += [self._rows(a, "a", KV_LORA_RANK), self._rows(b, "b", ROPE_DIM)]
+                d.a_token_stride, d.b_token_stride = a.stride(0), b.stride(0)
+            d.a, d.b = a.data_ptr(), b.data_ptr()
+        if norm is not None:
+            d.norm = self._weight(norm, "norm", self._dv)
+            d.norm_type = 1 if norm.dtype == torch.float32 else 0
+        if q is not None:
+            rows.append(self._rows(q, "q", self.heads, self._dr))
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            rows.append(self._rows(q_out, "q_out", self.heads, self._dr))
+            d.q, d.q_out = q.data_ptr(), q_out.data_ptr()
+            d.q_token_stride, d.q_head_stride, _ = q.stride()
+            d.q_out_token_stride, d.q_out_head_stride, _ = q_out.stride()
+            if q_norm is not None:
+                d.q_norm = self._weight(q_norm, "q_norm", self._dr)
+                if norm is not None and q_norm.dtype != norm.dtype:
+                    raise ValueError("norm and q_norm must have one dtype")
+                d.norm_type = 1 if q_norm.dtype == torch.float32 else 0
+        elif q_out is not None or q_norm is not None:
+            raise ValueError("q_out and q_norm need q")
+        d.tokens = min(rows) if rows else self.max_tokens
+        _check(_lib.ll_step_append(self._h, ctypes.byref(d), _stream_handle(stream, self._dev)))
+        return q_out
+
+    def attend(self, layer: int, q, q_pe=None, scale: float | None = None, causal: bool = True, window: int = 0,
+               out=None, lse=None, stream=None):
+        """Attention of the step's tokens over one layer (ll_step_attend).
+
+        MLA: q [T][heads][576] (latent part, then the rotated part), or q
+        [T][heads][512] with q_pe [T][heads][64]; the result is [T][heads][512] in
+        the latent space, and scale must be given.  GQA: q and the result are
+        [T][heads][head_dim], scale defaults to head_dim ** -0.5.  window > 0: a
+        token sees the last `window` rows up to its own.  lse=True (or a dense
+        float32 tensor [T][heads]) also returns the log sum exp: (out, lse)."""
+        import torch
+        d = _AttendDesc(layer=int(layer), causal=1 if causal else 0, window=int(window))
+        if scale is None:
+            if not self.gqa:
+                raise ValueError("scale must be given: the latent width does not say the model's head width")
+            scale = self._dq ** -0.5
+        d.scale = scale
+        if self.gqa:
+            if q_pe is not None:
+                raise ValueError("q_pe is for MLA pools only")
+            rows = self._rows(q, "q", self.heads, self._dq)
+        elif q_pe is None:
+            rows = self._rows(q, "q", self.heads, ROW)
+            d.q_pe = q.data_ptr() + 2 * KV_LORA_RANK
+            d.q_pe_token_stride, d.q_pe_head_stride, _ = q.stride()
+        else:
+            rows = min(self._rows(q, "q", self.heads, KV_LORA_RANK), self._rows(q_pe, "q_pe", self.heads, ROPE_DIM))
+            d.q_pe = q_pe.data_ptr()
+            d.q_pe_token_stride, d.q_pe_head_stride, _ = q_pe.stride()
+        d.q = q.data_ptr()
+        d.q_token_stride, d.q_head_stride, _ = q.stride()
+        if out is None:
+            out = torch.empty((q.shape[0], self.heads, self._dv), dtype=q.dtype, device=q.device)
+        rows = min(rows, self._rows(out, "out", self.heads, self._dv))
+        d.out = out.data_ptr()
+        d.out_token_stride, d.out_head_stride, _ = out.stride()
+        if lse is True:
+            lse = torch.empty((q.shape[0], self.heads), dtype=torch.float32, device=q.device)
+        if lse is not None and lse is not False:
+            rows = min(rows, self._rows(lse, "lse", self.heads, dtype=torch.float32))
+            if not lse.is_contiguous():
+                raise ValueError("lse must be contiguous")
+            d.lse = lse.data_ptr()
+        d.tokens = rows
+        _check(_lib.ll_step_attend(self._h, ctypes.byref(d), _stream_handle(stream, self._dev)))
+        return out if d.lse is None else (out, lse)
