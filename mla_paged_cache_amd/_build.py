@@ -39,6 +39,10 @@ FLAGS = [
     "-shared",
     "-ffp-contract=off",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    # matrix accumulators in ordinary registers: the attention scales and
+    # stores them, and moving each to and from the accumulation file costs more
+    # than the products (the compiler's own choice otherwise)
+    "-mllvm", "-amdgpu-mfma-vgpr-form=1",
     "-Wall",
     "-Winfinite-recursion",
     "-Wl,--no-undefined",

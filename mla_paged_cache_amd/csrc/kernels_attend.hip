@@ -80,10 +80,10 @@ __device__ __forceinline__ float dot8(const Vals& x, const Vals& y) {
 // values of the head (MLA: of the latent part, and of k_pe in lanes 0..7).
 // Reads exactly the rows that the query sees.
 template <bool GQA>
-__device__ void attend_rows(const AttendLaunch& a, const AttendItem& it, int kvh, int wave, int waves, int lane) {
+__device__ void attend_rows(const AttendLaunch& a, const AttendItem& it, const Seen& share, int kvh, int wave,
+                            int waves, int lane) {
   const int dv = GQA ? a.dim : kKvLoraRank;
   const bool live = lane * 8 < dv;
-  const Seen share = item_share(a, it, 64);
   const int shares = it.splits >> 16;
   for (int rr = wave; rr < a.tile && it.row0 + rr < it.q_rows; rr += waves) {
     const int r = it.row0 + rr;
@@ -139,12 +139,496 @@ __device__ void attend_rows(const AttendLaunch& a, const AttendItem& it, int kvh
   }
 }
 
-template <bool GQA>
-__global__ __launch_bounds__(kAttendThreads) void attend_rows_kernel(AttendLaunch a) {
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char* lds_ptr;
+
+// A tile of cached rows in LDS: regions of ROWCH 16-byte chunks per row, chunk c
+// of row r at place c ^ swizzle(r).  Both ways of reading it then touch every bank
+// evenly: 16 rows at one chunk (the scores' operand) fall on 16 different places
+// of a 256-byte line, and 4 consecutive rows at 4 consecutive chunks (the
+// transposing reads of the values) on 16 more.
+template <int ROWCH>
+__device__ __forceinline__ int swizzle(int r) {
+  if constexpr (ROWCH >= 16) {
+    return ((r & 3) << 2) | ((r >> 2) & 3);
+  } else {   // two rows per 256-byte line
+    const int h = (r >> 1) & 7;
+    return ((h & 1) << 2) | (h >> 1);
+  }
+}
+
+__device__ __forceinline__ bf16x8 lds_chunk(lds_ptr p) {
+  return *reinterpret_cast<__attribute__((address_space(3))) bf16x8*>(p);
+}
+// 16 lanes read 4 rows x 16 columns (8 bytes each) and get them transposed: lane
+// i the 4 rows of column i.
+__device__ __forceinline__ s16x4 lds_columns(lds_ptr p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4*>(p));
+}
+
+__device__ __forceinline__ bool not_finite(chunk_t c) {
+  bool bad = false;
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    bad |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+  return bad;
+}
+
+// How a workgroup does one item: QW waves side by side over the query rows (QN
+// tiles of 16 each), KW over the cached rows of a tile of BN.
+template <bool MLA_, int DP, int QN_, int QW_, int KW_, int BN_>
+struct Shape {
+  static constexpr bool MLA = MLA_;
+  static constexpr int QN = QN_, QW = QW_, KW = KW_, BN = BN_;
+  static constexpr int WAVES = QW * KW, THREADS = 64 * WAVES;
+  static constexpr int DK = MLA ? kRowElems : DP, DV = MLA ? kKvLoraRank : DP;
+  static constexpr int ROWCH = DV / 8;                       // chunks of a row of the main region
+  static constexpr int MAIN = BN * DV * 2;                   // MLA: latent part; GQA: K
+  static constexpr int SIDE = MLA ? BN * kRopeDim * 2 : MAIN;  // MLA: k_pe; GQA: V
+  static constexpr int SIDE_ROWCH = MLA ? kRopeDim / 8 : ROWCH;
+  static constexpr int STAGE = MAIN + SIDE;
+  static constexpr int VALUES = MLA ? 0 : MAIN;              // where the values lie in a stage
+  static constexpr int KVT = BN / KW;                        // cached rows of a tile per wave
+  static constexpr int TILE = 16 * QN * QW;                  // query rows
+  static_assert(KVT % 16 == 0 && BN <= THREADS, "whole matrix tiles, a thread per row");
+};
+
+// 64 x 16 bytes from memory straight into LDS at `dst` + 16 * lane (base: uniform;
+// off: the lane's byte offset).  As assembly, because the compiler otherwise waits
+// for every such load before each transposing LDS read; it has no result
+// register, and the kernel waits for it itself (vmcnt(0) before the barrier).
+__device__ __forceinline__ void load_lds(lds_ptr dst, const void* base, uint32_t off) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds(lds_ptr dst, const void* src) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
+}
+
+// A tile from the cache to LDS: an instruction fills 64 consecutive places, so
+// each lane fetches the chunk that the swizzle puts at its place.  `rows` (LDS)
+// holds the tile's physical rows.
+template <typename S>
+__device__ __forceinline__ void load_mla_tile(const uint16_t* plane, const int* rows, lds_ptr dst, int wave, int lane) {
+#pragma unroll
+  for (int i = 0; i < S::BN / S::WAVES; ++i) {   // a row's latent part each
+    const int r = i * S::WAVES + wave;
+    const int64_t row = __builtin_amdgcn_readfirstlane(rows[r]);
+    load_lds(dst + r * 1024, plane + row * kRowElems, static_cast<uint32_t>(lane ^ swizzle<64>(r)) * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < (S::BN / 8 + S::WAVES - 1) / S::WAVES; ++i) {   // 8 rows' k_pe each
+    const int b = i * S::WAVES + wave;
+    if (b >= S::BN / 8) break;
+    const int r = b * 8 + (lane >> 3);
+    load_lds(dst + S::MAIN + b * 1024, plane + int64_t{rows[r]} * kRowElems + kKvLoraRank + ((lane & 7) ^ swizzle<8>(r)) * 8);
+  }
+}
+// K and V of one KV head; chunks past `live` are left alone (they were zeroed
+// once).  `col` is the head's first value in a row.
+template <typename S, bool PART>
+__device__ __forceinline__ void load_gqa_tile(const uint16_t* k, const uint16_t* v, int64_t row_elems, int live,
+                                              const int* rows, lds_ptr dst, int wave, int lane) {
+  constexpr int N = S::BN * S::ROWCH / 64;   // instructions per region
+  static_assert(N % S::WAVES == 0, "the same number for every wave");
+#pragma unroll
+  for (int i = 0; i < N / S::WAVES; ++i) {
+    const int b = i * S::WAVES + wave;
+    const int place = b * 64 + lane;
+    const int r = place / S::ROWCH;
+    const int c = (place % S::ROWCH) ^ swizzle<S::ROWCH>(r);
+    const int64_t off = rows[r] * row_elems + c * 8;
+    if (!PART || c < live) {
+      load_lds(dst + b * 1024, k + off);
+      load_lds(dst + S::MAIN + b * 1024, v + off);
+    }
+  }
+}
+
+// The flash kernel: scores and weighted sums on the matrix units.
+//
+// Scores are computed transposed (S^T = K Q^T: cached rows along the matrix
+// instruction's rows, queries along its columns), so that a lane holds 4
+// consecutive cached rows of one query: the softmax runs along a lane's own
+// registers, and the weights, rounded to bf16, are already laid out as the operand
+// of O^T = V^T P^T.  V^T comes from the transposing LDS reads.  Nothing but the
+// cached rows goes through LDS.
+//
+// The running maximum is only a reference: it moves (and the sums are scaled)
+// when a score exceeds it by more than 2^8, so weights stay below 2^8 and most
+// tiles scale nothing.  Sums are float32; a weight is rounded to bf16 (relative
+// 2^-9 on average) because the matrix units multiply bf16 by bf16.
+//
+// In a tile of which some query sees only a part, unseen weights are 0; since 0
+// times a value that is not finite is not 0, such a tile is searched for those,
+// and the item falls back to reading exactly the rows each query sees.
+template <typename S>
+__global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::WAVES / 4))) void attend_kernel(AttendLaunch a) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  __shared__ int s_rows[2][S::BN];
+  constexpr int QN = S::QN, KT = S::KVT / 16, DT = S::DV / 16, KK = S::DK / 32;
   const int kvh = blockIdx.x % a.kv_heads;
-  const int i = blockIdx.x / a.kv_heads;
-  if (i >= a.counts->items) return;
-  attend_rows<GQA>(a, a.items[i], kvh, threadIdx.x >> 6, 4, threadIdx.x & 63);
+  const int item = blockIdx.x / a.kv_heads;
+  if (item >= a.counts->items) return;
+  const AttendItem it = a.items[item];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int qw = wave % S::QW, kw = wave / S::QW;
+  const int li = lane & 15, g = lane >> 4;
+  const Seen share = item_share(a, it, S::BN);
+  const lds_ptr lds = (lds_ptr)smem;
+  const int live = S::MLA ? S::ROWCH : a.dim / 8;   // chunks a cached head has
+
+  // queries: this lane's 8 values of each 32 of the row
+  int t_of[QN], h_of[QN];
+  Seen seen[QN];
+  bf16x8 q[QN][KK];
+#pragma unroll
+  for (int n = 0; n < QN; ++n) {
+    const int r = it.row0 + (qw * QN + n) * 16 + li;
+    const bool ok = r < it.q_rows;
+    const int tt = ok ? r / a.group : 0;
+    t_of[n] = it.tok0 + tt;
+    h_of[n] = kvh * a.group + (ok ? r - tt * a.group : 0);
+    seen[n] = rows_seen(a, it, r);
+    const uint16_t* p = a.q + t_of[n] * a.q_ts + h_of[n] * a.q_hs;
+    const uint16_t* pe = S::MLA ? a.q_pe + t_of[n] * a.qp_ts + h_of[n] * a.qp_hs : nullptr;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      const int c = k * 4 + g;
+      const bool in = ok && (S::MLA || c < live);
+      // a place without a value reads the row's first one, and counts as 0
+      chunk_t v = *reinterpret_cast<const chunk_t*>(S::MLA && k >= 16 ? pe + (c - 64) * 8 : p + (in ? c * 8 : 0));
+      if (!in) v = chunk_t{0u, 0u, 0u, 0u};
+      q[n][k] = __builtin_bit_cast(bf16x8, v);
+    }
+  }
+
+  f32x4 o[DT][QN];
+  float m[QN], l[QN];
+#pragma unroll
+  for (int n = 0; n < QN; ++n) {
+    m[n] = -__builtin_inff();
+    l[n] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int tiles = (share.hi - share.lo + S::BN - 1) / S::BN;
+  // every query of the item sees all of [full_lo, full_hi)
+  const int last = min(it.row0 + S::TILE, it.q_rows) - 1;
+  const int full_lo = rows_seen(a, it, last).lo;
+  const int full_hi = min(rows_seen(a, it, it.row0).hi, share.hi);
+
+  auto phys = [&](int tile) {   // rows past the sequence repeat its last one
+    return static_cast<int>(physical_row(a, it.seq, min(share.lo + tile * S::BN + tid, it.kv_len - 1)));
+  };
+  auto load = [&](int tile) {
+    const int* rows = s_rows[tile & 1];
+    const lds_ptr dst = lds + (tile & 1) * S::STAGE;
+    if constexpr (S::MLA) {
+      load_mla_tile<S>(a.k_plane, rows, dst, wave, lane);
+    } else {
+      const int64_t row_elems = int64_t{a.kv_heads} * a.dim, col = int64_t{kvh} * a.dim;
+      if (live == S::ROWCH)
+        load_gqa_tile<S, false>(a.k_plane + col, a.v_plane + col, row_elems, live, rows, dst, wave, lane);
+      else
+        load_gqa_tile<S, true>(a.k_plane + col, a.v_plane + col, row_elems, live, rows, dst, wave, lane);
+    }
+  };
+
+  if (!S::MLA && live < S::ROWCH) {
+    for (int i = tid; i < 2 * S::STAGE / 16; i += S::THREADS) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
+  }
+  if (tiles > 0 && tid < S::BN) {
+    s_rows[0][tid] = phys(0);
+    if (tiles > 1) s_rows[1][tid] = phys(1);
+  }
+  __syncthreads();
+  if (tiles > 0) load(0);
+
+  // this lane's byte offsets within a stage
+  int k_off[4], p_off[2], v_off[8];
+  {
+    const int r = kw * S::KVT + li;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) k_off[x] = (r * S::ROWCH + ((x * 4 + g) ^ swizzle<S::ROWCH>(r))) * 16;
+    if constexpr (S::ROWCH < 16) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) k_off[x] = (r * S::ROWCH + ((((x * 4 + g) & 7)) ^ swizzle<S::ROWCH>(r))) * 16;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) p_off[x] = S::MAIN + (r * S::SIDE_ROWCH + ((x * 4 + g) ^ swizzle<S::SIDE_ROWCH>(r))) * 16;
+    const int vr = kw * S::KVT + 4 * g + (li >> 2);
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      v_off[x] = S::VALUES + (vr * S::ROWCH + (((x * 2 + ((li >> 1) & 1)) & (S::ROWCH - 1)) ^ swizzle<S::ROWCH>(vr))) * 16 + (li & 1) * 8;
+  }
+  const float c2 = a.scale * kLog2e;
+
+  bool rows_only = false;
+  for (int tile = 0; tile < tiles; ++tile) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's part of the tile has landed
+    __syncthreads();                      // everyone's has, and the other stage is free
+    if (tile + 1 < tiles) load(tile + 1);
+    int next_row = 0;
+    if (tile + 2 < tiles && tid < S::BN) next_row = phys(tile + 2);
+
+    const lds_ptr st = lds + (tile & 1) * S::STAGE;
+    const int j0 = share.lo + tile * S::BN;
+    const bool whole = j0 >= full_lo && j0 + S::BN <= full_hi;
+    if (!whole) {
+      bool bad = false;
+      for (int i = tid; i < S::BN * S::ROWCH; i += S::THREADS)
+        bad |= not_finite(reinterpret_cast<const chunk_t*>(smem + (tile & 1) * S::STAGE + S::VALUES)[i]);
+      rows_only = __syncthreads_or(bad);
+      if (rows_only) break;
+    }
+
+    f32x4 s[KT][QN];
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int n = 0; n < QN; ++n) s[k][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // the operand of step kk is read two steps ahead; the fences keep the
+    // compiler from reading everything at once into registers it lacks
+    auto score_chunk = [&](int kk, int k) -> bf16x8 {
+      if (S::MLA && kk >= 16) return lds_chunk(st + p_off[kk & 1] + k * 16 * S::SIDE_ROWCH * 16);
+      if (S::ROWCH < 16) return lds_chunk(st + k_off[kk & 1] + k * 16 * S::ROWCH * 16);
+      return lds_chunk(st + k_off[kk & 3] + (kk >> 2) * 256 + k * 16 * S::ROWCH * 16);
+    };
+    bf16x8 x[3][KT];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int k = 0; k < KT; ++k) x[kk][k] = score_chunk(kk, k);
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      if (kk + 2 < KK)
+#pragma unroll
+        for (int k = 0; k < KT; ++k) x[(kk + 2) % 3][k] = score_chunk(kk + 2, k);
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int n = 0; n < QN; ++n)
+          s[k][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[kk % 3][k], q[n][kk], s[k][n], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // softmax weights, in base 2
+    float top[QN];
+    bool grew = false;
+#pragma unroll
+    for (int n = 0; n < QN; ++n) {
+      top[n] = -__builtin_inff();
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[k][n][e] * c2;
+          if (!whole) {
+            const int j = j0 + kw * S::KVT + k * 16 + g * 4 + e;
+            if (j < seen[n].lo || j >= seen[n].hi || j >= share.hi) x = -__builtin_inff();
+          }
+          s[k][n][e] = x;
+          top[n] = fmaxf(top[n], x);
+        }
+      grew |= top[n] > m[n] + 8.f;
+    }
+    if (__any(grew)) {
+#pragma unroll
+      for (int n = 0; n < QN; ++n) {
+        float x = fmaxf(top[n], m[n]);
+        x = fmaxf(x, __shfl_xor(x, 16));
+        x = fmaxf(x, __shfl_xor(x, 32));
+        const float keep = x == m[n] ? 1.f : exp2_(m[n] - x);
+        m[n] = x;
+        l[n] *= keep;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d][n] *= keep;
+      }
+    }
+    bf16x4 p[KT][QN];
+#pragma unroll
+    for (int n = 0; n < QN; ++n) {
+      const float ref = m[n] == -__builtin_inff() ? 0.f : m[n];   // nothing seen yet: every weight is 0
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        f32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = exp2_(s[k][n][e] - ref);
+          l[n] += w[e];
+        }
+        p[k][n] = __builtin_convertvector(w, bf16x4);
+      }
+    }
+
+    if constexpr (KT == 1) {
+      auto column = [&](int d) { return lds_columns(st + v_off[d & 7] + (d >> 3) * 256); };
+      s16x4 y[4];
+#pragma unroll
+      for (int d = 0; d < 3; ++d) y[d] = column(d);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        if (d + 3 < DT) y[(d + 3) & 3] = column(d + 3);
+#pragma unroll
+        for (int n = 0; n < QN; ++n)
+          o[d][n] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(y[d & 3], __builtin_bit_cast(s16x4, p[0][n]), o[d][n], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      // two 16-row tiles make one operand; step i: rows k = 2 (i / DT), columns d = i % DT
+      auto columns = [&](int i) -> bf16x8 {
+        const int d = i % DT;
+        const lds_ptr at = st + v_off[d & 7] + (d >> 3) * 256 + (i / DT) * 32 * S::ROWCH * 16;
+        const s16x4 x0 = lds_columns(at), x1 = lds_columns(at + 16 * S::ROWCH * 16);
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
+      };
+      constexpr int STEPS = KT / 2 * DT;
+      bf16x8 y[4];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) y[i] = columns(i);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        if (i + 3 < STEPS) y[(i + 3) & 3] = columns(i + 3);
+        const int k = i / DT * 2, d = i % DT;
+#pragma unroll
+        for (int n = 0; n < QN; ++n) {
+          const bf16x8 w = __builtin_shufflevector(p[k][n], p[k + 1][n], 0, 1, 2, 3, 4, 5, 6, 7);
+          o[d][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[i & 3], w, o[d][n], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (tile + 2 < tiles && tid < S::BN) s_rows[tile & 1][tid] = next_row;
+  }
+
+  if (rows_only) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // loads on their way into LDS
+    attend_rows<!S::MLA>(a, it, share, kvh, wave, S::WAVES, lane);
+    return;
+  }
+
+#pragma unroll
+  for (int n = 0; n < QN; ++n) {
+    l[n] += __shfl_xor(l[n], 16);
+    l[n] += __shfl_xor(l[n], 32);
+  }
+  const int shares = it.splits >> 16;
+  const int dv = S::MLA ? kKvLoraRank : a.dim;
+  if constexpr (S::KW > 1) {
+    // the waves' sums over their own cached rows, put together in LDS
+    __shared__ float s_m[S::WAVES][16 * QN], s_l[S::WAVES][16 * QN];
+    constexpr int OUT_ROWS = 16 * QN * S::QW;
+    static_assert(S::KW * OUT_ROWS * S::DV * 4 <= 2 * S::STAGE, "the sums fit where the tiles were");
+    __syncthreads();   // the tiles are no longer read
+    float* sums = reinterpret_cast<float*>(smem);
+    if (g == 0)
+#pragma unroll
+      for (int n = 0; n < QN; ++n) {
+        s_m[wave][n * 16 + li] = m[n];
+        s_l[wave][n * 16 + li] = l[n];
+      }
+#pragma unroll
+    for (int n = 0; n < QN; ++n)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        // 16-byte chunks rotated by the row, against bank conflicts
+        const int row = (qw * QN + n) * 16 + li, ch = ((d * 4 + g) + row) % (S::DV / 4);
+        *reinterpret_cast<f32x4*>(sums + (kw * OUT_ROWS + row) * S::DV + ch * 4) = o[d][n];
+      }
+    __syncthreads();
+    for (int i = tid; i < OUT_ROWS * (S::DV / 4); i += S::THREADS) {
+      const int row = i / (S::DV / 4), c = i % (S::DV / 4);
+      const int r = it.row0 + row;
+      if (r >= it.q_rows || c * 4 >= dv) continue;
+      const int rw = row / (16 * QN), rn = row % (16 * QN);
+      float top = -__builtin_inff(), total = 0.f;
+      f32x4 sum{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < S::KW; ++k) top = fmaxf(top, s_m[k * S::QW + rw][rn]);
+#pragma unroll
+      for (int k = 0; k < S::KW; ++k) {
+        const float lk = s_l[k * S::QW + rw][rn];
+        if (lk == 0.f) continue;
+        const float w = exp2_(s_m[k * S::QW + rw][rn] - top);
+        total = __builtin_fmaf(lk, w, total);
+        sum += *reinterpret_cast<const f32x4*>(sums + (k * OUT_ROWS + row) * S::DV + (c + row) % (S::DV / 4) * 4) * w;
+      }
+      if (shares > 1) {
+        const int64_t at = (static_cast<int64_t>(it.slot) * a.kv_heads + kvh) * a.tile + row;
+        *reinterpret_cast<f32x4*>(a.part_o + at * dv + c * 4) = sum;
+        if (c == 0) {
+          a.part_ml[at * 2] = top;
+          a.part_ml[at * 2 + 1] = total;
+        }
+      } else {
+        const int tt = r / a.group, h = kvh * a.group + r - tt * a.group;
+        const int64_t t = it.tok0 + tt;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        *reinterpret_cast<bf16x4*>(a.out + t * a.o_ts + h * a.o_hs + c * 4) = __builtin_convertvector(sum * inv, bf16x4);
+        if (a.lse && c == 0) a.lse[t * a.heads + h] = total == 0.f ? -__builtin_inff() : (top + __log2f(total)) * kLn2;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < QN; ++n) {
+      const int row = (qw * QN + n) * 16 + li;
+      if (it.row0 + row >= it.q_rows) continue;
+      const int64_t t = t_of[n];
+      if (shares > 1) {
+        const int64_t at = (static_cast<int64_t>(it.slot) * a.kv_heads + kvh) * a.tile + row;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          if (d * 16 + g * 4 < dv) *reinterpret_cast<f32x4*>(a.part_o + at * dv + d * 16 + g * 4) = o[d][n];
+        if (g == 0) {
+          a.part_ml[at * 2] = m[n];
+          a.part_ml[at * 2 + 1] = l[n];
+        }
+      } else {
+        const float inv = l[n] == 0.f ? 0.f : 1.f / l[n];
+        uint16_t* out = a.out + t * a.o_ts + h_of[n] * a.o_hs;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          if (d * 16 + g * 4 < dv)
+            *reinterpret_cast<bf16x4*>(out + d * 16 + g * 4) = __builtin_convertvector(o[d][n] * inv, bf16x4);
+        if (a.lse && g == 0) a.lse[t * a.heads + h_of[n]] = l[n] == 0.f ? -__builtin_inff() : (m[n] + __log2f(l[n])) * kLn2;
+      }
+    }
+  }
+}
+
+template <typename S>
+hipError_t launch_shape(const AttendLaunch& a, hipStream_t s) {
+  constexpr int lds = 2 * S::STAGE;
+  static bool set[64];   // per device: hipFuncSetAttribute is not cheap
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_kernel<S>), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  attend_kernel<S><<<dim3(static_cast<unsigned>(int64_t{a.n_items} * a.kv_heads)), dim3(S::THREADS), lds, s>>>(a);
+  return hipGetLastError();
+}
+
+// The query rows a workgroup takes follow from how many the sequences bring.
+template <bool MLA, int DP>
+hipError_t launch_tile(const AttendLaunch& a, hipStream_t s) {
+  switch (a.tile) {
+    case 16: return launch_shape<Shape<MLA, DP, 1, 1, 4, 64>>(a, s);
+    case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, 64>>(a, s);
+    case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, 64>>(a, s);
+    default: return launch_shape<Shape<MLA, DP, MLA ? 1 : 2, MLA ? 8 : 4, 1, MLA ? 32 : 64>>(a, s);
+  }
 }
 
 // The shares of a split tile put together: a wave per query row, each share
@@ -199,13 +683,14 @@ int attend_tile(bool gqa, int dim, int64_t rows) {
 }
 
 hipError_t launch_attend(const AttendLaunch& a, bool gqa, hipStream_t s) {
-  const dim3 g(static_cast<unsigned>(int64_t{a.n_items} * a.kv_heads)), b(kAttendThreads);
-  void (*k)(AttendLaunch) = gqa ? attend_rows_kernel<true> : attend_rows_kernel<false>;
-  k<<<g, b, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
+  hipError_t e;
+  if (!gqa) e = launch_tile<true, 0>(a, s);
+  else if (a.dim <= 64) e = launch_tile<false, 64>(a, s);
+  else if (a.dim <= 128) e = launch_tile<false, 128>(a, s);
+  else e = launch_tile<false, 256>(a, s);
   if (e != hipSuccess || a.n_shares == 0) return e;
-  k = gqa ? attend_join_kernel<true> : attend_join_kernel<false>;
-  k<<<dim3(static_cast<unsigned>(int64_t{a.n_shares} * a.kv_heads * (a.tile / 4))), b, 0, s>>>(a);
+  void (*k)(AttendLaunch) = gqa ? attend_join_kernel<true> : attend_join_kernel<false>;
+  k<<<dim3(static_cast<unsigned>(int64_t{a.n_shares} * a.kv_heads * (a.tile / 4))), dim3(kAttendThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
