@@ -181,7 +181,7 @@ __device__ __forceinline__ bool not_finite(chunk_t c) {
 
 // How a workgroup does one item: QW waves side by side over the query rows (QN
 // tiles of 16 each), KW over the cached rows of a tile of BN.
-template <bool MLA_, int DP, int QN_, int QW_, int KW_, int BN_>
+template <bool MLA_, int DP, int QN_, int QW_, int KW_, int BN_, int STAGES_>
 struct Shape {
   static constexpr bool MLA = MLA_;
   static constexpr int QN = QN_, QW = QW_, KW = KW_, BN = BN_;
@@ -193,9 +193,16 @@ struct Shape {
   static constexpr int SIDE_ROWCH = MLA ? kRopeDim / 8 : ROWCH;
   static constexpr int STAGE = MAIN + SIDE;
   static constexpr int VALUES = MLA ? 0 : MAIN;              // where the values lie in a stage
+  static constexpr int STAGES = STAGES_;                     // tiles in LDS
+  static constexpr int AHEAD = STAGES - 1;                   // a tile is asked for this many tiles ahead
+  static constexpr int PAGES = 2 * AHEAD + 1;                // tiles whose page numbers are in LDS
+  // a tile's loads per wave, at least
+  static constexpr int LOADS = MLA ? BN / WAVES + BN / 8 / WAVES : 2 * BN * ROWCH / 64 / WAVES;
+  static constexpr int LDS = STAGES * STAGE + WAVES * PAGES * BN * 4;
   static constexpr int KVT = BN / KW;                        // cached rows of a tile per wave
   static constexpr int TILE = 16 * QN * QW;                  // query rows
-  static_assert(KVT % 16 == 0 && BN <= THREADS, "whole matrix tiles, a thread per row");
+  static_assert(KVT % 16 == 0 && BN <= 64, "whole matrix tiles, a lane per row");
+  static_assert(LOADS * (AHEAD - 1) < 64, "the wait counter's range");
 };
 
 // 64 x 16 bytes from memory straight into LDS at `dst` + 16 * lane (base: uniform;
@@ -211,15 +218,31 @@ __device__ __forceinline__ void load_lds(lds_ptr dst, const void* src) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
 }
 
+__device__ __forceinline__ void load_lds4(lds_ptr dst, const void* src) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory");
+}
+
+// Where the rows of a tile lie: the page numbers of its rows, in LDS.
+struct TileRows {
+  const int* pages;
+  int j0, last;          // the tile's first row; the sequence's last one, which rows past it repeat
+  int shift, num_pages;
+  __device__ __forceinline__ int operator()(int r) const {
+    int page = pages[r];
+    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(num_pages)) page = 0;   // as in physical_row
+    return (page << shift) + (min(j0 + r, last) & ((1 << shift) - 1));
+  }
+};
+
 // A tile from the cache to LDS: an instruction fills 64 consecutive places, so
-// each lane fetches the chunk that the swizzle puts at its place.  `rows` (LDS)
-// holds the tile's physical rows.
+// each lane fetches the chunk that the swizzle puts at its place.
 template <typename S>
-__device__ __forceinline__ void load_mla_tile(const uint16_t* plane, const int* rows, lds_ptr dst, int wave, int lane) {
+__device__ __forceinline__ void load_mla_tile(const uint16_t* plane, const TileRows& rows, lds_ptr dst, int wave, int lane) {
 #pragma unroll
   for (int i = 0; i < S::BN / S::WAVES; ++i) {   // a row's latent part each
     const int r = i * S::WAVES + wave;
-    const int64_t row = __builtin_amdgcn_readfirstlane(rows[r]);
+    const int64_t row = __builtin_amdgcn_readfirstlane(rows(r));
     load_lds(dst + r * 1024, plane + row * kRowElems, static_cast<uint32_t>(lane ^ swizzle<64>(r)) * 16);
   }
 #pragma unroll
@@ -227,14 +250,14 @@ __device__ __forceinline__ void load_mla_tile(const uint16_t* plane, const int* 
     const int b = i * S::WAVES + wave;
     if (b >= S::BN / 8) break;
     const int r = b * 8 + (lane >> 3);
-    load_lds(dst + S::MAIN + b * 1024, plane + int64_t{rows[r]} * kRowElems + kKvLoraRank + ((lane & 7) ^ swizzle<8>(r)) * 8);
+    load_lds(dst + S::MAIN + b * 1024, plane + int64_t{rows(r)} * kRowElems + kKvLoraRank + ((lane & 7) ^ swizzle<8>(r)) * 8);
   }
 }
 // K and V of one KV head; chunks past `live` are left alone (they were zeroed
 // once).  `col` is the head's first value in a row.
 template <typename S, bool PART>
 __device__ __forceinline__ void load_gqa_tile(const uint16_t* k, const uint16_t* v, int64_t row_elems, int live,
-                                              const int* rows, lds_ptr dst, int wave, int lane) {
+                                              const TileRows& rows, lds_ptr dst, int wave, int lane) {
   constexpr int N = S::BN * S::ROWCH / 64;   // instructions per region
   static_assert(N % S::WAVES == 0, "the same number for every wave");
 #pragma unroll
@@ -243,7 +266,7 @@ __device__ __forceinline__ void load_gqa_tile(const uint16_t* k, const uint16_t*
     const int place = b * 64 + lane;
     const int r = place / S::ROWCH;
     const int c = (place % S::ROWCH) ^ swizzle<S::ROWCH>(r);
-    const int64_t off = rows[r] * row_elems + c * 8;
+    const int64_t off = rows(r) * row_elems + c * 8;
     if (!PART || c < live) {
       load_lds(dst + b * 1024, k + off);
       load_lds(dst + S::MAIN + b * 1024, v + off);
@@ -271,7 +294,6 @@ __device__ __forceinline__ void load_gqa_tile(const uint16_t* k, const uint16_t*
 template <typename S>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::WAVES / 4))) void attend_kernel(AttendLaunch a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ int s_rows[2][S::BN];
   constexpr int QN = S::QN, KT = S::KVT / 16, DT = S::DV / 16, KK = S::DK / 32;
   const int kvh = blockIdx.x % a.kv_heads;
   const int item = blockIdx.x / a.kv_heads;
@@ -325,12 +347,17 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   const int full_lo = rows_seen(a, it, last).lo;
   const int full_hi = min(rows_seen(a, it, it.row0).hi, share.hi);
 
-  auto phys = [&](int tile) {   // rows past the sequence repeat its last one
-    return static_cast<int>(physical_row(a, it.seq, min(share.lo + tile * S::BN + tid, it.kv_len - 1)));
+  // A wave's own copy of the page numbers of the last few tiles' rows, asked for
+  // AHEAD tiles before the tile itself.
+  int* const pages = reinterpret_cast<int*>(smem + S::STAGES * S::STAGE) + wave * S::PAGES * S::BN;
+  const int* const table = a.page_table + static_cast<int64_t>(it.seq) * a.max_pages_per_seq;
+  auto load_pages = [&](int tile) {
+    const int j = min(share.lo + tile * S::BN + lane, it.kv_len - 1);
+    if (S::BN == 64 || lane < S::BN) load_lds4((lds_ptr)(pages + tile % S::PAGES * S::BN), table + (j >> a.page_shift));
   };
   auto load = [&](int tile) {
-    const int* rows = s_rows[tile & 1];
-    const lds_ptr dst = lds + (tile & 1) * S::STAGE;
+    const TileRows rows{pages + tile % S::PAGES * S::BN, share.lo + tile * S::BN, it.kv_len - 1, a.page_shift, a.num_pages};
+    const lds_ptr dst = lds + tile % S::STAGES * S::STAGE;
     if constexpr (S::MLA) {
       load_mla_tile<S>(a.k_plane, rows, dst, wave, lane);
     } else {
@@ -343,14 +370,12 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   };
 
   if (!S::MLA && live < S::ROWCH) {
-    for (int i = tid; i < 2 * S::STAGE / 16; i += S::THREADS) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
+    for (int i = tid; i < S::STAGES * S::STAGE / 16; i += S::THREADS) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
+    __syncthreads();
   }
-  if (tiles > 0 && tid < S::BN) {
-    s_rows[0][tid] = phys(0);
-    if (tiles > 1) s_rows[1][tid] = phys(1);
-  }
-  __syncthreads();
-  if (tiles > 0) load(0);
+  for (int i = 0; i < min(2 * S::AHEAD, tiles); ++i) load_pages(i);
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+  for (int i = 0; i < min(S::AHEAD, tiles); ++i) load(i);
 
   // this lane's byte offsets within a stage
   int k_off[4], p_off[2], v_off[8];
@@ -373,19 +398,24 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 
   bool rows_only = false;
   for (int tile = 0; tile < tiles; ++tile) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's part of the tile has landed
-    __syncthreads();                      // everyone's has, and the other stage is free
-    if (tile + 1 < tiles) load(tile + 1);
-    int next_row = 0;
-    if (tile + 2 < tiles && tid < S::BN) next_row = phys(tile + 2);
+    // this wave's part of the tile has landed once only the loads of the
+    // AHEAD - 1 later tiles are on their way (loads land in order; the first
+    // tiles come without page numbers between them); near the end there are
+    // fewer
+    constexpr int later = S::LOADS * (S::AHEAD - 1);
+    if (tile + S::AHEAD - 1 < tiles) __builtin_amdgcn_s_waitcnt(0x0F70 | (later & 15) | (later >> 4) << 14);
+    else __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();   // everyone's has, and the stage of the tile before is free
+    if (tile + 2 * S::AHEAD < tiles) load_pages(tile + 2 * S::AHEAD);
+    if (tile + S::AHEAD < tiles) load(tile + S::AHEAD);
 
-    const lds_ptr st = lds + (tile & 1) * S::STAGE;
+    const lds_ptr st = lds + tile % S::STAGES * S::STAGE;
     const int j0 = share.lo + tile * S::BN;
     const bool whole = j0 >= full_lo && j0 + S::BN <= full_hi;
     if (!whole) {
       bool bad = false;
       for (int i = tid; i < S::BN * S::ROWCH; i += S::THREADS)
-        bad |= not_finite(reinterpret_cast<const chunk_t*>(smem + (tile & 1) * S::STAGE + S::VALUES)[i]);
+        bad |= not_finite(reinterpret_cast<const chunk_t*>(smem + tile % S::STAGES * S::STAGE + S::VALUES)[i]);
       rows_only = __syncthreads_or(bad);
       if (rows_only) break;
     }
@@ -506,7 +536,6 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (tile + 2 < tiles && tid < S::BN) s_rows[tile & 1][tid] = next_row;
   }
 
   if (rows_only) {
@@ -526,7 +555,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
     // the waves' sums over their own cached rows, put together in LDS
     __shared__ float s_m[S::WAVES][16 * QN], s_l[S::WAVES][16 * QN];
     constexpr int OUT_ROWS = 16 * QN * S::QW;
-    static_assert(S::KW * OUT_ROWS * S::DV * 4 <= 2 * S::STAGE, "the sums fit where the tiles were");
+    static_assert(S::KW * OUT_ROWS * S::DV * 4 <= S::STAGES * S::STAGE, "the sums fit where the tiles were");
     __syncthreads();   // the tiles are no longer read
     float* sums = reinterpret_cast<float*>(smem);
     if (g == 0)
@@ -606,7 +635,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 
 template <typename S>
 hipError_t launch_shape(const AttendLaunch& a, hipStream_t s) {
-  constexpr int lds = 2 * S::STAGE;
+  constexpr int lds = S::LDS;
   static bool set[64];   // per device: hipFuncSetAttribute is not cheap
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -624,10 +653,10 @@ hipError_t launch_shape(const AttendLaunch& a, hipStream_t s) {
 template <bool MLA, int DP>
 hipError_t launch_tile(const AttendLaunch& a, hipStream_t s) {
   switch (a.tile) {
-    case 16: return launch_shape<Shape<MLA, DP, 1, 1, 4, 64>>(a, s);
-    case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, 64>>(a, s);
-    case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, 64>>(a, s);
-    default: return launch_shape<Shape<MLA, DP, MLA ? 1 : 2, MLA ? 8 : 4, 1, MLA ? 32 : 64>>(a, s);
+    case 16: return launch_shape<Shape<MLA, DP, 1, 1, MLA ? 2 : 4, MLA ? 32 : 64, MLA ? 4 : (DP > 128 ? 2 : 3)>>(a, s);
+    case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, MLA ? 32 : 64, MLA ? 4 : (DP > 128 ? 2 : 3)>>(a, s);
+    case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, MLA ? 32 : 64, MLA ? 4 : 2>>(a, s);
+    default: return launch_shape<Shape<MLA, DP, MLA ? 1 : 2, MLA ? 8 : 4, 1, MLA ? 32 : 64, MLA ? 3 : 2>>(a, s);
   }
 }
 
@@ -680,6 +709,11 @@ int attend_tile(bool gqa, int dim, int64_t rows) {
   (void)gqa;
   (void)dim;
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
+
+int attend_groups(bool gqa, int dim, int tile) {
+  const int per_cu = !gqa || dim > 128 ? 1 : tile >= 64 ? 2 : 1;
+  return 256 * per_cu;
 }
 
 hipError_t launch_attend(const AttendLaunch& a, bool gqa, hipStream_t s) {

@@ -24,11 +24,11 @@ namespace {
 using ll::ceil_div;
 using ll::fail;
 
-// A sequence's rows are split over workgroups until this many (per tile size)
-// share the work; a share has at least kMinShare rows.
-constexpr int64_t kMinShare = 128;
 constexpr int64_t kMaxStride = int64_t{1} << 32;
-int64_t target_groups(int tile) { return tile >= 128 ? 256 : 512; }
+// Partial results of split tiles: query rows (times KV heads) that the step's
+// buffer holds, and shares (times KV heads) at most.
+constexpr int64_t kPartRows = 65536;
+constexpr int64_t kMaxShares = 2048;
 
 }  // namespace
 
@@ -40,7 +40,7 @@ struct ll_step {
   int32_t value_dim = 0;         // width of an output head
   int32_t tile = 16;             // query rows per attention item
   bool captured = false;         // a graph holds this step's attention: the tile stays
-  int64_t max_items = 0, max_slots = 0;
+  int64_t max_items = 0;
   // device: [counts | items | rows | tab | theta | parts]
   char* d_buf = nullptr;
   ll::StepCounts* d_counts = nullptr;
@@ -63,42 +63,95 @@ namespace {
 
 int64_t tiles_of(int64_t q_rows, int tile) { return ceil_div(q_rows, tile); }
 
-// The attention's items: every sequence's query rows in tiles, the last (and
-// longest) tile first; a tile whose cached rows exceed an even share of the
-// whole work is split over several workgroups.  Shares come first.
-int64_t plan_items(const ll_step* s, const std::vector<ll::StepSeq>& seqs, std::vector<ll::AttendItem>* out) {
-  const int tile = s->tile;
-  int64_t total = 0;
-  auto seen = [&](const ll::StepSeq& q, int64_t k) {   // rows the last query of tile k sees
-    const int64_t last = std::min<int64_t>((k + 1) * tile, int64_t{q.count} * s->group) - 1;
-    return int64_t{q.row0} + last / s->group + 1;
+// Shares of split tiles that the partial results' buffer holds, per KV head.
+int64_t max_slots(const ll_step* s, int tile) { return std::min(kMaxShares, kPartRows / tile) / s->kv_heads; }
+
+// How many cached rows a workgroup takes at most.  `seen` holds the rows that each
+// tile needs.  With few tiles a share is as short as the chip's workgroups allow,
+// so that all run at once; with many, shorter shares even out the end, and cost
+// their partial results.  Estimated in rows: a workgroup's own cost is about
+// `kOverhead` rows.
+int64_t pick_share(const ll_step* s, const std::vector<int64_t>& seen, int64_t groups) {
+  constexpr int64_t kOverhead = 160, kGrain = 64;
+  int64_t total = 0, longest = 1;
+  for (int64_t w : seen) {
+    total += w;
+    longest = std::max(longest, w);
+  }
+  const int64_t slots = max_slots(s, s->tile);
+  auto count = [&](int64_t share, int64_t* split) {   // workgroups per KV head, and those of split tiles
+    int64_t n = 0;
+    *split = 0;
+    for (int64_t w : seen) {
+      const int64_t k = ceil_div(w, share);
+      n += k;
+      if (k > 1) *split += k;
+    }
+    return n;
   };
-  for (const ll::StepSeq& q : seqs)
-    for (int64_t k = 0, n = tiles_of(int64_t{q.count} * s->group, tile); k < n; ++k) total += seen(q, k);
-  const int64_t share = std::max(kMinShare, ceil_div(total * s->kv_heads, target_groups(tile)));
-  int64_t slot = 0;
-  std::vector<ll::AttendItem> whole;
-  for (const ll::StepSeq& q : seqs) {
-    const int64_t q_rows = int64_t{q.count} * s->group;
-    for (int64_t k = tiles_of(q_rows, tile) - 1; k >= 0; --k) {
-      int64_t shares = ceil_div(seen(q, k), share);
-      if (shares > 1 && slot + shares > s->max_slots) shares = 1;   // cannot happen (see max_slots)
-      ll::AttendItem it{};
-      it.seq = q.seq;
-      it.tok0 = q.tok0;
-      it.q_rows = static_cast<int32_t>(q_rows);
-      it.row0 = static_cast<int32_t>(k * tile);
-      it.first = q.row0;
-      it.kv_len = q.row0 + q.count;
-      for (int64_t c = 0; c < shares; ++c) {
-        it.splits = static_cast<int32_t>(c | shares << 16);
-        it.slot = static_cast<int32_t>(slot + c);
-        (shares > 1 ? *out : whole).push_back(it);
-      }
-      if (shares > 1) slot += shares;
+  auto cost = [&](int64_t share, int64_t n) {
+    const int64_t rounds = ceil_div(n * s->kv_heads, groups);
+    if (rounds <= 1) return share + kOverhead;
+    return total * s->kv_heads / groups + share / 2 + rounds * kOverhead;
+  };
+  int64_t split = 0, best = longest, best_cost = cost(longest, count(longest, &split));
+  for (int rounds = 1; rounds <= 4; ++rounds) {
+    int64_t lo = 1, hi = ceil_div(longest, kGrain);   // the shortest share (in grains) that fits
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      const int64_t n = count(mid * kGrain, &split);
+      if (n * s->kv_heads <= rounds * groups && split <= slots) hi = mid;
+      else lo = mid + 1;
+    }
+    const int64_t share = hi * kGrain, n = count(share, &split);
+    if (split > slots) continue;
+    if (const int64_t c = cost(share, n); c < best_cost) {
+      best = share;
+      best_cost = c;
     }
   }
-  out->insert(out->end(), whole.begin(), whole.end());
+  return best;
+}
+
+// The attention's items: every sequence's query rows in tiles, the longest first;
+// a tile that needs more cached rows than a share is split over several
+// workgroups.  Shares of split tiles come before the others.
+int64_t plan_items(const ll_step* s, const std::vector<ll::StepSeq>& seqs, std::vector<ll::AttendItem>* out) {
+  struct Tile {
+    int64_t seen;
+    int32_t seq, index;
+  };
+  const int tile = s->tile;
+  std::vector<Tile> tiles;
+  std::vector<int64_t> seen;
+  for (size_t i = 0; i < seqs.size(); ++i) {
+    const int64_t q_rows = int64_t{seqs[i].count} * s->group;
+    for (int64_t k = tiles_of(q_rows, tile) - 1; k >= 0; --k) {
+      const int64_t last = std::min<int64_t>((k + 1) * tile, q_rows) - 1;
+      seen.push_back(int64_t{seqs[i].row0} + last / s->group + 1);
+      tiles.push_back(Tile{seen.back(), static_cast<int32_t>(i), static_cast<int32_t>(k)});
+    }
+  }
+  std::stable_sort(tiles.begin(), tiles.end(), [](const Tile& a, const Tile& b) { return a.seen > b.seen; });
+  const int64_t share = pick_share(s, seen, ll::attend_groups(s->pool->gqa, s->value_dim, tile));
+  int64_t slot = 0;
+  for (const Tile& x : tiles) {
+    const ll::StepSeq& q = seqs[x.seq];
+    const int64_t shares = ceil_div(x.seen, share);
+    ll::AttendItem it{};
+    it.seq = q.seq;
+    it.tok0 = q.tok0;
+    it.q_rows = q.count * s->group;
+    it.row0 = x.index * tile;
+    it.first = q.row0;
+    it.kv_len = q.row0 + q.count;
+    for (int64_t c = 0; c < shares; ++c) {
+      it.splits = static_cast<int32_t>(c | shares << 16);
+      it.slot = static_cast<int32_t>(slot + c);
+      out->push_back(it);
+    }
+    if (shares > 1) slot += shares;   // the longer tiles: all before the first whole one
+  }
   return slot;
 }
 
@@ -199,11 +252,7 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
   s->seqs.reserve(static_cast<size_t>(d->max_seqs));
   s->gens.reserve(static_cast<size_t>(d->max_seqs));
   const int tile = ll::attend_tile(p->gqa, s->value_dim, int64_t{d->max_tokens} * s->group);
-  // tiles of the smallest size; each split tile has at most twice its even
-  // share of target_groups
-  const int64_t groups = target_groups(16);
-  s->max_slots = 2 * groups / kv_heads + 2;
-  s->max_items = int64_t{d->max_tokens} * s->group / 16 + d->max_seqs + s->max_slots;
+  s->max_items = int64_t{d->max_tokens} * s->group / 16 + d->max_seqs + kMaxShares / kv_heads;
   if (s->max_items * kv_heads > ll::kMaxDispatchItems / 256)
     return fail(LL_EUNSUPPORTED, "the step's attention would not fit one dispatch");
   const size_t pairs = p->theta.size();
@@ -218,9 +267,7 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
   const size_t o_rows = take(sizeof(int32_t) * static_cast<size_t>(d->max_tokens));
   const size_t o_tab = take(sizeof(float) * 2 * pairs * static_cast<size_t>(d->max_tokens));
   const size_t o_theta = take(sizeof(double) * pairs);
-  // tile 128 splits into half as many shares as the smaller tiles
-  const size_t part_rows = std::max<size_t>(static_cast<size_t>(s->max_slots) * kv_heads * std::min(tile, 64),
-                                            tile > 64 ? (target_groups(tile) * 2 + 2 * kv_heads) * size_t{128} : 0);
+  const size_t part_rows = static_cast<size_t>(std::min(kMaxShares * tile, kPartRows));
   const size_t o_po = take(part_rows * s->value_dim * sizeof(float));
   const size_t o_ml = take(part_rows * 2 * sizeof(float));
   ll::DeviceGuard g(s->device);
@@ -509,7 +556,7 @@ ll_status ll_step_attend(ll_step* s, const ll_attend_desc* d, void* stream) try 
   a.counts = s->d_counts;
   a.items = s->d_items;
   a.n_items = static_cast<int32_t>(capturing ? s->max_items : s->items);
-  a.n_shares = static_cast<int32_t>(capturing ? s->max_slots : s->shares);
+  a.n_shares = static_cast<int32_t>(capturing ? max_slots(s, s->tile) : s->shares);
   a.kv_heads = s->kv_heads;
   a.group = s->group;
   a.tile = s->tile;

@@ -124,6 +124,8 @@ hipError_t launch_step_setup(const StepSetupLaunch& a, hipStream_t s);
 hipError_t launch_append(const AppendLaunch& a, bool gqa, int pairing, hipStream_t s);
 // Query rows per item for a step whose sequences bring at most `rows` each.
 int attend_tile(bool gqa, int dim, int64_t rows);
+// Workgroups of that tile that the chip runs at once.
+int attend_groups(bool gqa, int dim, int tile);
 hipError_t launch_attend(const AttendLaunch& a, bool gqa, hipStream_t s);
 
 }  // namespace ll
