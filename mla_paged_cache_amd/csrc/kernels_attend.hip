@@ -223,26 +223,15 @@ __device__ __forceinline__ void load_lds4(lds_ptr dst, const void* src) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory");
 }
 
-// Where the rows of a tile lie: the page numbers of its rows, in LDS.
-struct TileRows {
-  const int* pages;
-  int j0, last;          // the tile's first row; the sequence's last one, which rows past it repeat
-  int shift, num_pages;
-  __device__ __forceinline__ int operator()(int r) const {
-    int page = pages[r];
-    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(num_pages)) page = 0;   // as in physical_row
-    return (page << shift) + (min(j0 + r, last) & ((1 << shift) - 1));
-  }
-};
-
 // A tile from the cache to LDS: an instruction fills 64 consecutive places, so
-// each lane fetches the chunk that the swizzle puts at its place.
+// each lane fetches the chunk that the swizzle puts at its place.  Lane r holds
+// the physical row of the tile's row r.
 template <typename S>
-__device__ __forceinline__ void load_mla_tile(const uint16_t* plane, const TileRows& rows, lds_ptr dst, int wave, int lane) {
+__device__ __forceinline__ void load_mla_tile(const uint16_t* plane, int phys, lds_ptr dst, int wave, int lane) {
 #pragma unroll
   for (int i = 0; i < S::BN / S::WAVES; ++i) {   // a row's latent part each
     const int r = i * S::WAVES + wave;
-    const int64_t row = __builtin_amdgcn_readfirstlane(rows(r));
+    const int64_t row = __builtin_amdgcn_readlane(phys, r);
     load_lds(dst + r * 1024, plane + row * kRowElems, static_cast<uint32_t>(lane ^ swizzle<64>(r)) * 16);
   }
 #pragma unroll
@@ -250,14 +239,15 @@ __device__ __forceinline__ void load_mla_tile(const uint16_t* plane, const TileR
     const int b = i * S::WAVES + wave;
     if (b >= S::BN / 8) break;
     const int r = b * 8 + (lane >> 3);
-    load_lds(dst + S::MAIN + b * 1024, plane + int64_t{rows(r)} * kRowElems + kKvLoraRank + ((lane & 7) ^ swizzle<8>(r)) * 8);
+    load_lds(dst + S::MAIN + b * 1024,
+             plane + int64_t{__shfl(phys, r)} * kRowElems + kKvLoraRank + ((lane & 7) ^ swizzle<8>(r)) * 8);
   }
 }
 // K and V of one KV head; chunks past `live` are left alone (they were zeroed
-// once).  `col` is the head's first value in a row.
+// once).
 template <typename S, bool PART>
 __device__ __forceinline__ void load_gqa_tile(const uint16_t* k, const uint16_t* v, int64_t row_elems, int live,
-                                              const TileRows& rows, lds_ptr dst, int wave, int lane) {
+                                              int phys, lds_ptr dst, int wave, int lane) {
   constexpr int N = S::BN * S::ROWCH / 64;   // instructions per region
   static_assert(N % S::WAVES == 0, "the same number for every wave");
 #pragma unroll
@@ -266,7 +256,7 @@ __device__ __forceinline__ void load_gqa_tile(const uint16_t* k, const uint16_t*
     const int place = b * 64 + lane;
     const int r = place / S::ROWCH;
     const int c = (place % S::ROWCH) ^ swizzle<S::ROWCH>(r);
-    const int64_t off = rows(r) * row_elems + c * 8;
+    const int64_t off = __shfl(phys, r) * row_elems + c * 8;
     if (!PART || c < live) {
       load_lds(dst + b * 1024, k + off);
       load_lds(dst + S::MAIN + b * 1024, v + off);
@@ -356,16 +346,21 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
     if (S::BN == 64 || lane < S::BN) load_lds4((lds_ptr)(pages + tile % S::PAGES * S::BN), table + (j >> a.page_shift));
   };
   auto load = [&](int tile) {
-    const TileRows rows{pages + tile % S::PAGES * S::BN, share.lo + tile * S::BN, it.kv_len - 1, a.page_shift, a.num_pages};
+    // rows past the sequence's last one repeat it; a page number outside the
+    // pool reads page 0 (see physical_row)
+    int page = pages[tile % S::PAGES * S::BN + (lane & (S::BN - 1))];
+    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) page = 0;
+    const int j = min(share.lo + tile * S::BN + (lane & (S::BN - 1)), it.kv_len - 1);
+    const int phys = (page << a.page_shift) + (j & ((1 << a.page_shift) - 1));
     const lds_ptr dst = lds + tile % S::STAGES * S::STAGE;
     if constexpr (S::MLA) {
-      load_mla_tile<S>(a.k_plane, rows, dst, wave, lane);
+      load_mla_tile<S>(a.k_plane, phys, dst, wave, lane);
     } else {
       const int64_t row_elems = int64_t{a.kv_heads} * a.dim, col = int64_t{kvh} * a.dim;
       if (live == S::ROWCH)
-        load_gqa_tile<S, false>(a.k_plane + col, a.v_plane + col, row_elems, live, rows, dst, wave, lane);
+        load_gqa_tile<S, false>(a.k_plane + col, a.v_plane + col, row_elems, live, phys, dst, wave, lane);
       else
-        load_gqa_tile<S, true>(a.k_plane + col, a.v_plane + col, row_elems, live, rows, dst, wave, lane);
+        load_gqa_tile<S, true>(a.k_plane + col, a.v_plane + col, row_elems, live, phys, dst, wave, lane);
     }
   };
 
@@ -660,47 +655,61 @@ hipError_t launch_tile(const AttendLaunch& a, hipStream_t s) {
   }
 }
 
-// The shares of a split tile put together: a wave per query row, each share
-// weighed by how far its maximum lies below the largest.
+// The shares of a split tile put together: 4 values of a query row per thread,
+// each share weighed by how far its maximum lies below the largest.  Bound by the
+// latency of its loads, so several shares are on their way at once.
 template <bool GQA>
 __global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendLaunch a) {
-  const int lane = threadIdx.x & 63;
-  const int rows4 = a.tile / 4;
-  const int rr = (blockIdx.x % rows4) * 4 + (threadIdx.x >> 6);
-  const int b = blockIdx.x / rows4;
+  const int dv = GQA ? a.dim : kKvLoraRank;
+  const int per_row = dv / 4;
+  const int unit = blockIdx.x % a.join_blocks * kAttendThreads + threadIdx.x;
+  const int b = blockIdx.x / a.join_blocks;
   const int kvh = b % a.kv_heads;
   const int i = b / a.kv_heads;
-  if (i >= a.counts->shares) return;
   const AttendItem it = a.items[i];
-  const int shares = it.splits >> 16;
+  if (i >= a.counts->shares || (it.splits & 0xFFFF) != 0) return;
+  const int rr = unit / per_row, c4 = unit - rr * per_row;
   const int r = it.row0 + rr;
-  if ((it.splits & 0xFFFF) != 0 || r >= it.q_rows) return;
-  const int dv = GQA ? a.dim : kKvLoraRank;
-  const bool live = lane * 8 < dv;
+  if (rr >= a.tile || r >= it.q_rows) return;
+  const int shares = it.splits >> 16;
   const int64_t at0 = (static_cast<int64_t>(it.slot) * a.kv_heads + kvh) * a.tile + rr;
   const int64_t step = static_cast<int64_t>(a.kv_heads) * a.tile;
-  float m = -__builtin_inff();
-  for (int c = lane; c < shares; c += 64) m = fmaxf(m, a.part_ml[(at0 + c * step) * 2]);
-  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-  float l = 0.f;
-  Vals o{};
-  for (int c = 0; c < shares; ++c) {
-    const int64_t at = at0 + c * step;
-    const float lc = a.part_ml[at * 2 + 1];
-    if (lc == 0.f) continue;   // an empty share
-    const float w = exp2_(a.part_ml[at * 2] - m);
-    l = __builtin_fmaf(lc, w, l);
-    if (!live) continue;
+  const float* const ml = a.part_ml + at0 * 2;
+  const f32x4* const po = reinterpret_cast<const f32x4*>(a.part_o + at0 * dv) + c4;
+  constexpr int N = 8;
+  float m = -__builtin_inff(), l = 0.f;
+  f32x4 o{0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < shares; c += N) {
+    float mc[N], lc[N];
+    f32x4 oc[N];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) o.v[k] = __builtin_fmaf(a.part_o[at * dv + lane * 8 + k], w, o.v[k]);
+    for (int k = 0; k < N; ++k) {   // past the last share: the last one again, weighing nothing
+      const int64_t s = min(c + k, shares - 1) * step;
+      mc[k] = ml[s * 2];
+      lc[k] = c + k < shares ? ml[s * 2 + 1] : 0.f;
+      oc[k] = po[s * per_row];
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (lc[k] != 0.f) top = fmaxf(top, mc[k]);
+    const float keep = top == m ? 1.f : exp2_(m - top);
+    l *= keep;
+    o *= keep;
+    m = top;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (lc[k] == 0.f) continue;   // an empty share
+      const float w = mc[k] == m ? 1.f : exp2_(mc[k] - m);
+      l = __builtin_fmaf(lc[k], w, l);
+      o += oc[k] * w;
+    }
   }
-  const int t = it.tok0 + r / a.group, h = kvh * a.group + r % a.group;
+  const int tt = r / a.group, h = kvh * a.group + r - tt * a.group;
+  const int64_t t = it.tok0 + tt;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = to_bf16(o.v[2 * k] * inv) | (to_bf16(o.v[2 * k + 1] * inv) << 16);
-  if (live) *reinterpret_cast<chunk_t*>(a.out + t * a.o_ts + h * a.o_hs + lane * 8) = chunk_t{w[0], w[1], w[2], w[3]};
-  if (a.lse && lane == 0) a.lse[static_cast<int64_t>(t) * a.heads + h] = l == 0.f ? -__builtin_inff() : (m + __log2f(l)) * kLn2;
+  *reinterpret_cast<bf16x4*>(a.out + t * a.o_ts + h * a.o_hs + c4 * 4) = __builtin_convertvector(o * inv, bf16x4);
+  if (a.lse && c4 == 0) a.lse[t * a.heads + h] = l == 0.f ? -__builtin_inff() : (m + __log2f(l)) * kLn2;
 }
 
 }  // namespace
@@ -724,7 +733,7 @@ hipError_t launch_attend(const AttendLaunch& a, bool gqa, hipStream_t s) {
   else e = launch_tile<false, 256>(a, s);
   if (e != hipSuccess || a.n_shares == 0) return e;
   void (*k)(AttendLaunch) = gqa ? attend_join_kernel<true> : attend_join_kernel<false>;
-  k<<<dim3(static_cast<unsigned>(int64_t{a.n_shares} * a.kv_heads * (a.tile / 4))), dim3(kAttendThreads), 0, s>>>(a);
+  k<<<dim3(static_cast<unsigned>(int64_t{a.n_shares} * a.kv_heads * a.join_blocks)), dim3(kAttendThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 

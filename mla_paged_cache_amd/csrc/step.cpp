@@ -557,6 +557,7 @@ ll_status ll_step_attend(ll_step* s, const ll_attend_desc* d, void* stream) try 
   a.items = s->d_items;
   a.n_items = static_cast<int32_t>(capturing ? s->max_items : s->items);
   a.n_shares = static_cast<int32_t>(capturing ? max_slots(s, s->tile) : s->shares);
+  a.join_blocks = static_cast<int32_t>(ceil_div(int64_t{s->tile} * s->value_dim, 1024));
   a.kv_heads = s->kv_heads;
   a.group = s->group;
   a.tile = s->tile;

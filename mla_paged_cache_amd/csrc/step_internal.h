@@ -93,6 +93,7 @@ struct AttendLaunch {
   const AttendItem* items;
   int32_t n_items;               // items the grid covers
   int32_t n_shares;              // shares that the joining grid covers (0: nothing to join)
+  int32_t join_blocks;           // workgroups that join one tile
   int32_t kv_heads;
   int32_t group;                 // query heads per KV head
   int32_t tile;                  // query rows of an item
