@@ -201,6 +201,8 @@ struct Shape {
   static constexpr int LDS = STAGES * STAGE + WAVES * PAGES * BN * 4;
   static constexpr int KVT = BN / KW;                        // cached rows of a tile per wave
   static constexpr int TILE = 16 * QN * QW;                  // query rows
+  // the sums fill the accumulation registers, which only assembly can ask for
+  static constexpr bool ACC = QN * DV / 4 >= 256;
   static_assert(KVT % 16 == 0 && BN <= 64, "whole matrix tiles, a lane per row");
   static_assert(LOADS * (AHEAD - 1) < 64, "the wait counter's range");
 };
@@ -328,7 +330,10 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
     m[n] = -__builtin_inff();
     l[n] = 0.f;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) o[d][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int d = 0; d < DT; ++d) {
+      o[d][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (S::ACC) asm volatile("" : "+a"(o[d][n]));
+    }
   }
 
   const int tiles = (share.hi - share.lo + S::BN - 1) / S::BN;
@@ -465,7 +470,13 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
         }
       grew |= top[n] > m[n] + 8.f;
     }
+    if constexpr (S::ACC)   // the sums stay where they are, whatever follows reads
+#pragma unroll
+      for (int n = 0; n < QN; ++n)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) asm volatile("" : "+a"(o[d][n]));
     if (__any(grew)) {
+      if constexpr (S::ACC) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");   // results of the last products
 #pragma unroll
       for (int n = 0; n < QN; ++n) {
         float x = fmaxf(top[n], m[n]);
@@ -475,7 +486,14 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
         m[n] = x;
         l[n] *= keep;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) o[d][n] *= keep;
+        for (int d = 0; d < DT; ++d) {
+          if constexpr (S::ACC) asm volatile("" : "+a"(o[d][n]));   // four at a time leave the accumulators
+          o[d][n] *= keep;
+          if constexpr (S::ACC) {
+            asm volatile("" : "+a"(o[d][n]));
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
       }
     }
     bf16x4 p[KT][QN];
@@ -526,7 +544,10 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 #pragma unroll
         for (int n = 0; n < QN; ++n) {
           const bf16x8 w = __builtin_shufflevector(p[k][n], p[k + 1][n], 0, 1, 2, 3, 4, 5, 6, 7);
-          o[d][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[i & 3], w, o[d][n], 0, 0, 0);
+          if constexpr (S::ACC)   // an operand just written by an ordinary instruction needs two wait states
+            asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(o[d][n]) : "v"(y[i & 3]), "v"(w));
+          else
+            o[d][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[i & 3], w, o[d][n], 0, 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -539,6 +560,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
     return;
   }
 
+  if constexpr (S::ACC) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");   // results of the last products
 #pragma unroll
   for (int n = 0; n < QN; ++n) {
     l[n] += __shfl_xor(l[n], 16);
@@ -609,8 +631,11 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
       if (shares > 1) {
         const int64_t at = (static_cast<int64_t>(it.slot) * a.kv_heads + kvh) * a.tile + row;
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+        for (int d = 0; d < DT; ++d) {
+          if constexpr (S::ACC) asm volatile("" : "+a"(o[d][n]));
           if (d * 16 + g * 4 < dv) *reinterpret_cast<f32x4*>(a.part_o + at * dv + d * 16 + g * 4) = o[d][n];
+          __builtin_amdgcn_sched_barrier(0);
+        }
         if (g == 0) {
           a.part_ml[at * 2] = m[n];
           a.part_ml[at * 2 + 1] = l[n];
@@ -619,9 +644,12 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
         const float inv = l[n] == 0.f ? 0.f : 1.f / l[n];
         uint16_t* out = a.out + t * a.o_ts + h_of[n] * a.o_hs;
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+        for (int d = 0; d < DT; ++d) {
+          if constexpr (S::ACC) asm volatile("" : "+a"(o[d][n]));
           if (d * 16 + g * 4 < dv)
             *reinterpret_cast<bf16x4*>(out + d * 16 + g * 4) = __builtin_convertvector(o[d][n] * inv, bf16x4);
+          __builtin_amdgcn_sched_barrier(0);
+        }
         if (a.lse && g == 0) a.lse[t * a.heads + h_of[n]] = l[n] == 0.f ? -__builtin_inff() : (m[n] + __log2f(l[n])) * kLn2;
       }
     }
@@ -651,7 +679,7 @@ hipError_t launch_tile(const AttendLaunch& a, hipStream_t s) {
     case 16: return launch_shape<Shape<MLA, DP, 1, 1, MLA ? 2 : 4, MLA ? 32 : 64, MLA ? 4 : (DP > 128 ? 2 : 3)>>(a, s);
     case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, MLA ? 32 : 64, MLA ? 4 : (DP > 128 ? 2 : 3)>>(a, s);
     case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, MLA ? 32 : 64, MLA ? 4 : 2>>(a, s);
-    default: return launch_shape<Shape<MLA, DP, MLA ? 1 : 2, MLA ? 8 : 4, 1, MLA ? 32 : 64, MLA ? 3 : 2>>(a, s);
+    default: return launch_shape<Shape<MLA, DP, 2, 4, 1, MLA ? 32 : 64, MLA ? 3 : 2>>(a, s);
   }
 }
 
