@@ -6,6 +6,8 @@
 // One pass over the rows keeps m, l and the unscaled sum of v, in float32; when m
 // grows, l and the sum are scaled down.  Scores are kept in base 2 (times
 // log2 e), so that each exponential is one instruction.
+#include <type_traits>
+
 #include "device_common.h"
 #include "step_internal.h"
 
@@ -199,14 +201,16 @@ struct Shape {
   static constexpr int STAGES = STAGES_;                     // tiles in LDS
   static constexpr int AHEAD = STAGES - 1;                   // a tile is asked for this many tiles ahead
   static constexpr int PAGES = 2 * AHEAD + 1;                // tiles whose page numbers are in LDS
-  // a tile's loads per wave, at least
+  // a tile's loads per wave, at least, and the pieces they come in
   static constexpr int LOADS = MLA ? BN / WAVES + BN / 8 / WAVES : 2 * BN * ROWCH / 64 / WAVES;
+  static constexpr int PIECES = MLA ? BN / WAVES + (BN / 8 + WAVES - 1) / WAVES : BN * ROWCH / 64 / WAVES;
   static constexpr int LDS = STAGES * STAGE + WAVES * PAGES * BN * 4;
   static constexpr int KVT = BN / KW;                        // cached rows of a tile per wave
   static constexpr int TILE = 16 * QN * QW;                  // query rows
   // the sums fill the accumulation registers, which only assembly can ask for
   static constexpr bool ACC = QN * DV / 4 >= 256;
-  static_assert(KVT % 16 == 0 && BN <= 64, "whole matrix tiles, a lane per row");
+  static_assert(KVT % 16 == 0 && BN <= 64 && BN % WAVES == 0, "whole matrix tiles, a lane per row");
+  static_assert(BN * ROWCH / 64 % WAVES == 0 && AHEAD >= 2, "as many loads for every wave; the next tile is there early");
   static_assert(LOADS * (AHEAD - 1) < 64, "the wait counter's range");
 };
 
@@ -230,42 +234,35 @@ __device__ __forceinline__ void load_lds4(lds_ptr dst, const void* src) {
 
 // A tile from the cache to LDS: an instruction fills 64 consecutive places, so
 // each lane fetches the chunk that the swizzle puts at its place.  Lane r holds
-// the physical row of the tile's row r.
+// the physical row of the tile's row r.  A wave's part comes in S::PIECES pieces,
+// which the products of an earlier tile cover.
 template <typename S>
-__device__ __forceinline__ void load_mla_tile(const uint16_t* plane, int phys, lds_ptr dst, int wave, int lane) {
-#pragma unroll
-  for (int i = 0; i < S::BN / S::WAVES; ++i) {   // a row's latent part each
+__device__ __forceinline__ void load_mla_piece(int i, const uint16_t* plane, int phys, lds_ptr dst, int wave, int lane) {
+  if (i < S::BN / S::WAVES) {   // a row's latent part
     const int r = i * S::WAVES + wave;
     const int64_t row = __builtin_amdgcn_readlane(phys, r);
     load_lds(dst + r * 1024, plane + row * kRowElems, static_cast<uint32_t>(lane ^ swizzle<64>(r)) * 16);
-  }
-#pragma unroll
-  for (int i = 0; i < (S::BN / 8 + S::WAVES - 1) / S::WAVES; ++i) {   // 8 rows' k_pe each
-    const int b = i * S::WAVES + wave;
-    if (b >= S::BN / 8) break;
+  } else {                      // 8 rows' k_pe
+    const int b = (i - S::BN / S::WAVES) * S::WAVES + wave;
+    if (S::BN / 8 % S::WAVES != 0 && b >= S::BN / 8) return;
     const int r = b * 8 + (lane >> 3);
     load_lds(dst + S::MAIN + b * 1024,
              plane + int64_t{__shfl(phys, r)} * kRowElems + kKvLoraRank + ((lane & 7) ^ swizzle<8>(r)) * 8);
   }
 }
-// K and V of one KV head; chunks past `live` are left alone (they were zeroed
-// once).
-template <typename S, bool PART>
-__device__ __forceinline__ void load_gqa_tile(const uint16_t* k, const uint16_t* v, int64_t row_elems, int live,
-                                              int phys, lds_ptr dst, int wave, int lane) {
-  constexpr int N = S::BN * S::ROWCH / 64;   // instructions per region
-  static_assert(N % S::WAVES == 0, "the same number for every wave");
-#pragma unroll
-  for (int i = 0; i < N / S::WAVES; ++i) {
-    const int b = i * S::WAVES + wave;
-    const int place = b * 64 + lane;
-    const int r = place / S::ROWCH;
-    const int c = (place % S::ROWCH) ^ swizzle<S::ROWCH>(r);
-    const int64_t off = __shfl(phys, r) * row_elems + c * 8;
-    if (!PART || c < live) {
-      load_lds(dst + b * 1024, k + off);
-      load_lds(dst + S::MAIN + b * 1024, v + off);
-    }
+// K and V of one KV head (k and v: its first value in row 0); chunks past `live`
+// are left alone (they were zeroed once).
+template <typename S>
+__device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const uint16_t* v, int row_elems, int live,
+                                               int phys, lds_ptr dst, int wave, int lane) {
+  const int b = i * S::WAVES + wave;
+  const int place = b * 64 + lane;
+  const int r = place / S::ROWCH;
+  const int c = (place % S::ROWCH) ^ swizzle<S::ROWCH>(r);
+  const int64_t off = int64_t{__shfl(phys, r)} * row_elems + c * 8;
+  if (c < live) {
+    load_lds(dst + b * 1024, k + off);
+    load_lds(dst + S::MAIN + b * 1024, v + off);
   }
 }
 
@@ -287,7 +284,7 @@ __device__ __forceinline__ void load_gqa_tile(const uint16_t* k, const uint16_t*
 // times a value that is not finite is not 0, such a tile is searched for those,
 // and the item falls back to reading exactly the rows each query sees.
 template <typename S>
-__global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::WAVES / 4))) void attend_kernel(AttendLaunch a) {
+__global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::WAVES > 4 ? 2 : 1))) void attend_kernel(AttendLaunch a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   constexpr int QN = S::QN, KT = S::KVT / 16, DT = S::DV / 16, KK = S::DK / 32;
   const int kvh = blockIdx.x % a.kv_heads;
@@ -302,19 +299,15 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   const int live = S::MLA ? S::ROWCH : a.dim / 8;   // chunks a cached head has
 
   // queries: this lane's 8 values of each 32 of the row
-  int t_of[QN], h_of[QN];
-  Seen seen[QN];
   bf16x8 q[QN][KK];
 #pragma unroll
   for (int n = 0; n < QN; ++n) {
     const int r = it.row0 + (qw * QN + n) * 16 + li;
     const bool ok = r < it.q_rows;
     const int tt = ok ? r / a.group : 0;
-    t_of[n] = it.tok0 + tt;
-    h_of[n] = kvh * a.group + (ok ? r - tt * a.group : 0);
-    seen[n] = rows_seen(a, it, r);
-    const uint16_t* p = a.q + t_of[n] * a.q_ts + h_of[n] * a.q_hs;
-    const uint16_t* pe = S::MLA ? a.q_pe + t_of[n] * a.qp_ts + h_of[n] * a.qp_hs : nullptr;
+    const int64_t t = it.tok0 + tt, h = kvh * a.group + (ok ? r - tt * a.group : 0);
+    const uint16_t* p = a.q + t * a.q_ts + h * a.q_hs;
+    const uint16_t* pe = S::MLA ? a.q_pe + t * a.qp_ts + h * a.qp_hs : nullptr;
 #pragma unroll
     for (int k = 0; k < KK; ++k) {
       const int c = k * 4 + g;
@@ -325,6 +318,23 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
       q[n][k] = __builtin_bit_cast(bf16x8, v);
     }
   }
+
+  // A negative scale turns the queries' signs; one too small to tell scores apart
+  // counts as 0, and so do the queries then.
+  float c2 = a.scale * kLog2e;
+  const bool nothing = !(fabsf(c2) >= 1e-37f);
+  if (c2 < 0.f || nothing) {
+    const uint32_t keep = nothing ? 0u : ~0u, flip = nothing ? 0u : 0x80008000u;
+#pragma unroll
+    for (int n = 0; n < QN; ++n)
+#pragma unroll
+      for (int k = 0; k < KK; ++k) {
+        chunk_t v = __builtin_bit_cast(chunk_t, q[n][k]);
+        v = (v & keep) ^ flip;
+        q[n][k] = __builtin_bit_cast(bf16x8, v);
+      }
+  }
+  c2 = nothing ? 1.f : fabsf(c2);
 
   f32x4 o[DT][QN];
   float m[QN], l[QN];
@@ -353,23 +363,27 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
     const int j = min(share.lo + tile * S::BN + lane, it.kv_len - 1);
     if (S::BN == 64 || lane < S::BN) load_lds4((lds_ptr)(pages + tile % S::PAGES * S::BN), table + (j >> a.page_shift));
   };
-  auto load = [&](int tile) {
-    // rows past the sequence's last one repeat it; a page number outside the
-    // pool reads page 0 (see physical_row)
+  // rows past the sequence's last one repeat it; a page number outside the pool
+  // reads page 0 (see physical_row)
+  auto tile_rows = [&](int tile) {
     int page = pages[tile % S::PAGES * S::BN + (lane & (S::BN - 1))];
     if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) page = 0;
     const int j = min(share.lo + tile * S::BN + (lane & (S::BN - 1)), it.kv_len - 1);
-    const int phys = (page << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+    return (page << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+  };
+  const int row_elems = a.kv_heads * a.dim;
+  auto load_piece = [&](int i, int tile, int phys) {
     const lds_ptr dst = lds + tile % S::STAGES * S::STAGE;
-    if constexpr (S::MLA) {
-      load_mla_tile<S>(a.k_plane, phys, dst, wave, lane);
-    } else {
-      const int64_t row_elems = int64_t{a.kv_heads} * a.dim, col = int64_t{kvh} * a.dim;
-      if (live == S::ROWCH)
-        load_gqa_tile<S, false>(a.k_plane + col, a.v_plane + col, row_elems, live, phys, dst, wave, lane);
-      else
-        load_gqa_tile<S, true>(a.k_plane + col, a.v_plane + col, row_elems, live, phys, dst, wave, lane);
-    }
+    if constexpr (S::MLA) load_mla_piece<S>(i, a.k_plane, phys, dst, wave, lane);
+    else load_gqa_piece<S>(i, a.k_plane + kvh * a.dim, a.v_plane + kvh * a.dim, row_elems, live, phys, dst, wave, lane);
+  };
+  // This wave's part of a tile has landed once only the loads of `later` tiles
+  // after it are on their way: loads land in order, page numbers between them
+  // only make the wait stricter.
+  auto landed = [&](auto later, bool all_asked) {
+    constexpr int n = S::LOADS * later.value;
+    if (all_asked) __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | (n >> 4) << 14);
+    else __builtin_amdgcn_s_waitcnt(0x0F70);   // near the end there are fewer: wait for all
   };
 
   if (!S::MLA && live < S::ROWCH) {
@@ -378,82 +392,83 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   }
   for (int i = 0; i < min(2 * S::AHEAD, tiles); ++i) load_pages(i);
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-  for (int i = 0; i < min(S::AHEAD, tiles); ++i) load(i);
-
-  // this lane's byte offsets within a stage
-  int k_off[4], p_off[2], v_off[8];
-  {
-    const int r = kw * S::KVT + li;
+  for (int t = 0; t < min(S::AHEAD, tiles); ++t) {
+    const int phys = tile_rows(t);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) k_off[x] = (r * S::ROWCH + ((x * 4 + g) ^ swizzle<S::ROWCH>(r))) * 16;
-    if constexpr (S::ROWCH < 16) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) k_off[x] = (r * S::ROWCH + ((((x * 4 + g) & 7)) ^ swizzle<S::ROWCH>(r))) * 16;
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) p_off[x] = S::MAIN + (r * S::SIDE_ROWCH + ((x * 4 + g) ^ swizzle<S::SIDE_ROWCH>(r))) * 16;
-    const int vr = kw * S::KVT + 4 * g + (li >> 2);
-#pragma unroll
-    for (int x = 0; x < 8; ++x)
-      v_off[x] = S::VALUES + (vr * S::ROWCH + (((x * 2 + ((li >> 1) & 1)) & (S::ROWCH - 1)) ^ swizzle<S::ROWCH>(vr))) * 16 + (li & 1) * 8;
+    for (int i = 0; i < S::PIECES; ++i) load_piece(i, t, phys);
   }
-  const float c2 = a.scale * kLog2e;
 
+  // This lane's byte offsets within a stage, of the first chunks; the swizzle is
+  // an exclusive or, so that other chunks are one more away.
+  const int kr = kw * S::KVT + li, vr = kw * S::KVT + 4 * g + (li >> 2);
+  const int k_at = kr * S::ROWCH * 16 + ((g ^ swizzle<S::ROWCH>(kr)) << 4);
+  const int p_at = S::MAIN + kr * S::SIDE_ROWCH * 16 + ((g ^ swizzle<S::SIDE_ROWCH>(kr)) << 4);
+  const int v_at = S::VALUES + vr * S::ROWCH * 16 + ((((li >> 1) & 1) ^ swizzle<S::ROWCH>(vr)) << 4) + (li & 1) * 8;
+  static_assert(S::STAGE % 256 == 0 && S::MAIN % 256 == 0, "the low bits of an address are the lane's");
+
+  // Scores of a tile.  The operand of a step is read XD steps ahead, and `fill`
+  // puts other work between the steps' products; the fences keep the compiler
+  // from reading everything at once into registers it lacks.
+  auto scores = [&](int tile, f32x4 (&s)[KT][QN], auto&& fill) {
+    const int st = tile % S::STAGES * S::STAGE;
+    const int main = st + k_at, side = st + p_at;
+    auto chunk = [&](int kk, int k) -> bf16x8 {
+      if (S::MLA && kk >= 16) return lds_chunk(lds + (side ^ ((kk & 1) << 6)) + k * 16 * S::SIDE_ROWCH * 16);
+      if (S::ROWCH < 16) return lds_chunk(lds + (main ^ ((kk & 1) << 6)) + k * 16 * S::ROWCH * 16);
+      return lds_chunk(lds + (main ^ ((kk & 3) << 6)) + (kk >> 2) * 256 + k * 16 * S::ROWCH * 16);
+    };
+    constexpr int XD = KK < 3 ? 1 : 2;
+    bf16x8 x[XD + 1][KT];
+#pragma unroll
+    for (int kk = 0; kk < XD; ++kk)
+#pragma unroll
+      for (int k = 0; k < KT; ++k) x[kk][k] = chunk(kk, k);
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      if (kk + XD < KK)
+#pragma unroll
+        for (int k = 0; k < KT; ++k) x[(kk + XD) % (XD + 1)][k] = chunk(kk + XD, k);
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int n = 0; n < QN; ++n)
+          s[k][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[kk % (XD + 1)][k], q[n][kk],
+                                                            kk == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[k][n], 0, 0, 0);
+      fill(kk);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  f32x4 s[KT][QN];
+  if (tiles > 0) {
+    landed(std::integral_constant<int, S::AHEAD - 1>{}, tiles >= S::AHEAD);
+    __syncthreads();
+    scores(0, s, [](int) {});
+  }
   bool rows_only = false;
   for (int tile = 0; tile < tiles; ++tile) {
-    // this wave's part of the tile has landed once only the loads of the
-    // AHEAD - 1 later tiles are on their way (loads land in order; the first
-    // tiles come without page numbers between them); near the end there are
-    // fewer
-    constexpr int later = S::LOADS * (S::AHEAD - 1);
-    if (tile + S::AHEAD - 1 < tiles) __builtin_amdgcn_s_waitcnt(0x0F70 | (later & 15) | (later >> 4) << 14);
-    else __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();   // everyone's has, and the stage of the tile before is free
-    if (tile + 2 * S::AHEAD < tiles) load_pages(tile + 2 * S::AHEAD);
-    if (tile + S::AHEAD < tiles) load(tile + S::AHEAD);
-
-    const lds_ptr st = lds + tile % S::STAGES * S::STAGE;
     const int j0 = share.lo + tile * S::BN;
-    const bool whole = j0 >= full_lo && j0 + S::BN <= full_hi;
-    if (!whole) {
+    if (j0 < full_lo || j0 + S::BN > full_hi) {   // some query does not see all of the tile
       bool bad = false;
       for (int i = tid; i < S::BN * S::ROWCH; i += S::THREADS)
         bad |= not_finite(reinterpret_cast<const chunk_t*>(smem + tile % S::STAGES * S::STAGE + S::VALUES)[i]);
       rows_only = __syncthreads_or(bad);
       if (rows_only) break;
+#pragma unroll
+      for (int n = 0; n < QN; ++n) {
+        const Seen seen = rows_seen(a, it, it.row0 + (qw * QN + n) * 16 + li);
+        const int lo = seen.lo, hi = min(seen.hi, share.hi);
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = j0 + kw * S::KVT + k * 16 + g * 4 + e;
+            if (j < lo || j >= hi) s[k][n][e] = -__builtin_inff();
+          }
+      }
     }
 
-    f32x4 s[KT][QN];
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int n = 0; n < QN; ++n) s[k][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // the operand of step kk is read two steps ahead; the fences keep the
-    // compiler from reading everything at once into registers it lacks
-    auto score_chunk = [&](int kk, int k) -> bf16x8 {
-      if (S::MLA && kk >= 16) return lds_chunk(st + p_off[kk & 1] + k * 16 * S::SIDE_ROWCH * 16);
-      if (S::ROWCH < 16) return lds_chunk(st + k_off[kk & 1] + k * 16 * S::ROWCH * 16);
-      return lds_chunk(st + k_off[kk & 3] + (kk >> 2) * 256 + k * 16 * S::ROWCH * 16);
-    };
-    bf16x8 x[3][KT];
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-      for (int k = 0; k < KT; ++k) x[kk][k] = score_chunk(kk, k);
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      if (kk + 2 < KK)
-#pragma unroll
-        for (int k = 0; k < KT; ++k) x[(kk + 2) % 3][k] = score_chunk(kk + 2, k);
-#pragma unroll
-      for (int k = 0; k < KT; ++k)
-#pragma unroll
-        for (int n = 0; n < QN; ++n)
-          s[k][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[kk % 3][k], q[n][kk], s[k][n], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-
-    // softmax weights, in base 2
+    // the reference of the weights, in base 2
     float top[QN];
     bool grew = false;
 #pragma unroll
@@ -462,15 +477,8 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 #pragma unroll
       for (int k = 0; k < KT; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[k][n][e] * c2;
-          if (!whole) {
-            const int j = j0 + kw * S::KVT + k * 16 + g * 4 + e;
-            if (j < seen[n].lo || j >= seen[n].hi || j >= share.hi) x = -__builtin_inff();
-          }
-          s[k][n][e] = x;
-          top[n] = fmaxf(top[n], x);
-        }
+        for (int e = 0; e < 4; ++e) top[n] = fmaxf(top[n], s[k][n][e]);
+      top[n] *= c2;
       grew |= top[n] > m[n] + 8.f;
     }
     if constexpr (S::ACC)   // the sums stay where they are, whatever follows reads
@@ -479,7 +487,6 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 #pragma unroll
         for (int d = 0; d < DT; ++d) asm volatile("" : "+a"(o[d][n]));
     if (__any(grew)) {
-      if constexpr (S::ACC) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");   // results of the last products
 #pragma unroll
       for (int n = 0; n < QN; ++n) {
         float x = fmaxf(top[n], m[n]);
@@ -499,62 +506,123 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
         }
       }
     }
+
+    // the weights, a few at a time: value v of KT * QN * 4
+    float ref[QN];
+#pragma unroll
+    for (int n = 0; n < QN; ++n) ref[n] = m[n] == -__builtin_inff() ? 0.f : m[n];   // nothing seen yet: every weight is 0
+    constexpr int W = KT * QN * 4;
     bf16x4 p[KT][QN];
+    auto weight = [&](int v) {
+      const int k = v / 4 / QN, n = v / 4 % QN, e = v % 4;
+      s[k][n][e] = exp2_(__builtin_fmaf(s[k][n][e], c2, -ref[n]));
+      l[n] += s[k][n][e];
+      if (e == 3) p[k][n] = __builtin_convertvector(s[k][n], bf16x4);
+    };
+    f32x4 next[KT][QN];
+    if (tile + 1 < tiles) {
+      // the next tile's scores, with this one's weights between the products
+      landed(std::integral_constant<int, S::AHEAD - 2>{}, tile + S::AHEAD - 1 < tiles);
+      __syncthreads();   // all of it has landed, and the stage of the tile before this one is free
+      scores(tile + 1, next, [&](int kk) {
 #pragma unroll
-    for (int n = 0; n < QN; ++n) {
-      const float ref = m[n] == -__builtin_inff() ? 0.f : m[n];   // nothing seen yet: every weight is 0
+        for (int v = kk * W / KK; v < (kk + 1) * W / KK; ++v) weight(v);
+      });
+    } else {
 #pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        f32x4 w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = exp2_(s[k][n][e] - ref);
-          l[n] += w[e];
-        }
-        p[k][n] = __builtin_convertvector(w, bf16x4);
-      }
+      for (int v = 0; v < W; ++v) weight(v);
     }
 
-    if constexpr (KT == 1) {
-      auto column = [&](int d) { return lds_columns(st + v_off[d & 7] + (d >> 3) * 256); };
-      s16x4 y[4];
+    // the weighted values, with the loads of a later tile between the products
+    const bool more = tile + S::AHEAD < tiles;
+    int phys = 0;
+    if (more) {
+      phys = tile_rows(tile + S::AHEAD);
+      if (tile + 2 * S::AHEAD < tiles) load_pages(tile + 2 * S::AHEAD);
+    }
+    const int values = tile % S::STAGES * S::STAGE + v_at;
+    // step i: two 16-row tiles (or the only one) make one operand, rows
+    // 32 (i / DT) on, columns d = i % DT
+    constexpr int STEPS = (KT + 1) / 2 * DT, PIECES = S::PIECES;
+    using operand = std::conditional_t<KT == 1, s16x4, bf16x8>;
+    auto columns = [&](int i) -> operand {
+      const int d = i % DT;
+      const lds_ptr at = lds + (values ^ ((d & 7) << 5)) + (d >> 3) * 256 + (i / DT) * 32 * S::ROWCH * 16;
+      const s16x4 x0 = lds_columns(at);
+      if constexpr (KT == 1) {
+        return x0;
+      } else {
+        const s16x4 x1 = lds_columns(at + 16 * S::ROWCH * 16);
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+    };
+    auto weights = [&](int i, int n) -> operand {
+      if constexpr (KT == 1) return __builtin_bit_cast(s16x4, p[0][n]);
+      else return __builtin_shufflevector(p[i / DT * 2][n], p[i / DT * 2 + 1][n], 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    auto pieces = [&](int i, int steps) {   // piece x goes into step x steps / PIECES
+      if (!more) return;
 #pragma unroll
-      for (int d = 0; d < 3; ++d) y[d] = column(d);
+      for (int x = (i * PIECES + steps - 1) / steps; x < ((i + 1) * PIECES + steps - 1) / steps; ++x)
+        load_piece(x, tile + S::AHEAD, phys);
+    };
+    if constexpr (S::ACC) {
+      // Four columns and both query tiles at a time.  An operand that an ordinary
+      // instruction has just written needs two wait states, and a sum is safe to
+      // touch eight after its product: the block waits for both itself, since the
+      // compiler does not see what it holds.
+      static_assert(!S::ACC || (QN == 2 && KT == 2), "the block below");
+      bf16x8 y[2][4];
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        if (d + 3 < DT) y[(d + 3) & 3] = column(d + 3);
+      for (int e = 0; e < 4; ++e) y[0][e] = columns(e);
 #pragma unroll
-        for (int n = 0; n < QN; ++n)
-          o[d][n] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(y[d & 3], __builtin_bit_cast(s16x4, p[0][n]), o[d][n], 0, 0, 0);
+      for (int i = 0; i < STEPS; i += 4) {
+        const int b = i / 4 & 1;
+        if (i + 4 < STEPS)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[b ^ 1][e] = columns(i + 4 + e);
+        const bf16x8 w0 = weights(i, 0), w1 = weights(i, QN - 1);
+        asm volatile(
+            "s_nop 1\n\t"
+            "v_mfma_f32_16x16x32_bf16 %0, %8, %12, %0\n\t"
+            "v_mfma_f32_16x16x32_bf16 %1, %8, %13, %1\n\t"
+            "v_mfma_f32_16x16x32_bf16 %2, %9, %12, %2\n\t"
+            "v_mfma_f32_16x16x32_bf16 %3, %9, %13, %3\n\t"
+            "v_mfma_f32_16x16x32_bf16 %4, %10, %12, %4\n\t"
+            "v_mfma_f32_16x16x32_bf16 %5, %10, %13, %5\n\t"
+            "v_mfma_f32_16x16x32_bf16 %6, %11, %12, %6\n\t"
+            "v_mfma_f32_16x16x32_bf16 %7, %11, %13, %7\n\t"
+            "s_nop 9"
+            : "+a"(o[i][0]), "+a"(o[i][QN - 1]), "+a"(o[i + 1][0]), "+a"(o[i + 1][QN - 1]), "+a"(o[i + 2][0]),
+              "+a"(o[i + 2][QN - 1]), "+a"(o[i + 3][0]), "+a"(o[i + 3][QN - 1])
+            : "v"(y[b][0]), "v"(y[b][1]), "v"(y[b][2]), "v"(y[b][3]), "v"(w0), "v"(w1));
+        pieces(i / 4, STEPS / 4);
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
-      // two 16-row tiles make one operand; step i: rows k = 2 (i / DT), columns d = i % DT
-      auto columns = [&](int i) -> bf16x8 {
-        const int d = i % DT;
-        const lds_ptr at = st + v_off[d & 7] + (d >> 3) * 256 + (i / DT) * 32 * S::ROWCH * 16;
-        const s16x4 x0 = lds_columns(at), x1 = lds_columns(at + 16 * S::ROWCH * 16);
-        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
-      };
-      constexpr int STEPS = KT / 2 * DT;
-      bf16x8 y[4];
+      constexpr int YD = 3;   // operands are read this many steps ahead
+      operand y[YD + 1];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) y[i] = columns(i);
+      for (int i = 0; i < YD; ++i) y[i] = columns(i);
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        if (i + 3 < STEPS) y[(i + 3) & 3] = columns(i + 3);
-        const int k = i / DT * 2, d = i % DT;
+        if (i + YD < STEPS) y[(i + YD) % (YD + 1)] = columns(i + YD);
+        const int d = i % DT;
 #pragma unroll
         for (int n = 0; n < QN; ++n) {
-          const bf16x8 w = __builtin_shufflevector(p[k][n], p[k + 1][n], 0, 1, 2, 3, 4, 5, 6, 7);
-          if constexpr (S::ACC)   // an operand just written by an ordinary instruction needs two wait states
-            asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(o[d][n]) : "v"(y[i & 3]), "v"(w));
+          if constexpr (KT == 1)
+            o[d][n] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(y[i % (YD + 1)], weights(i, n), o[d][n], 0, 0, 0);
           else
-            o[d][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[i & 3], w, o[d][n], 0, 0, 0);
+            o[d][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[i % (YD + 1)], weights(i, n), o[d][n], 0, 0, 0);
         }
+        pieces(i, STEPS);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int n = 0; n < QN; ++n) s[k][n] = next[k][n];
   }
 
   if (rows_only) {
@@ -563,7 +631,6 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
     return;
   }
 
-  if constexpr (S::ACC) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");   // results of the last products
 #pragma unroll
   for (int n = 0; n < QN; ++n) {
     l[n] += __shfl_xor(l[n], 16);
@@ -629,8 +696,10 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 #pragma unroll
     for (int n = 0; n < QN; ++n) {
       const int row = (qw * QN + n) * 16 + li;
-      if (it.row0 + row >= it.q_rows) continue;
-      const int64_t t = t_of[n];
+      const int r = it.row0 + row;
+      if (r >= it.q_rows) continue;
+      const int tt = r / a.group, h = kvh * a.group + r - tt * a.group;
+      const int64_t t = it.tok0 + tt;
       if (shares > 1) {
         const int64_t at = (static_cast<int64_t>(it.slot) * a.kv_heads + kvh) * a.tile + row;
 #pragma unroll
@@ -645,7 +714,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
         }
       } else {
         const float inv = l[n] == 0.f ? 0.f : 1.f / l[n];
-        uint16_t* out = a.out + t * a.o_ts + h_of[n] * a.o_hs;
+        uint16_t* out = a.out + t * a.o_ts + h * a.o_hs;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           if constexpr (S::ACC) asm volatile("" : "+a"(o[d][n]));
@@ -653,7 +722,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
             *reinterpret_cast<bf16x4*>(out + d * 16 + g * 4) = __builtin_convertvector(o[d][n] * inv, bf16x4);
           __builtin_amdgcn_sched_barrier(0);
         }
-        if (a.lse && g == 0) a.lse[t * a.heads + h_of[n]] = l[n] == 0.f ? -__builtin_inff() : (m[n] + __log2f(l[n])) * kLn2;
+        if (a.lse && g == 0) a.lse[t * a.heads + h] = l[n] == 0.f ? -__builtin_inff() : (m[n] + __log2f(l[n])) * kLn2;
       }
     }
   }
@@ -678,11 +747,15 @@ hipError_t launch_shape(const AttendLaunch& a, hipStream_t s) {
 // The query rows a workgroup takes follow from how many the sequences bring.
 template <bool MLA, int DP>
 hipError_t launch_tile(const AttendLaunch& a, hipStream_t s) {
+  constexpr bool WIDE = MLA || DP > 128;   // rows of 1 KiB: tiles of 32
   switch (a.tile) {
-    case 16: return launch_shape<Shape<MLA, DP, 1, 1, MLA ? 2 : 4, MLA ? 32 : 64, MLA ? 4 : (DP > 128 ? 2 : 3)>>(a, s);
-    case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, MLA ? 32 : 64, MLA ? 4 : (DP > 128 ? 2 : 3)>>(a, s);
-    case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, MLA ? 32 : 64, MLA ? 4 : 2>>(a, s);
-    default: return launch_shape<Shape<MLA, DP, 2, 4, 1, MLA ? 32 : 64, MLA ? 3 : 2>>(a, s);
+    case 16: return launch_shape<Shape<MLA, DP, 1, 1, WIDE ? 2 : 4, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
+    case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
+    case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
+    case 128: return launch_shape<Shape<MLA, DP, 2, 4, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
+    default:
+      if constexpr (WIDE) return hipErrorInvalidValue;   // attend_tile never says so
+      else return launch_shape<Shape<MLA, DP, 2, 8, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
   }
 }
 
@@ -746,14 +819,11 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendLaunc
 }  // namespace
 
 int attend_tile(bool gqa, int dim, int64_t rows) {
-  (void)gqa;
-  (void)dim;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 || !gqa || dim > 128 ? 128 : 256;
 }
 
 int attend_groups(bool gqa, int dim, int tile) {
-  const int per_cu = !gqa || dim > 128 ? 1 : tile >= 64 ? 2 : 1;
-  return 256 * per_cu;
+  return gqa && dim <= 64 && tile < 256 ? 512 : 256;
 }
 
 hipError_t launch_attend(const AttendLaunch& a, bool gqa, hipStream_t s) {

@@ -25,9 +25,9 @@ using ll::ceil_div;
 using ll::fail;
 
 constexpr int64_t kMaxStride = int64_t{1} << 32;
-// Partial results of split tiles: query rows (times KV heads) that the step's
-// buffer holds, and shares (times KV heads) at most.
-constexpr int64_t kPartRows = 65536;
+// Partial results of split tiles: values that the step's buffer holds (128 MiB),
+// and shares (times KV heads) at most.
+constexpr int64_t kPartValues = int64_t{1} << 25;
 constexpr int64_t kMaxShares = 2048;
 
 }  // namespace
@@ -64,7 +64,9 @@ namespace {
 int64_t tiles_of(int64_t q_rows, int tile) { return ceil_div(q_rows, tile); }
 
 // Shares of split tiles that the partial results' buffer holds, per KV head.
-int64_t max_slots(const ll_step* s, int tile) { return std::min(kMaxShares, kPartRows / tile) / s->kv_heads; }
+int64_t max_slots(const ll_step* s, int tile) {
+  return std::min(kMaxShares, kPartValues / s->value_dim / tile) / s->kv_heads;
+}
 
 // How many cached rows a workgroup takes at most.  `seen` holds the rows that each
 // tile needs.  With few tiles a share is as short as the chip's workgroups allow,
@@ -267,7 +269,7 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
   const size_t o_rows = take(sizeof(int32_t) * static_cast<size_t>(d->max_tokens));
   const size_t o_tab = take(sizeof(float) * 2 * pairs * static_cast<size_t>(d->max_tokens));
   const size_t o_theta = take(sizeof(double) * pairs);
-  const size_t part_rows = static_cast<size_t>(std::min(kMaxShares * tile, kPartRows));
+  const size_t part_rows = static_cast<size_t>(std::min(kMaxShares * tile, kPartValues / s->value_dim));
   const size_t o_po = take(part_rows * s->value_dim * sizeof(float));
   const size_t o_ml = take(part_rows * 2 * sizeof(float));
   ll::DeviceGuard g(s->device);
