@@ -237,32 +237,38 @@ __device__ __forceinline__ void load_lds4(lds_ptr dst, const void* src) {
 // the physical row of the tile's row r.  A wave's part comes in S::PIECES pieces,
 // which the products of an earlier tile cover.
 template <typename S>
-__device__ __forceinline__ void load_mla_piece(int i, const uint16_t* plane, int phys, lds_ptr dst, int wave, int lane) {
+__device__ __forceinline__ void load_mla_piece(int i, uint64_t row, lds_ptr dst, int wave, int lane) {
+  const uint32_t lo = static_cast<uint32_t>(row), hi = static_cast<uint32_t>(row >> 32);
   if (i < S::BN / S::WAVES) {   // a row's latent part
     const int r = i * S::WAVES + wave;
-    const int64_t row = __builtin_amdgcn_readlane(phys, r);
-    load_lds(dst + r * 1024, plane + row * kRowElems, static_cast<uint32_t>(lane ^ swizzle<64>(r)) * 16);
+    // (a lane's value comes back signed: without the casts its top bit would
+    // spread over the upper half)
+    const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r))) << 32 |
+                        static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, r));
+    load_lds(dst + r * 1024, reinterpret_cast<const void*>(at), static_cast<uint32_t>(lane ^ swizzle<64>(r)) * 16);
   } else {                      // 8 rows' k_pe
     const int b = (i - S::BN / S::WAVES) * S::WAVES + wave;
     if (S::BN / 8 % S::WAVES != 0 && b >= S::BN / 8) return;
     const int r = b * 8 + (lane >> 3);
-    load_lds(dst + S::MAIN + b * 1024,
-             plane + int64_t{__shfl(phys, r)} * kRowElems + kKvLoraRank + ((lane & 7) ^ swizzle<8>(r)) * 8);
+    const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__shfl(hi, r))) << 32 | static_cast<uint32_t>(__shfl(lo, r));
+    load_lds(dst + S::MAIN + b * 1024, reinterpret_cast<const void*>(at + kKvLoraRank * 2 + ((lane & 7) ^ swizzle<8>(r)) * 16));
   }
 }
-// K and V of one KV head (k and v: its first value in row 0); chunks past `live`
-// are left alone (they were zeroed once).
+// K and V of one KV head (k and v: its first value in row 0; row: the byte
+// offset); chunks past `live` are left alone (they were zeroed once).
 template <typename S>
-__device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const uint16_t* v, int row_elems, int live,
-                                               int phys, lds_ptr dst, int wave, int lane) {
+__device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const uint16_t* v, int live, uint64_t row,
+                                               lds_ptr dst, int wave, int lane) {
   const int b = i * S::WAVES + wave;
   const int place = b * 64 + lane;
   const int r = place / S::ROWCH;
   const int c = (place % S::ROWCH) ^ swizzle<S::ROWCH>(r);
-  const int64_t off = int64_t{__shfl(phys, r)} * row_elems + c * 8;
+  const uint32_t lo = static_cast<uint32_t>(row), hi = static_cast<uint32_t>(row >> 32);
+  const uint64_t off = (static_cast<uint64_t>(static_cast<uint32_t>(__shfl(hi, r))) << 32 |
+                        static_cast<uint32_t>(__shfl(lo, r))) + c * 16;
   if (c < live) {
-    load_lds(dst + b * 1024, k + off);
-    load_lds(dst + S::MAIN + b * 1024, v + off);
+    load_lds(dst + b * 1024, reinterpret_cast<const char*>(k) + off);
+    load_lds(dst + S::MAIN + b * 1024, reinterpret_cast<const char*>(v) + off);
   }
 }
 
@@ -365,17 +371,18 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   };
   // rows past the sequence's last one repeat it; a page number outside the pool
   // reads page 0 (see physical_row)
-  auto tile_rows = [&](int tile) {
+  const uint32_t row_bytes = S::MLA ? kRowBytes : a.kv_heads * a.dim * 2;
+  auto tile_rows = [&](int tile) -> uint64_t {   // MLA: the row's address; GQA: its offset in a plane
     int page = pages[tile % S::PAGES * S::BN + (lane & (S::BN - 1))];
     if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) page = 0;
     const int j = min(share.lo + tile * S::BN + (lane & (S::BN - 1)), it.kv_len - 1);
-    return (page << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+    const uint32_t row = (page << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+    return static_cast<uint64_t>(row) * row_bytes + (S::MLA ? reinterpret_cast<uint64_t>(a.k_plane) : 0);
   };
-  const int row_elems = a.kv_heads * a.dim;
-  auto load_piece = [&](int i, int tile, int phys) {
+  auto load_piece = [&](int i, int tile, uint64_t row) {
     const lds_ptr dst = lds + tile % S::STAGES * S::STAGE;
-    if constexpr (S::MLA) load_mla_piece<S>(i, a.k_plane, phys, dst, wave, lane);
-    else load_gqa_piece<S>(i, a.k_plane + kvh * a.dim, a.v_plane + kvh * a.dim, row_elems, live, phys, dst, wave, lane);
+    if constexpr (S::MLA) load_mla_piece<S>(i, row, dst, wave, lane);
+    else load_gqa_piece<S>(i, a.k_plane + kvh * a.dim, a.v_plane + kvh * a.dim, live, row, dst, wave, lane);
   };
   // This wave's part of a tile has landed once only the loads of `later` tiles
   // after it are on their way: loads land in order, page numbers between them
@@ -393,9 +400,9 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   for (int i = 0; i < min(2 * S::AHEAD, tiles); ++i) load_pages(i);
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
   for (int t = 0; t < min(S::AHEAD, tiles); ++t) {
-    const int phys = tile_rows(t);
+    const uint64_t row = tile_rows(t);
 #pragma unroll
-    for (int i = 0; i < S::PIECES; ++i) load_piece(i, t, phys);
+    for (int i = 0; i < S::PIECES; ++i) load_piece(i, t, row);
   }
 
   // This lane's byte offsets within a stage, of the first chunks; the swizzle is
@@ -425,17 +432,16 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
       for (int k = 0; k < KT; ++k) x[kk][k] = chunk(kk, k);
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
-      if (kk + XD < KK)
-#pragma unroll
-        for (int k = 0; k < KT; ++k) x[(kk + XD) % (XD + 1)][k] = chunk(kk + XD, k);
 #pragma unroll
       for (int k = 0; k < KT; ++k)
 #pragma unroll
-        for (int n = 0; n < QN; ++n)
+        for (int n = 0; n < QN; ++n) {
+          if (n == 0 && kk + XD < KK) x[(kk + XD) % (XD + 1)][k] = chunk(kk + XD, k);
           s[k][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[kk % (XD + 1)][k], q[n][kk],
                                                             kk == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[k][n], 0, 0, 0);
-      fill(kk);
-      __builtin_amdgcn_sched_barrier(0);
+          fill((kk * KT + k) * QN + n);
+          __builtin_amdgcn_sched_barrier(0);
+        }
     }
   };
 
@@ -524,9 +530,10 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
       // the next tile's scores, with this one's weights between the products
       landed(std::integral_constant<int, S::AHEAD - 2>{}, tile + S::AHEAD - 1 < tiles);
       __syncthreads();   // all of it has landed, and the stage of the tile before this one is free
-      scores(tile + 1, next, [&](int kk) {
+      scores(tile + 1, next, [&](int i) {
+        constexpr int PRODUCTS = KK * KT * QN;
 #pragma unroll
-        for (int v = kk * W / KK; v < (kk + 1) * W / KK; ++v) weight(v);
+        for (int v = i * W / PRODUCTS; v < (i + 1) * W / PRODUCTS; ++v) weight(v);
       });
     } else {
 #pragma unroll
@@ -535,9 +542,9 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 
     // the weighted values, with the loads of a later tile between the products
     const bool more = tile + S::AHEAD < tiles;
-    int phys = 0;
+    uint64_t row = 0;
     if (more) {
-      phys = tile_rows(tile + S::AHEAD);
+      row = tile_rows(tile + S::AHEAD);
       if (tile + 2 * S::AHEAD < tiles) load_pages(tile + 2 * S::AHEAD);
     }
     const int values = tile % S::STAGES * S::STAGE + v_at;
@@ -564,7 +571,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
       if (!more) return;
 #pragma unroll
       for (int x = (i * PIECES + steps - 1) / steps; x < ((i + 1) * PIECES + steps - 1) / steps; ++x)
-        load_piece(x, tile + S::AHEAD, phys);
+        load_piece(x, tile + S::AHEAD, row);
     };
     if constexpr (S::ACC) {
       // Four columns and both query tiles at a time.  An operand that an ordinary
@@ -592,7 +599,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
             "v_mfma_f32_16x16x32_bf16 %5, %10, %13, %5\n\t"
             "v_mfma_f32_16x16x32_bf16 %6, %11, %12, %6\n\t"
             "v_mfma_f32_16x16x32_bf16 %7, %11, %13, %7\n\t"
-            "s_nop 9"
+            "s_nop 7"
             : "+a"(o[i][0]), "+a"(o[i][QN - 1]), "+a"(o[i + 1][0]), "+a"(o[i + 1][QN - 1]), "+a"(o[i + 2][0]),
               "+a"(o[i + 2][QN - 1]), "+a"(o[i + 3][0]), "+a"(o[i + 3][QN - 1])
             : "v"(y[b][0]), "v"(y[b][1]), "v"(y[b][2]), "v"(y[b][3]), "v"(w0), "v"(w1));
@@ -749,9 +756,9 @@ template <bool MLA, int DP>
 hipError_t launch_tile(const AttendLaunch& a, hipStream_t s) {
   constexpr bool WIDE = MLA || DP > 128;   // rows of 1 KiB: tiles of 32
   switch (a.tile) {
-    case 16: return launch_shape<Shape<MLA, DP, 1, 1, WIDE ? 2 : 4, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
-    case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
-    case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
+    case 16: return launch_shape<Shape<MLA, DP, 1, 1, WIDE ? 2 : 4, WIDE ? 32 : 64, 4>>(a, s);
+    case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, WIDE ? 32 : 64, 4>>(a, s);
+    case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, WIDE ? 32 : 64, 4>>(a, s);
     case 128: return launch_shape<Shape<MLA, DP, 2, 4, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
     default:
       if constexpr (WIDE) return hipErrorInvalidValue;   // attend_tile never says so
