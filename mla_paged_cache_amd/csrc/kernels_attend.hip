@@ -175,22 +175,22 @@ __device__ __forceinline__ s16x4 lds_columns(lds_ptr p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4*>(p));
 }
 
-__device__ __forceinline__ bool not_finite(chunk_t c) {
-  bool bad = false;
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    bad |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
-  return bad;
+// Bits kNotFinite of the result are set where one of the chunk's values has all
+// exponent bits set: one more in its lowest exponent bit then reaches the sign's.
+constexpr uint32_t kNotFinite = 0x80008000u;
+__device__ __forceinline__ uint32_t exponents(chunk_t c) {
+  const chunk_t e = (c & 0x7F807F80u) + 0x00800080u;
+  return e.x | e.y | e.z | e.w;
 }
 
 // How a workgroup does one item: QW waves side by side over the query rows (QN
-// tiles of 16 each), KW over the cached rows of a tile of BN.
-template <bool MLA_, int DP, int QN_, int QW_, int KW_, int BN_, int STAGES_>
+// tiles of 16 each), KW over the cached rows of a tile of BN, DW over the columns
+// of the values (each of these computes the scores for itself).
+template <bool MLA_, int DP, int QN_, int QW_, int KW_, int DW_, int BN_, int STAGES_>
 struct Shape {
   static constexpr bool MLA = MLA_;
-  static constexpr int QN = QN_, QW = QW_, KW = KW_, BN = BN_;
-  static constexpr int WAVES = QW * KW, THREADS = 64 * WAVES;
+  static constexpr int QN = QN_, QW = QW_, KW = KW_, DW = DW_, BN = BN_;
+  static constexpr int WAVES = QW * KW * DW, THREADS = 64 * WAVES;
   static constexpr int DK = MLA ? kRowElems : DP, DV = MLA ? kKvLoraRank : DP;
   static constexpr int ROWCH = DV / 8;                       // chunks of a row of the main region
   static constexpr int MAIN = BN * DV * 2;                   // MLA: latent part; GQA: K
@@ -292,13 +292,13 @@ __device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const u
 template <typename S>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::WAVES > 4 ? 2 : 1))) void attend_kernel(AttendLaunch a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  constexpr int QN = S::QN, KT = S::KVT / 16, DT = S::DV / 16, KK = S::DK / 32;
+  constexpr int QN = S::QN, KT = S::KVT / 16, DT = S::DV / S::DW / 16, KK = S::DK / 32;
   const int kvh = blockIdx.x % a.kv_heads;
   const int item = blockIdx.x / a.kv_heads;
+  const AttendItem it = a.items[item];   // asked for together with the count
   if (item >= a.counts->items) return;
-  const AttendItem it = a.items[item];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int qw = wave % S::QW, kw = wave / S::QW;
+  const int qw = wave % S::QW, kw = wave / S::QW % S::KW, dw = wave / (S::QW * S::KW);
   const int li = lane & 15, g = lane >> 4;
   const Seen share = item_share(a, it, S::BN);
   const lds_ptr lds = (lds_ptr)smem;
@@ -410,7 +410,9 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   const int kr = kw * S::KVT + li, vr = kw * S::KVT + 4 * g + (li >> 2);
   const int k_at = kr * S::ROWCH * 16 + ((g ^ swizzle<S::ROWCH>(kr)) << 4);
   const int p_at = S::MAIN + kr * S::SIDE_ROWCH * 16 + ((g ^ swizzle<S::SIDE_ROWCH>(kr)) << 4);
-  const int v_at = S::VALUES + vr * S::ROWCH * 16 + ((((li >> 1) & 1) ^ swizzle<S::ROWCH>(vr)) << 4) + (li & 1) * 8;
+  const int vc = dw * (S::ROWCH / S::DW);   // this wave's first chunk of the values
+  const int v_at = S::VALUES + vr * S::ROWCH * 16 + (vc >> 4) * 256 +
+                   ((((vc & 15) | ((li >> 1) & 1)) ^ swizzle<S::ROWCH>(vr)) << 4) + (li & 1) * 8;
   static_assert(S::STAGE % 256 == 0 && S::MAIN % 256 == 0, "the low bits of an address are the lane's");
 
   // Scores of a tile.  The operand of a step is read XD steps ahead, and `fill`
@@ -455,10 +457,11 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   for (int tile = 0; tile < tiles; ++tile) {
     const int j0 = share.lo + tile * S::BN;
     if (j0 < full_lo || j0 + S::BN > full_hi) {   // some query does not see all of the tile
-      bool bad = false;
+      uint32_t bits = 0;
+#pragma unroll 8
       for (int i = tid; i < S::BN * S::ROWCH; i += S::THREADS)
-        bad |= not_finite(reinterpret_cast<const chunk_t*>(smem + tile % S::STAGES * S::STAGE + S::VALUES)[i]);
-      rows_only = __syncthreads_or(bad);
+        bits |= exponents(reinterpret_cast<const chunk_t*>(smem + tile % S::STAGES * S::STAGE + S::VALUES)[i]);
+      rows_only = __syncthreads_or((bits & kNotFinite) != 0);
       if (rows_only) break;
 #pragma unroll
       for (int n = 0; n < QN; ++n) {
@@ -599,7 +602,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
             "v_mfma_f32_16x16x32_bf16 %5, %10, %13, %5\n\t"
             "v_mfma_f32_16x16x32_bf16 %6, %11, %12, %6\n\t"
             "v_mfma_f32_16x16x32_bf16 %7, %11, %13, %7\n\t"
-            "s_nop 7"
+            "s_nop 9"
             : "+a"(o[i][0]), "+a"(o[i][QN - 1]), "+a"(o[i + 1][0]), "+a"(o[i + 1][QN - 1]), "+a"(o[i + 2][0]),
               "+a"(o[i + 2][QN - 1]), "+a"(o[i + 3][0]), "+a"(o[i + 3][QN - 1])
             : "v"(y[b][0]), "v"(y[b][1]), "v"(y[b][2]), "v"(y[b][3]), "v"(w0), "v"(w1));
@@ -648,7 +651,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   if constexpr (S::KW > 1) {
     // the waves' sums over their own cached rows, put together in LDS
     __shared__ float s_m[S::WAVES][16 * QN], s_l[S::WAVES][16 * QN];
-    constexpr int OUT_ROWS = 16 * QN * S::QW;
+    constexpr int OUT_ROWS = 16 * QN * S::QW;   // m and l are the same in the DW waves of a row: the first ones' count
     static_assert(S::KW * OUT_ROWS * S::DV * 4 <= S::STAGES * S::STAGE, "the sums fit where the tiles were");
     __syncthreads();   // the tiles are no longer read
     float* sums = reinterpret_cast<float*>(smem);
@@ -663,7 +666,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         // 16-byte chunks rotated by the row, against bank conflicts
-        const int row = (qw * QN + n) * 16 + li, ch = ((d * 4 + g) + row) % (S::DV / 4);
+        const int row = (qw * QN + n) * 16 + li, ch = ((dw * DT + d) * 4 + g + row) % (S::DV / 4);
         *reinterpret_cast<f32x4*>(sums + (kw * OUT_ROWS + row) * S::DV + ch * 4) = o[d][n];
       }
     __syncthreads();
@@ -703,7 +706,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 #pragma unroll
     for (int n = 0; n < QN; ++n) {
       const int row = (qw * QN + n) * 16 + li;
-      const int r = it.row0 + row;
+      const int r = it.row0 + row, col = dw * (S::DV / S::DW) + g * 4;
       if (r >= it.q_rows) continue;
       const int tt = r / a.group, h = kvh * a.group + r - tt * a.group;
       const int64_t t = it.tok0 + tt;
@@ -712,10 +715,10 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           if constexpr (S::ACC) asm volatile("" : "+a"(o[d][n]));
-          if (d * 16 + g * 4 < dv) *reinterpret_cast<f32x4*>(a.part_o + at * dv + d * 16 + g * 4) = o[d][n];
+          if (col + d * 16 < dv) *reinterpret_cast<f32x4*>(a.part_o + at * dv + col + d * 16) = o[d][n];
           __builtin_amdgcn_sched_barrier(0);
         }
-        if (g == 0) {
+        if (col == 0) {
           a.part_ml[at * 2] = m[n];
           a.part_ml[at * 2 + 1] = l[n];
         }
@@ -725,11 +728,11 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           if constexpr (S::ACC) asm volatile("" : "+a"(o[d][n]));
-          if (d * 16 + g * 4 < dv)
-            *reinterpret_cast<bf16x4*>(out + d * 16 + g * 4) = __builtin_convertvector(o[d][n] * inv, bf16x4);
+          if (col + d * 16 < dv)
+            *reinterpret_cast<bf16x4*>(out + col + d * 16) = __builtin_convertvector(o[d][n] * inv, bf16x4);
           __builtin_amdgcn_sched_barrier(0);
         }
-        if (a.lse && g == 0) a.lse[t * a.heads + h] = l[n] == 0.f ? -__builtin_inff() : (m[n] + __log2f(l[n])) * kLn2;
+        if (a.lse && col == 0) a.lse[t * a.heads + h] = l[n] == 0.f ? -__builtin_inff() : (m[n] + __log2f(l[n])) * kLn2;
       }
     }
   }
@@ -756,13 +759,13 @@ template <bool MLA, int DP>
 hipError_t launch_tile(const AttendLaunch& a, hipStream_t s) {
   constexpr bool WIDE = MLA || DP > 128;   // rows of 1 KiB: tiles of 32
   switch (a.tile) {
-    case 16: return launch_shape<Shape<MLA, DP, 1, 1, WIDE ? 2 : 4, WIDE ? 32 : 64, 4>>(a, s);
-    case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, WIDE ? 32 : 64, 4>>(a, s);
-    case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, WIDE ? 32 : 64, 4>>(a, s);
-    case 128: return launch_shape<Shape<MLA, DP, 2, 4, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
+    case 16: return launch_shape<Shape<MLA, DP, 1, 1, WIDE ? 2 : 4, MLA ? 2 : 1, WIDE ? 32 : 64, 4>>(a, s);
+    case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, MLA ? 2 : 1, WIDE ? 32 : 64, 4>>(a, s);
+    case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, MLA ? 2 : 1, WIDE ? 32 : 64, 4>>(a, s);
+    case 128: return launch_shape<Shape<MLA, DP, 2, 4, 1, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
     default:
       if constexpr (WIDE) return hipErrorInvalidValue;   // attend_tile never says so
-      else return launch_shape<Shape<MLA, DP, 2, 8, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
+      else return launch_shape<Shape<MLA, DP, 2, 8, 1, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
   }
 }
 

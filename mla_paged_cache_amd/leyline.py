@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -127,47 +128,9 @@ class _StepDesc(ctypes.Structure):
     ]
 
 
-class _AppendDesc(ctypes.Structure):
-    _fields_ = [
-        ("tokens", ctypes.c_int64),
-        ("layer", ctypes.c_int32),
-        ("norm_type", ctypes.c_int32),
-        ("a", ctypes.c_void_p),
-        ("a_token_stride", ctypes.c_int64),
-        ("a_head_stride", ctypes.c_int64),
-        ("b", ctypes.c_void_p),
-        ("b_token_stride", ctypes.c_int64),
-        ("b_head_stride", ctypes.c_int64),
-        ("norm", ctypes.c_void_p),
-        ("q", ctypes.c_void_p),
-        ("q_token_stride", ctypes.c_int64),
-        ("q_head_stride", ctypes.c_int64),
-        ("q_out", ctypes.c_void_p),
-        ("q_out_token_stride", ctypes.c_int64),
-        ("q_out_head_stride", ctypes.c_int64),
-        ("q_norm", ctypes.c_void_p),
-        ("eps", ctypes.c_float),
-    ]
-
-
-class _AttendDesc(ctypes.Structure):
-    _fields_ = [
-        ("tokens", ctypes.c_int64),
-        ("layer", ctypes.c_int32),
-        ("causal", ctypes.c_int32),
-        ("window", ctypes.c_int64),
-        ("scale", ctypes.c_float),
-        ("q", ctypes.c_void_p),
-        ("q_token_stride", ctypes.c_int64),
-        ("q_head_stride", ctypes.c_int64),
-        ("q_pe", ctypes.c_void_p),
-        ("q_pe_token_stride", ctypes.c_int64),
-        ("q_pe_head_stride", ctypes.c_int64),
-        ("out", ctypes.c_void_p),
-        ("out_token_stride", ctypes.c_int64),
-        ("out_head_stride", ctypes.c_int64),
-        ("lse", ctypes.c_void_p),
-    ]
+# ll_append_desc and ll_attend_desc, packed in their C layout
+_APPEND_DESC = struct.Struct("@qii Pqq Pqq P Pqq Pqq P f4x")
+_ATTEND_DESC = struct.Struct("@qiiq f4x Pqq Pqq Pqq P")
 
 
 def _load():
@@ -207,8 +170,8 @@ def _load():
         "ll_step_create": (i32, [vp, P(_StepDesc), P(vp)]),
         "ll_step_destroy": (None, [vp]),
         "ll_step_begin": (i32, [vp, vp, vp, i32, i32, vp]),
-        "ll_step_append": (i32, [vp, P(_AppendDesc), vp]),
-        "ll_step_attend": (i32, [vp, P(_AttendDesc), vp]),
+        "ll_step_append": (i32, [vp, vp, vp]),
+        "ll_step_attend": (i32, [vp, vp, vp]),
         "ll_last_error": (ctypes.c_char_p, []),
         "ll_status_str": (ctypes.c_char_p, [i32]),
     }
@@ -705,6 +668,7 @@ class Step:
     the other strides are multiples of 8 values and the data is 16-byte aligned."""
 
     def __init__(self, pool: Pool, heads: int, max_seqs: int, max_tokens: int):
+        import torch
         d = _StepDesc(int(heads), int(max_seqs), int(max_tokens))
         h = ctypes.c_void_p()
         _check(_lib.ll_step_create(pool._h, ctypes.byref(d), ctypes.byref(h)))
@@ -713,8 +677,15 @@ class Step:
         self.gqa, self.heads, self.max_seqs, self.max_tokens = pool.gqa, int(heads), int(max_seqs), int(max_tokens)
         self.device, self._dev = pool.device, pool._dev
         self.tokens = 0
-        # widths of a query as attend takes it, of its rotated part, of a result
-        self._dq, self._dr, self._dv = (pool.head_dim,) * 3 if pool.gqa else (ROW, ROPE_DIM, KV_LORA_RANK)
+        # widths of a result and of a query's rotated part (append), and the axes
+        # behind the tokens of every tensor that append and attend take
+        self._dv, self._dr = (pool.head_dim,) * 2 if pool.gqa else (KV_LORA_RANK, ROPE_DIM)
+        self._a_tail = (pool.heads, pool.head_dim) if pool.gqa else (KV_LORA_RANK,)
+        self._b_tail = (pool.heads, pool.head_dim) if pool.gqa else (ROPE_DIM,)
+        self._q_tail, self._r_tail, self._o_tail = (self.heads, ROW), (self.heads, self._dr), (self.heads, self._dv)
+        self._l_tail = (self.heads,)
+        self._torch, self._bf16, self._f32 = torch, torch.bfloat16, torch.float32
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: _stream_handle(None, d))
 
     def close(self):
         if getattr(self, "_h", None):
@@ -740,19 +711,18 @@ class Step:
         self.tokens = int(c_arr.sum())
         return self.tokens
 
-    def _rows(self, t, name: str, *tail, dtype=None):
+    def _rows(self, t, name: str, tail, dtype):
         """Token count of a [tokens][*tail] tensor on the pool's device."""
-        import torch
-        if not isinstance(t, torch.Tensor) or t.dtype != (dtype or torch.bfloat16) or t.device != self.device \
-                or t.dim() != 1 + len(tail) or tuple(t.shape[1:]) != tail or t.stride(-1) != 1:
-            raise ValueError(f"{name}: need a {dtype or torch.bfloat16} tensor [tokens]{list(tail)} on {self.device} "
-                             f"with a dense last axis")
+        try:
+            ok = t.dtype is dtype and t.shape[1:] == tail and t.device == self.device and t.stride(-1) == 1
+        except (AttributeError, IndexError):   # no tensor, or one without axes
+            ok = False
+        if not ok:
+            raise ValueError(f"{name}: need a {dtype} tensor [tokens]{list(tail)} on {self.device} with a dense last axis")
         return t.shape[0]
 
     def _weight(self, w, name: str, n: int):
-        import torch
-        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.bfloat16, torch.float32) or w.device != self.device \
-                or tuple(w.shape) != (n,) or w.stride(0) != 1:
+        if w.dtype not in (self._bf16, self._f32) or w.shape != (n,) or w.device != self.device or w.stride(0) != 1:
             raise ValueError(f"{name}: need a dense bf16 or float32 tensor [{n}] on {self.device}")
         return w.data_ptr()
 
@@ -765,41 +735,46 @@ class Step:
         [T][heads][head_dim].  norm / q_norm: RMS-norm weights (bf16 or float32) of
         c_kv or the K heads / the query heads (GQA).  Returns q_out (new when not
         given; q itself turns the queries in place), or None without q."""
-        import torch
-        d = _AppendDesc(layer=int(layer), eps=eps)
-        rows = []
-        if (a is None) != (b is None):
-            raise ValueError("a and b go together")
-        if a is not None:
-            if self.gqa:
-                shape = (self._pool.heads, self._pool.head_dim)
-                rows += [self._rows(a, "a", *shape), self._rows(b, "b", *shape)]
-                d.a_token_stride, d.a_head_stride, _ = a.stride()
-                d.b_token_stride, d.b_head_stride, _ = b.stride()
+        bf16, gqa = self._bf16, self.gqa
+        room = 1 << 62
+        a_ptr = a_ts = a_hs = b_ptr = b_ts = b_hs = 0
+        if a is not None and b is not None:
+            room = min(self._rows(a, "a", self._a_tail, bf16), self._rows(b, "b", self._b_tail, bf16))
+            a_ptr, b_ptr = a.data_ptr(), b.data_ptr()
+            if gqa:
+                a_ts, a_hs, _ = a.stride()
+                b_ts, b_hs, _ = b.stride()
             else:
-                rows += [self._rows(a, "a", KV_LORA_RANK), self._rows(b, "b", ROPE_DIM)]
-                d.a_token_stride, d.b_token_stride = a.stride(0), b.stride(0)
-            d.a, d.b = a.data_ptr(), b.data_ptr()
+                a_ts, b_ts = a.stride(0), b.stride(0)
+        elif a is not None or b is not None:
+            raise ValueError("a and b go together")
+        norm_ptr = qn_ptr = f32 = 0
         if norm is not None:
-            d.norm = self._weight(norm, "norm", self._dv)
-            d.norm_type = 1 if norm.dtype == torch.float32 else 0
+            norm_ptr = self._weight(norm, "norm", self._dv)
+            f32 = 1 if norm.dtype is self._f32 else 0
+        q_ptr = q_ts = q_hs = o_ptr = o_ts = o_hs = 0
         if q is not None:
-            rows.append(self._rows(q, "q", self.heads, self._dr))
+            room = min(room, self._rows(q, "q", self._r_tail, bf16))
+            q_ptr = q.data_ptr()
+            q_ts, q_hs, _ = q.stride()
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            rows.append(self._rows(q_out, "q_out", self.heads, self._dr))
-            d.q, d.q_out = q.data_ptr(), q_out.data_ptr()
-            d.q_token_stride, d.q_head_stride, _ = q.stride()
-            d.q_out_token_stride, d.q_out_head_stride, _ = q_out.stride()
+                q_out = self._torch.empty(q.shape, dtype=bf16, device=self.device)
+            elif q_out is not q:
+                room = min(room, self._rows(q_out, "q_out", self._r_tail, bf16))
+            o_ptr = q_out.data_ptr()
+            o_ts, o_hs, _ = q_out.stride()
             if q_norm is not None:
-                d.q_norm = self._weight(q_norm, "q_norm", self._dr)
-                if norm is not None and q_norm.dtype != norm.dtype:
+                qn_ptr = self._weight(q_norm, "q_norm", self._dr)
+                if norm is not None and q_norm.dtype is not norm.dtype:
                     raise ValueError("norm and q_norm must have one dtype")
-                d.norm_type = 1 if q_norm.dtype == torch.float32 else 0
+                f32 = 1 if q_norm.dtype is self._f32 else 0
         elif q_out is not None or q_norm is not None:
             raise ValueError("q_out and q_norm need q")
-        d.tokens = min(rows) if rows else self.max_tokens
-        _check(_lib.ll_step_append(self._h, ctypes.byref(d), _stream_handle(stream, self._dev)))
+        desc = _APPEND_DESC.pack(room, layer, f32, a_ptr, a_ts, a_hs, b_ptr, b_ts, b_hs, norm_ptr, q_ptr, q_ts, q_hs,
+                                 o_ptr, o_ts, o_hs, qn_ptr, eps)
+        rc = _lib.ll_step_append(self._h, desc, self._raw_stream(self._dev) if stream is None else stream.cuda_stream)
+        if rc:
+            _check(rc)
         return q_out
 
     def attend(self, layer: int, q, q_pe=None, scale: float | None = None, causal: bool = True, window: int = 0,
@@ -812,39 +787,43 @@ class Step:
         [T][heads][head_dim], scale defaults to head_dim ** -0.5.  window > 0: a
         token sees the last `window` rows up to its own.  lse=True (or a dense
         float32 tensor [T][heads]) also returns the log sum exp: (out, lse)."""
-        import torch
-        d = _AttendDesc(layer=int(layer), causal=1 if causal else 0, window=int(window))
+        bf16 = self._bf16
         if scale is None:
             if not self.gqa:
                 raise ValueError("scale must be given: the latent width does not say the model's head width")
-            scale = self._dq ** -0.5
-        d.scale = scale
+            scale = self._dv ** -0.5
+        p_ptr = p_ts = p_hs = 0
         if self.gqa:
             if q_pe is not None:
                 raise ValueError("q_pe is for MLA pools only")
-            rows = self._rows(q, "q", self.heads, self._dq)
+            room = self._rows(q, "q", self._o_tail, bf16)
         elif q_pe is None:
-            rows = self._rows(q, "q", self.heads, ROW)
-            d.q_pe = q.data_ptr() + 2 * KV_LORA_RANK
-            d.q_pe_token_stride, d.q_pe_head_stride, _ = q.stride()
+            room = self._rows(q, "q", self._q_tail, bf16)
+            p_ptr = q.data_ptr() + 2 * KV_LORA_RANK
+            p_ts, p_hs, _ = q.stride()
         else:
-            rows = min(self._rows(q, "q", self.heads, KV_LORA_RANK), self._rows(q_pe, "q_pe", self.heads, ROPE_DIM))
-            d.q_pe = q_pe.data_ptr()
-            d.q_pe_token_stride, d.q_pe_head_stride, _ = q_pe.stride()
-        d.q = q.data_ptr()
-        d.q_token_stride, d.q_head_stride, _ = q.stride()
+            room = min(self._rows(q, "q", self._o_tail, bf16), self._rows(q_pe, "q_pe", self._r_tail, bf16))
+            p_ptr = q_pe.data_ptr()
+            p_ts, p_hs, _ = q_pe.stride()
+        q_ts, q_hs, _ = q.stride()
         if out is None:
-            out = torch.empty((q.shape[0], self.heads, self._dv), dtype=q.dtype, device=q.device)
-        rows = min(rows, self._rows(out, "out", self.heads, self._dv))
-        d.out = out.data_ptr()
-        d.out_token_stride, d.out_head_stride, _ = out.stride()
+            out = self._torch.empty((q.shape[0], *self._o_tail), dtype=bf16, device=self.device)
+        else:
+            room = min(room, self._rows(out, "out", self._o_tail, bf16))
+        o_ts, o_hs, _ = out.stride()
+        l_ptr = 0
         if lse is True:
-            lse = torch.empty((q.shape[0], self.heads), dtype=torch.float32, device=q.device)
+            lse = self._torch.empty((q.shape[0], self.heads), dtype=self._f32, device=self.device)
         if lse is not None and lse is not False:
-            rows = min(rows, self._rows(lse, "lse", self.heads, dtype=torch.float32))
+            room = min(room, self._rows(lse, "lse", self._l_tail, self._f32))
             if not lse.is_contiguous():
                 raise ValueError("lse must be contiguous")
-            d.lse = lse.data_ptr()
-        d.tokens = rows
-        _check(_lib.ll_step_attend(self._h, ctypes.byref(d), _stream_handle(stream, self._dev)))
-        return out if d.lse is None else (out, lse)
+            l_ptr = lse.data_ptr()
+        else:
+            lse = None
+        desc = _ATTEND_DESC.pack(room, layer, 1 if causal else 0, window, scale, q.data_ptr(), q_ts, q_hs, p_ptr, p_ts, p_hs,
+                                 out.data_ptr(), o_ts, o_hs, l_ptr)
+        rc = _lib.ll_step_attend(self._h, desc, self._raw_stream(self._dev) if stream is None else stream.cuda_stream)
+        if rc:
+            _check(rc)
+        return out if lse is None else (out, lse)
