@@ -115,16 +115,9 @@ int64_t pick_share(const ll_step* s, const std::vector<int64_t>& seen, int64_t g
   return best;
 }
 
-// The attention's items.  A sequence's query rows come in tiles; a tile that needs
-// more cached rows than a share is split over several workgroups, whose items
-// come before the whole ones'.  Returns their number.
-//
-// Order: workgroup b runs on chip b % 8 (each with its own L2 cache), and item i
-// of KV head h is workgroup i * kv_heads + h, so items of one class i % (8 /
-// gcd(8, kv_heads)) always meet the same caches.  Tiles of one sequence and share
-// read the same cached rows, at about the same time when they run side by side:
-// such groups are kept in one class as far as the classes' work stays even, and
-// each class runs its longest items first.
+// The attention's items: every sequence's query rows in tiles, the longest first;
+// a tile that needs more cached rows than a share is split over several
+// workgroups.  Shares of split tiles come before the others.
 int64_t plan_items(const ll_step* s, const std::vector<ll::StepSeq>& seqs, std::vector<ll::AttendItem>* out) {
   struct Tile {
     int64_t seen;
@@ -141,87 +134,27 @@ int64_t plan_items(const ll_step* s, const std::vector<ll::StepSeq>& seqs, std::
       tiles.push_back(Tile{seen.back(), static_cast<int32_t>(i), static_cast<int32_t>(k)});
     }
   }
+  std::stable_sort(tiles.begin(), tiles.end(), [](const Tile& a, const Tile& b) { return a.seen > b.seen; });
   const int64_t share = pick_share(s, seen, ll::attend_groups(s->pool->gqa, s->value_dim, tile));
-  // groups: (sequence, share) with their tiles, in two parts: split tiles, whole ones
-  struct Group {
-    int64_t work = 0;
-    std::vector<std::pair<int64_t, ll::AttendItem>> items;   // rows, item
-  };
   int64_t slot = 0;
-  std::vector<Group> parts[2];
-  for (size_t at = 0; at < tiles.size();) {
-    size_t end = at;
-    while (end < tiles.size() && tiles[end].seq == tiles[at].seq) ++end;
-    const ll::StepSeq& q = seqs[static_cast<size_t>(tiles[at].seq)];
-    const int64_t most = ceil_div(tiles[at].seen, share);   // the last tile sees most
-    std::vector<Group> mine[2];
-    mine[0].resize(static_cast<size_t>(most > 1 ? most : 0));
-    mine[1].resize(1);
-    for (size_t x = at; x < end; ++x) {
-      const int64_t shares = ceil_div(tiles[x].seen, share);
-      ll::AttendItem it{};
-      it.seq = q.seq;
-      it.tok0 = q.tok0;
-      it.q_rows = q.count * s->group;
-      it.row0 = tiles[x].index * tile;
-      it.first = q.row0;
-      it.kv_len = q.row0 + q.count;
-      for (int64_t c = 0; c < shares; ++c) {
-        it.splits = static_cast<int32_t>(c | shares << 16);
-        it.slot = static_cast<int32_t>(slot + c);
-        Group& g = shares > 1 ? mine[0][static_cast<size_t>(c)] : mine[1][0];
-        g.items.emplace_back(ceil_div(tiles[x].seen, shares), it);
-        g.work += g.items.back().first;
-      }
-      if (shares > 1) slot += shares;
+  for (const Tile& x : tiles) {
+    const ll::StepSeq& q = seqs[x.seq];
+    const int64_t shares = ceil_div(x.seen, share);
+    ll::AttendItem it{};
+    it.seq = q.seq;
+    it.tok0 = q.tok0;
+    it.q_rows = q.count * s->group;
+    it.row0 = x.index * tile;
+    it.first = q.row0;
+    it.kv_len = q.row0 + q.count;
+    for (int64_t c = 0; c < shares; ++c) {
+      it.splits = static_cast<int32_t>(c | shares << 16);
+      it.slot = static_cast<int32_t>(slot + c);
+      out->push_back(it);
     }
-    for (int k = 0; k < 2; ++k)
-      for (Group& g : mine[k])
-        if (!g.items.empty()) parts[k].push_back(std::move(g));
-    at = end;
+    if (shares > 1) slot += shares;   // the longer tiles: all before the first whole one
   }
-  int classes = 8;
-  while (classes > 1 && s->kv_heads % (16 / classes) == 0) classes /= 2;
-  int64_t leading = 0;
-  for (int k = 0; k < 2; ++k) {
-    std::vector<Group>& groups = parts[k];
-    int64_t work = 0, count = 0;
-    for (const Group& g : groups) {
-      work += g.work;
-      count += static_cast<int64_t>(g.items.size());
-    }
-    if (count == 0) continue;
-    std::stable_sort(groups.begin(), groups.end(), [](const Group& a, const Group& b) { return a.work > b.work; });
-    std::vector<std::vector<std::pair<int64_t, ll::AttendItem>>> queue(static_cast<size_t>(classes));
-    std::vector<int64_t> load(static_cast<size_t>(classes), 0);
-    const int64_t even = ceil_div(work, classes);
-    for (const Group& g : groups) {
-      // a group larger than the room of the emptiest class goes on in the next
-      size_t x = static_cast<size_t>(std::min_element(load.begin(), load.end()) - load.begin());
-      for (const auto& item : g.items) {
-        if (load[x] > 0 && load[x] + item.first > even)
-          x = static_cast<size_t>(std::min_element(load.begin(), load.end()) - load.begin());
-        queue[x].push_back(item);
-        load[x] += item.first;
-      }
-    }
-    for (auto& v : queue)
-      std::stable_sort(v.begin(), v.end(), [](const auto& a, const auto& b) { return a.first < b.first; });
-    for (int64_t i = 0; i < count; ++i) {   // from the back: the longest; a class without any takes another's shortest
-      auto& own = queue[out->size() % static_cast<size_t>(classes)];
-      if (!own.empty()) {
-        out->push_back(own.back().second);
-        own.pop_back();
-        continue;
-      }
-      auto& other = *std::max_element(queue.begin(), queue.end(),
-                                      [](const auto& a, const auto& b) { return a.size() < b.size(); });
-      out->push_back(other.front().second);
-      other.erase(other.begin());
-    }
-    if (k == 0) leading = static_cast<int64_t>(out->size());
-  }
-  return leading;
+  return slot;
 }
 
 ll_status check_step(const ll_step* s) {
