@@ -59,7 +59,7 @@ enum { LL_TYPE_BF16 = 0, LL_TYPE_F32 = 1 };
 /* Create a step on a pool: device buffers for its plan and for the parts of
  * split attention, all sized here.  The pool's head_dim may be at most 256.
  * Errors: LL_EINVAL, LL_EUNSUPPORTED (head_dim above 256, or more sequences
- * times KV heads than one dispatch holds: about 2^24), LL_ENOMEM,
+ * times KV heads than one dispatch holds: about 2^23), LL_ENOMEM,
  * LL_EDEVICE, LL_EPOISONED. */
 ll_status ll_step_create(ll_pool* pool, const ll_step_desc* desc, ll_step** out);
 
@@ -107,7 +107,8 @@ typedef struct {
  *   GQA: K head = R(position) norm(k), V head = v;  q_out = R(position) norm(q)
  * where R turns the pool's RoPE band (GQA: the first rotary_dim values of a head)
  * with the pool's pairing and base, from the float64 angle's cos and sin rounded
- * to float32.  a = b = NULL leaves the cache alone, q = NULL the queries.
+ * to float32.  a = b = NULL leaves the cache alone, q = NULL the queries.  q_out
+ * may be q, and may not overlap the inputs otherwise.
  * Errors: LL_EINVAL (layer, too few tokens, NULL or misaligned pointer or stride, overlapping
  * q_out rows, negative eps, a changed sequence, no begin yet), LL_EDEVICE. */
 ll_status ll_step_append(ll_step* step, const ll_append_desc* desc, void* stream);
@@ -133,7 +134,8 @@ typedef struct {
  * row is no row; positions play no part).  MLA: k_j is the whole row, v_j its
  * first 512 values, shared by all heads; GQA: head h reads KV head
  * h / (num_heads / num_kv_heads).  Rows that a token does not see never reach its
- * result, whatever they hold.  Results do not depend on the other sequences'
+ * result, whatever they hold; a token that sees none gets zeros and lse = -inf, and
+so does one whose scores are all -inf.  out may not overlap q or q_pe.  Results do not depend on the other sequences'
  * contents, and the same call on the same plan gives the same bits.
  * Errors: LL_EINVAL (layer, too few tokens, NULL or misaligned pointer or stride, overlapping out
  * rows, a scale that is not finite, window < 0 or without causal, a changed

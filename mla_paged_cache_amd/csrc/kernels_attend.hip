@@ -6,6 +6,7 @@
 // One pass over the rows keeps m, l and the unscaled sum of v, in float32; when m
 // grows, l and the sum are scaled down.  Scores are kept in base 2 (times
 // log2 e), so that each exponential is one instruction.
+#include <atomic>
 #include <type_traits>
 
 #include "device_common.h"
@@ -217,7 +218,7 @@ struct Shape {
 // 64 x 16 bytes from memory straight into LDS at `dst` + 16 * lane (base: uniform;
 // off: the lane's byte offset).  As assembly, because the compiler otherwise waits
 // for every such load before each transposing LDS read; it has no result
-// register, and the kernel waits for it itself (vmcnt(0) before the barrier).
+// register, and the kernel waits for it itself (`landed`, then a barrier).
 __device__ __forceinline__ void load_lds(lds_ptr dst, const void* base, uint32_t off) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
@@ -741,7 +742,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 template <typename S>
 hipError_t launch_shape(const AttendLaunch& a, hipStream_t s) {
   constexpr int lds = S::LDS;
-  static bool set[64];   // per device: hipFuncSetAttribute is not cheap
+  static std::atomic<bool> set[64];   // per device: hipFuncSetAttribute is not cheap
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;

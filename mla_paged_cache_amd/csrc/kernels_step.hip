@@ -45,7 +45,10 @@ __global__ __launch_bounds__(256) void step_setup_kernel(StepSetupLaunch a) {
       // the fresh ones), the uploaded list for the rest
       const int page = lp < s.old_pages ? a.page_table[int64_t{s.seq} * a.max_pages_per_seq + lp]
                                         : a.fresh[s.fresh_off + lp - s.old_pages];
-      a.rows[tok] = (page << a.page_shift) + (r & ((1 << a.page_shift) - 1));
+      // a page number outside the pool (only a page table that something else has
+      // written can hold one) is no row: append leaves it out
+      const bool in_pool = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pages);
+      a.rows[tok] = in_pool ? (page << a.page_shift) + (r & ((1 << a.page_shift) - 1)) : -1;
     }
   }
   const chunk_t* src = reinterpret_cast<const chunk_t*>(a.src_items);
@@ -146,8 +149,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendLaunch a) {
   if (!GQA && w == 0 && a.kv_waves) {   // the latent part: 64 chunks
     Vals x = widen(*reinterpret_cast<const chunk_t*>(a.a + t * a.a_ts + lane * 8));
     if (a.norm) rms_norm(x, a.norm, a.norm_f32, lane, true, 64, kKvLoraRank, a.eps);
-    chunk_t* dst = reinterpret_cast<chunk_t*>(a.k_plane) + int64_t{a.rows[t]} * kRowChunks;
-    dst[lane] = narrow(x);
+    const int row = a.rows[t];
+    if (row >= 0) reinterpret_cast<chunk_t*>(a.k_plane)[int64_t{row} * kRowChunks + lane] = narrow(x);
     return;
   }
   const int chunk = lane & ((1 << a.group_shift) - 1);
@@ -165,13 +168,15 @@ __global__ __launch_bounds__(256) void append_kernel(AppendLaunch a) {
       const int h = (is_v ? w - half : w) * per_wave + sub;
       if (h < a.kv_heads && in_head) {
         src = is_v ? a.b + t * a.b_ts + h * a.b_hs : a.a + t * a.a_ts + h * a.a_hs;
-        dst = (is_v ? a.v_plane : a.k_plane) + (int64_t{a.rows[t]} * a.kv_heads + h) * (a.head_chunks * 8);
+        const int row = a.rows[t];
+        if (row >= 0) dst = (is_v ? a.v_plane : a.k_plane) + (int64_t{row} * a.kv_heads + h) * (a.head_chunks * 8);
       }
       norm = is_v ? nullptr : a.norm;
       turn = !is_v;
     } else if (sub == 0) {
+      const int row = a.rows[t];
       src = a.b + t * a.b_ts;
-      dst = a.k_plane + int64_t{a.rows[t]} * kRowElems + kKvLoraRank;
+      if (row >= 0) dst = a.k_plane + int64_t{row} * kRowElems + kKvLoraRank;
     }
   } else {
     const int h = (w - a.kv_waves) * per_wave + sub;

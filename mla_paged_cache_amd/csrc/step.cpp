@@ -73,14 +73,14 @@ int64_t max_slots(const ll_step* s, int tile) {
 // so that all run at once; with many, shorter shares even out the end, and cost
 // their partial results.  Estimated in rows: a workgroup's own cost is about
 // `kOverhead` rows.
-int64_t pick_share(const ll_step* s, const std::vector<int64_t>& seen, int64_t groups) {
+int64_t pick_share(const ll_step* s, int tile, const std::vector<int64_t>& seen, int64_t groups) {
   constexpr int64_t kOverhead = 160, kGrain = 64;
   int64_t total = 0, longest = 1;
   for (int64_t w : seen) {
     total += w;
     longest = std::max(longest, w);
   }
-  const int64_t slots = max_slots(s, s->tile);
+  const int64_t slots = max_slots(s, tile);
   auto count = [&](int64_t share, int64_t* split) {   // workgroups per KV head, and those of split tiles
     int64_t n = 0;
     *split = 0;
@@ -118,12 +118,11 @@ int64_t pick_share(const ll_step* s, const std::vector<int64_t>& seen, int64_t g
 // The attention's items: every sequence's query rows in tiles, the longest first;
 // a tile that needs more cached rows than a share is split over several
 // workgroups.  Shares of split tiles come before the others.
-int64_t plan_items(const ll_step* s, const std::vector<ll::StepSeq>& seqs, std::vector<ll::AttendItem>* out) {
+int64_t plan_items(const ll_step* s, int tile, const std::vector<ll::StepSeq>& seqs, std::vector<ll::AttendItem>* out) {
   struct Tile {
     int64_t seen;
     int32_t seq, index;
   };
-  const int tile = s->tile;
   std::vector<Tile> tiles;
   std::vector<int64_t> seen;
   for (size_t i = 0; i < seqs.size(); ++i) {
@@ -135,7 +134,7 @@ int64_t plan_items(const ll_step* s, const std::vector<ll::StepSeq>& seqs, std::
     }
   }
   std::stable_sort(tiles.begin(), tiles.end(), [](const Tile& a, const Tile& b) { return a.seen > b.seen; });
-  const int64_t share = pick_share(s, seen, ll::attend_groups(s->pool->gqa, s->value_dim, tile));
+  const int64_t share = pick_share(s, tile, seen, ll::attend_groups(s->pool->gqa, s->value_dim, tile));
   int64_t slot = 0;
   for (const Tile& x : tiles) {
     const ll::StepSeq& q = seqs[x.seq];
@@ -255,7 +254,7 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
   s->gens.reserve(static_cast<size_t>(d->max_seqs));
   const int tile = ll::attend_tile(p->gqa, s->value_dim, int64_t{d->max_tokens} * s->group);
   s->max_items = int64_t{d->max_tokens} * s->group / 16 + d->max_seqs + kMaxShares / kv_heads;
-  if (s->max_items * kv_heads > ll::kMaxDispatchItems / 256)
+  if (s->max_items * kv_heads > ll::kMaxDispatchItems / 512)   // of up to 512 threads
     return fail(LL_EUNSUPPORTED, "the step's attention would not fit one dispatch");
   const size_t pairs = p->theta.size();
   size_t at = 0;
@@ -380,13 +379,9 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
   }
   const int tile = s->captured ? s->tile : ll::attend_tile(p->gqa, s->value_dim, most * s->group);
   std::vector<ll::AttendItem> items;
-  const int old_tile = s->tile;
-  s->tile = tile;
-  const int64_t shares = plan_items(s, ss, &items);
-  if (static_cast<int64_t>(items.size()) > s->max_items) {
-    s->tile = old_tile;
+  const int64_t shares = plan_items(s, tile, ss, &items);
+  if (static_cast<int64_t>(items.size()) > s->max_items)
     return fail(LL_EINVAL, "the step's attention needs %zu items, more than %lld", items.size(), (long long)s->max_items);
-  }
   // host memory that the commit below needs, before anything changes
   for (int32_t i = 0; i < n; ++i) {
     ll::SeqState& q = p->seqs[seq_ids[i]];
@@ -399,10 +394,7 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
   const size_t b_seq = ll::align_up(ss.size() * sizeof(ll::StepSeq), 256);
   const size_t b_it = ll::align_up(items.size() * sizeof(ll::AttendItem), 256);
   const size_t b_pg = ll::align_up(fresh.size() * sizeof(int32_t), 256);
-  if ((rc = ll::pool_stage(p, b_seq + b_it + b_pg + 256, &sg))) {
-    s->tile = old_tile;
-    return rc;
-  }
+  if ((rc = ll::pool_stage(p, b_seq + b_it + b_pg + 256, &sg))) return rc;
   if (!ss.empty()) std::memcpy(sg->host, ss.data(), ss.size() * sizeof(ll::StepSeq));
   if (!items.empty()) std::memcpy(sg->host + b_seq, items.data(), items.size() * sizeof(ll::AttendItem));
   if (!fresh.empty()) std::memcpy(sg->host + b_seq + b_it, fresh.data(), fresh.size() * sizeof(int32_t));
@@ -420,6 +412,7 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
   a.pairs = static_cast<int32_t>(p->theta.size());
   a.page_shift = p->page_shift;
   a.max_pages_per_seq = p->desc.max_pages_per_seq;
+  a.num_pages = p->desc.num_pages;
   a.page_table = p->desc.page_table;
   a.dst_counts = s->d_counts;
   a.dst_items = s->d_items;
@@ -444,6 +437,7 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
     gens[i] = q.gen;
   }
   s->gens = std::move(gens);
+  s->tile = tile;
   s->tokens = tokens;
   s->items = static_cast<int64_t>(items.size());
   s->shares = shares;

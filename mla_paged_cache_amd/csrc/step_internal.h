@@ -52,10 +52,11 @@ struct StepSetupLaunch {
   int32_t pairs;
   int32_t page_shift;
   int32_t max_pages_per_seq;
+  int32_t num_pages;
   int32_t* page_table;
   StepCounts* dst_counts;
   AttendItem* dst_items;
-  int32_t* rows;                 // [tokens] physical row
+  int32_t* rows;                 // [tokens] physical row, -1: none
   float* tab;                    // [tokens][2][pairs] float32 cos, then sin
 };
 

@@ -722,7 +722,11 @@ class Step:
         return t.shape[0]
 
     def _weight(self, w, name: str, n: int):
-        if w.dtype not in (self._bf16, self._f32) or w.shape != (n,) or w.device != self.device or w.stride(0) != 1:
+        try:
+            ok = w.dtype in (self._bf16, self._f32) and w.shape == (n,) and w.device == self.device and w.stride(0) == 1
+        except AttributeError:   # no tensor
+            ok = False
+        if not ok:
             raise ValueError(f"{name}: need a dense bf16 or float32 tensor [{n}] on {self.device}")
         return w.data_ptr()
 
@@ -770,8 +774,11 @@ class Step:
                 f32 = 1 if q_norm.dtype is self._f32 else 0
         elif q_out is not None or q_norm is not None:
             raise ValueError("q_out and q_norm need q")
-        desc = _APPEND_DESC.pack(room, layer, f32, a_ptr, a_ts, a_hs, b_ptr, b_ts, b_hs, norm_ptr, q_ptr, q_ts, q_hs,
-                                 o_ptr, o_ts, o_hs, qn_ptr, eps)
+        try:
+            desc = _APPEND_DESC.pack(room, layer, f32, a_ptr, a_ts, a_hs, b_ptr, b_ts, b_hs, norm_ptr, q_ptr, q_ts, q_hs,
+                                     o_ptr, o_ts, o_hs, qn_ptr, eps)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"layer or eps: {e}") from None
         rc = _lib.ll_step_append(self._h, desc, self._raw_stream(self._dev) if stream is None else stream.cuda_stream)
         if rc:
             _check(rc)
@@ -821,8 +828,11 @@ class Step:
             l_ptr = lse.data_ptr()
         else:
             lse = None
-        desc = _ATTEND_DESC.pack(room, layer, 1 if causal else 0, window, scale, q.data_ptr(), q_ts, q_hs, p_ptr, p_ts, p_hs,
-                                 out.data_ptr(), o_ts, o_hs, l_ptr)
+        try:
+            desc = _ATTEND_DESC.pack(room, layer, 1 if causal else 0, window, scale, q.data_ptr(), q_ts, q_hs,
+                                     p_ptr, p_ts, p_hs, out.data_ptr(), o_ts, o_hs, l_ptr)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"layer, window or scale: {e}") from None
         rc = _lib.ll_step_attend(self._h, desc, self._raw_stream(self._dev) if stream is None else stream.cuda_stream)
         if rc:
             _check(rc)
