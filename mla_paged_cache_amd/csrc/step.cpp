@@ -490,10 +490,9 @@ ll_status ll_step_append(ll_step* s, const ll_append_desc* d, void* stream) try 
   a.head_chunks = static_cast<int32_t>(D / 8);
   a.group_shift = 0;
   while ((1 << a.group_shift) < a.head_chunks) ++a.group_shift;
-  const int32_t per_wave = 64 >> a.group_shift;   // heads a wave takes
-  // MLA: a wave for the latent part, and k_pe as one head more
-  a.kv_waves = !rows ? 0 : p->gqa ? 2 * static_cast<int32_t>(ceil_div(s->kv_heads, per_wave)) : 2;
-  a.waves_per_token = a.kv_waves + (asks ? static_cast<int32_t>(ceil_div(s->heads, per_wave)) : 0);
+  const int32_t per_wave = 64 >> a.group_shift;   // heads of a piece
+  a.kv_pieces = !rows ? 0 : p->gqa ? 2 * static_cast<int32_t>(ceil_div(s->kv_heads, per_wave)) : 1;
+  a.pieces = a.kv_pieces + (asks ? static_cast<int32_t>(ceil_div(s->heads, per_wave)) : 0);
   a.band_chunks = static_cast<int32_t>(p->theta.size() / 4);
   a.norm_f32 = d->norm_type == LL_TYPE_F32;
   a.eps = d->eps;

@@ -67,8 +67,9 @@ struct AppendLaunch {
   const float* tab;
   int32_t pairs;
   int32_t capacity;              // tokens the grid covers
-  int32_t waves_per_token;       // kv_waves + the query waves
-  int32_t kv_waves;              // waves of a token that write cache rows (0: queries only)
+  int32_t waves_per_token;       // set by the launch
+  int32_t pieces;                // a token's pieces of 64 chunks: kv_pieces + those of the queries
+  int32_t kv_pieces;             // of them for cache rows (GQA: K's, then V's; MLA: 1; 0: queries only)
   int32_t heads, kv_heads;
   int32_t head_chunks;           // GQA: head_dim / 8
   int32_t group_shift;           // log2 of the lanes a head takes
