@@ -205,11 +205,17 @@ struct Shape {
   // a tile's loads per wave, at least, and the pieces they come in
   static constexpr int LOADS = MLA ? BN / WAVES + BN / 8 / WAVES : 2 * BN * ROWCH / 64 / WAVES;
   static constexpr int PIECES = MLA ? BN / WAVES + (BN / 8 + WAVES - 1) / WAVES : BN * ROWCH / 64 / WAVES;
-  static constexpr int LDS = STAGES * STAGE + WAVES * PAGES * BN * 4;
   static constexpr int KVT = BN / KW;                        // cached rows of a tile per wave
   static constexpr int TILE = 16 * QN * QW;                  // query rows
   // the sums fill the accumulation registers, which only assembly can ask for
   static constexpr bool ACC = QN * DV / 4 >= 256;
+  // then the waves share the weights through LDS, and each sums the columns
+  // [wave * DV / QW ...) of all queries: the values are read from LDS once, not by
+  // every wave (a 2048-token MLA chunk of 16 heads over 16384 rows, two sequences:
+  // 1846 us with each wave summing its own queries, 1732 us so)
+  static constexpr int WEIGHTS = STAGES * STAGE + WAVES * PAGES * BN * 4;   // where these lie in LDS
+  static constexpr int KEEPS = WEIGHTS + TILE * BN * 2;                     // two tiles' scalings, and which waves have any
+  static constexpr int LDS = ACC ? KEEPS + 2 * (TILE * 4 + 16) : WEIGHTS;
   static_assert(KVT % 16 == 0 && BN <= 64 && BN % WAVES == 0, "whole matrix tiles, a lane per row");
   static_assert(BN * ROWCH / 64 % WAVES == 0 && AHEAD >= 2, "as many loads for every wave; the next tile is there early");
   static_assert(LOADS * (AHEAD - 1) < 64, "the wait counter's range");
@@ -221,7 +227,8 @@ struct Shape {
 // register, and the kernel waits for it itself (`landed`, then a barrier).
 __device__ __forceinline__ void load_lds(lds_ptr dst, const void* base, uint32_t off) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+  // (five wait states between a vector instruction that writes `base` and the load)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void load_lds(lds_ptr dst, const void* src) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
@@ -293,7 +300,9 @@ __device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const u
 template <typename S>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::WAVES > 4 ? 2 : 1))) void attend_kernel(AttendLaunch a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  constexpr int QN = S::QN, KT = S::KVT / 16, DT = S::DV / S::DW / 16, KK = S::DK / 32;
+  constexpr int QN = S::QN, KT = S::KVT / 16, KK = S::DK / 32;
+  constexpr int DT = S::DV / (S::ACC ? S::QW : S::DW) / 16;   // 16-column tiles of a wave's sums
+  constexpr int ON = S::ACC ? QN * S::QW : QN;                // and their query tiles
   const int kvh = blockIdx.x % a.kv_heads;
   const int item = blockIdx.x / a.kv_heads;
   const AttendItem it = a.items[item];   // asked for together with the count
@@ -343,12 +352,15 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   }
   c2 = nothing ? 1.f : fabsf(c2);
 
-  f32x4 o[DT][QN];
+  f32x4 o[DT][ON];
   float m[QN], l[QN];
 #pragma unroll
   for (int n = 0; n < QN; ++n) {
     m[n] = -__builtin_inff();
     l[n] = 0.f;
+  }
+#pragma unroll
+  for (int n = 0; n < ON; ++n) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
       o[d][n] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -411,7 +423,8 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   const int kr = kw * S::KVT + li, vr = kw * S::KVT + 4 * g + (li >> 2);
   const int k_at = kr * S::ROWCH * 16 + ((g ^ swizzle<S::ROWCH>(kr)) << 4);
   const int p_at = S::MAIN + kr * S::SIDE_ROWCH * 16 + ((g ^ swizzle<S::SIDE_ROWCH>(kr)) << 4);
-  const int vc = dw * (S::ROWCH / S::DW);   // this wave's first chunk of the values
+  // this wave's first chunk of the values
+  const int vc = S::ACC ? qw * (S::ROWCH / S::QW) : dw * (S::ROWCH / S::DW);
   const int v_at = S::VALUES + vr * S::ROWCH * 16 + (vc >> 4) * 256 +
                    ((((vc & 15) | ((li >> 1) & 1)) ^ swizzle<S::ROWCH>(vr)) << 4) + (li & 1) * 8;
   static_assert(S::STAGE % 256 == 0 && S::MAIN % 256 == 0, "the low bits of an address are the lane's");
@@ -454,6 +467,8 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
     __syncthreads();
     scores(0, s, [](int) {});
   }
+  float* const keeps = reinterpret_cast<float*>(smem + S::KEEPS);
+  int* const moved = reinterpret_cast<int*>(smem + S::KEEPS + 2 * S::TILE * 4);
   bool rows_only = false;
   for (int tile = 0; tile < tiles; ++tile) {
     const int j0 = share.lo + tile * S::BN;
@@ -493,10 +508,12 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
     }
     if constexpr (S::ACC)   // the sums stay where they are, whatever follows reads
 #pragma unroll
-      for (int n = 0; n < QN; ++n)
+      for (int n = 0; n < ON; ++n)
 #pragma unroll
         for (int d = 0; d < DT; ++d) asm volatile("" : "+a"(o[d][n]));
-    if (__any(grew)) {
+    const bool moves = __any(grew);
+    if constexpr (S::ACC) moved[(tile & 1) * S::WAVES + wave] = moves;
+    if (moves) {
 #pragma unroll
       for (int n = 0; n < QN; ++n) {
         float x = fmaxf(top[n], m[n]);
@@ -505,14 +522,11 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
         const float keep = x == m[n] ? 1.f : exp2_(m[n] - x);
         m[n] = x;
         l[n] *= keep;
+        if constexpr (S::ACC) {
+          if (g == 0) keeps[(tile & 1) * S::TILE + (qw * QN + n) * 16 + li] = keep;
+        } else {
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          if constexpr (S::ACC) asm volatile("" : "+a"(o[d][n]));   // four at a time leave the accumulators
-          o[d][n] *= keep;
-          if constexpr (S::ACC) {
-            asm volatile("" : "+a"(o[d][n]));
-            __builtin_amdgcn_sched_barrier(0);
-          }
+          for (int d = 0; d < DT; ++d) o[d][n] *= keep;
         }
       }
     }
@@ -540,6 +554,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
         for (int v = i * W / PRODUCTS; v < (i + 1) * W / PRODUCTS; ++v) weight(v);
       });
     } else {
+      if constexpr (S::ACC) __syncthreads();   // nobody reads the last tile's weights any more
 #pragma unroll
       for (int v = 0; v < W; ++v) weight(v);
     }
@@ -578,36 +593,91 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
         load_piece(x, tile + S::AHEAD, row);
     };
     if constexpr (S::ACC) {
-      // Four columns and both query tiles at a time.  An operand that an ordinary
+      // The weights go through LDS as they lie in the registers, and so do the
+      // scalings of queries whose reference has moved.
+      static_assert(!S::ACC || (QN == 2 && KT == 2 && S::QW == 4 && ON == 8), "the block below");
+#pragma unroll
+      for (int n = 0; n < QN; ++n)
+        *reinterpret_cast<__attribute__((address_space(3))) bf16x8*>(lds + S::WEIGHTS + ((qw * QN + n) * 64 + lane) * 16) =
+            weights(0, n);
+      if (more) load_piece(PIECES - 1, tile + S::AHEAD, row);
+      __syncthreads();
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      const i32x4 moves = *reinterpret_cast<const i32x4*>(moved + (tile & 1) * S::WAVES);
+      bf16x8 w[8], y[4];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) w[n] = lds_chunk(lds + S::WEIGHTS + (n * 64 + lane) * 16);
+      y[0] = columns(0), y[1] = columns(1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (__builtin_amdgcn_readfirstlane(moves.x | moves.y | moves.z | moves.w))
+#pragma unroll
+        for (int n = 0; n < ON; ++n) {
+          if (!__builtin_amdgcn_readfirstlane(moves[n / QN])) continue;
+          const float keep = keeps[(tile & 1) * S::TILE + n * 16 + li];
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            asm volatile("" : "+a"(o[d][n]));   // four at a time leave the accumulators
+            o[d][n] *= keep;
+            asm volatile("" : "+a"(o[d][n]));
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      // Thirty-two columns and all query tiles at a time.  An operand that an ordinary
       // instruction has just written needs two wait states, and a sum is safe to
       // touch eight after its product: the block waits for both itself, since the
-      // compiler does not see what it holds.
-      static_assert(!S::ACC || (QN == 2 && KT == 2), "the block below");
-      bf16x8 y[2][4];
+      // compiler does not see what it holds.  Two rows' loads go between its
+      // products (outside they cost 100 clocks each, which no product covers); the
+      // first is five wait states behind the instructions that wrote its address.
+      static_assert(!S::ACC || (STEPS == 8 && PIECES == 9), "the loads of the block below");
+      const uint32_t loads = __builtin_amdgcn_readfirstlane(more ? ~0u : 0u);
+      const uint64_t lanes = static_cast<uint64_t>(loads) << 32 | loads;
+      const uint32_t lo = static_cast<uint32_t>(row), hi = static_cast<uint32_t>(row >> 32);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[0][e] = columns(e);
-#pragma unroll
-      for (int i = 0; i < STEPS; i += 4) {
-        const int b = i / 4 & 1;
-        if (i + 4 < STEPS)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[b ^ 1][e] = columns(i + 4 + e);
-        const bf16x8 w0 = weights(i, 0), w1 = weights(i, QN - 1);
+      for (int i = 0; i < STEPS; i += 2) {
+        const int b = i & 2;
+        if (i + 2 < STEPS) y[b ^ 2] = columns(i + 2), y[(b ^ 2) + 1] = columns(i + 3);
+        const int r0 = i * S::WAVES + wave, r1 = r0 + S::WAVES;   // pieces i and i + 1 (see load_mla_piece)
+        const uint64_t at0 = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r0))) << 32 |
+                             static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, r0));
+        const uint64_t at1 = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r1))) << 32 |
+                             static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, r1));
+        const uint32_t to = __builtin_amdgcn_readfirstlane(
+            static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds + (tile + S::AHEAD) % S::STAGES * S::STAGE + r0 * 1024)));
+        const uint32_t off0 = static_cast<uint32_t>(lane ^ swizzle<64>(r0)) * 16;
+        const uint32_t off1 = static_cast<uint32_t>(lane ^ swizzle<64>(r1)) * 16;
         asm volatile(
+            "s_mov_b32 m0, %26\n\t"
             "s_nop 1\n\t"
-            "v_mfma_f32_16x16x32_bf16 %0, %8, %12, %0\n\t"
-            "v_mfma_f32_16x16x32_bf16 %1, %8, %13, %1\n\t"
-            "v_mfma_f32_16x16x32_bf16 %2, %9, %12, %2\n\t"
-            "v_mfma_f32_16x16x32_bf16 %3, %9, %13, %3\n\t"
-            "v_mfma_f32_16x16x32_bf16 %4, %10, %12, %4\n\t"
-            "v_mfma_f32_16x16x32_bf16 %5, %10, %13, %5\n\t"
-            "v_mfma_f32_16x16x32_bf16 %6, %11, %12, %6\n\t"
-            "v_mfma_f32_16x16x32_bf16 %7, %11, %13, %7\n\t"
+            "v_mfma_f32_16x16x32_bf16 %0, %16, %18, %0\n\t"
+            "v_mfma_f32_16x16x32_bf16 %1, %16, %19, %1\n\t"
+            "v_mfma_f32_16x16x32_bf16 %2, %16, %20, %2\n\t"
+            "v_mfma_f32_16x16x32_bf16 %3, %16, %21, %3\n\t"
+            "s_mov_b64 exec, %32\n\t"
+            "global_load_lds_dwordx4 %28, %30\n\t"
+            "s_mov_b64 exec, -1\n\t"
+            "v_mfma_f32_16x16x32_bf16 %4, %16, %22, %4\n\t"
+            "v_mfma_f32_16x16x32_bf16 %5, %16, %23, %5\n\t"
+            "v_mfma_f32_16x16x32_bf16 %6, %16, %24, %6\n\t"
+            "v_mfma_f32_16x16x32_bf16 %7, %16, %25, %7\n\t"
+            "s_mov_b32 m0, %27\n\t"
+            "v_mfma_f32_16x16x32_bf16 %8, %17, %18, %8\n\t"
+            "v_mfma_f32_16x16x32_bf16 %9, %17, %19, %9\n\t"
+            "v_mfma_f32_16x16x32_bf16 %10, %17, %20, %10\n\t"
+            "v_mfma_f32_16x16x32_bf16 %11, %17, %21, %11\n\t"
+            "s_mov_b64 exec, %32\n\t"
+            "global_load_lds_dwordx4 %29, %31\n\t"
+            "s_mov_b64 exec, -1\n\t"
+            "v_mfma_f32_16x16x32_bf16 %12, %17, %22, %12\n\t"
+            "v_mfma_f32_16x16x32_bf16 %13, %17, %23, %13\n\t"
+            "v_mfma_f32_16x16x32_bf16 %14, %17, %24, %14\n\t"
+            "v_mfma_f32_16x16x32_bf16 %15, %17, %25, %15\n\t"
             "s_nop 9"
-            : "+a"(o[i][0]), "+a"(o[i][QN - 1]), "+a"(o[i + 1][0]), "+a"(o[i + 1][QN - 1]), "+a"(o[i + 2][0]),
-              "+a"(o[i + 2][QN - 1]), "+a"(o[i + 3][0]), "+a"(o[i + 3][QN - 1])
-            : "v"(y[b][0]), "v"(y[b][1]), "v"(y[b][2]), "v"(y[b][3]), "v"(w0), "v"(w1));
-        pieces(i / 4, STEPS / 4);
+            : "+a"(o[i][0]), "+a"(o[i][1]), "+a"(o[i][2]), "+a"(o[i][3]), "+a"(o[i][4]), "+a"(o[i][5]), "+a"(o[i][6]),
+              "+a"(o[i][7]), "+a"(o[i + 1][0]), "+a"(o[i + 1][1]), "+a"(o[i + 1][2]), "+a"(o[i + 1][3]), "+a"(o[i + 1][4]),
+              "+a"(o[i + 1][5]), "+a"(o[i + 1][6]), "+a"(o[i + 1][7])
+            : "v"(y[b]), "v"(y[b + 1]), "v"(w[0]), "v"(w[1]), "v"(w[2]), "v"(w[3]), "v"(w[4]), "v"(w[5]), "v"(w[6]),
+              "v"(w[7]), "s"(to), "s"(to + S::WAVES * 1024), "v"(off0), "v"(off1), "s"(at0), "s"(at1), "s"(lanes)
+            : "memory");
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
@@ -704,10 +774,22 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
       }
     }
   } else {
+    float* const ends = reinterpret_cast<float*>(smem + S::WEIGHTS);   // ACC: every query's m and l
+    if constexpr (S::ACC) {
+      __syncthreads();   // the weights are no longer read
+      if (g == 0)
 #pragma unroll
-    for (int n = 0; n < QN; ++n) {
-      const int row = (qw * QN + n) * 16 + li;
-      const int r = it.row0 + row, col = dw * (S::DV / S::DW) + g * 4;
+        for (int n = 0; n < QN; ++n) {
+          ends[(qw * QN + n) * 16 + li] = m[n];
+          ends[S::TILE + (qw * QN + n) * 16 + li] = l[n];
+        }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < ON; ++n) {
+      const int row = ((S::ACC ? 0 : qw * QN) + n) * 16 + li;
+      const int r = it.row0 + row, col = (S::ACC ? qw : dw) * DT * 16 + g * 4;
+      const float top = S::ACC ? ends[row] : m[S::ACC ? 0 : n], sum = S::ACC ? ends[S::TILE + row] : l[S::ACC ? 0 : n];
       if (r >= it.q_rows) continue;
       const int tt = r / a.group, h = kvh * a.group + r - tt * a.group;
       const int64_t t = it.tok0 + tt;
@@ -720,11 +802,11 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
           __builtin_amdgcn_sched_barrier(0);
         }
         if (col == 0) {
-          a.part_ml[at * 2] = m[n];
-          a.part_ml[at * 2 + 1] = l[n];
+          a.part_ml[at * 2] = top;
+          a.part_ml[at * 2 + 1] = sum;
         }
       } else {
-        const float inv = l[n] == 0.f ? 0.f : 1.f / l[n];
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         uint16_t* out = a.out + t * a.o_ts + h * a.o_hs;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
@@ -733,7 +815,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
             *reinterpret_cast<bf16x4*>(out + col + d * 16) = __builtin_convertvector(o[d][n] * inv, bf16x4);
           __builtin_amdgcn_sched_barrier(0);
         }
-        if (a.lse && col == 0) a.lse[t * a.heads + h] = l[n] == 0.f ? -__builtin_inff() : (m[n] + __log2f(l[n])) * kLn2;
+        if (a.lse && col == 0) a.lse[t * a.heads + h] = sum == 0.f ? -__builtin_inff() : (top + __log2f(sum)) * kLn2;
       }
     }
   }
