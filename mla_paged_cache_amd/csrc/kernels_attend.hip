@@ -741,7 +741,10 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
         *reinterpret_cast<f32x4*>(sums + (kw * OUT_ROWS + row) * S::DV + ch * 4) = o[d][n];
       }
     __syncthreads();
-    for (int i = tid; i < OUT_ROWS * (S::DV / 4); i += S::THREADS) {
+    static_assert(OUT_ROWS * (S::DV / 4) % S::THREADS == 0, "as many chunks for every thread");
+#pragma unroll
+    for (int x = 0; x < OUT_ROWS * (S::DV / 4) / S::THREADS; ++x) {
+      const int i = x * S::THREADS + tid;
       const int row = i / (S::DV / 4), c = i % (S::DV / 4);
       const int r = it.row0 + row;
       if (r >= it.q_rows || c * 4 >= dv) continue;
