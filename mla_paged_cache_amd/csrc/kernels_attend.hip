@@ -297,6 +297,12 @@ __device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const u
 // In a tile of which some query sees only a part, unseen weights are 0; since 0
 // times a value that is not finite is not 0, such a tile is searched for those,
 // and the item falls back to reading exactly the rows each query sees.
+//
+// One token per sequence is bound by reading the cache: 64 MLA sequences of up to
+// 32768 rows 286 us (5.3 TB/s), 128 GQA ones of up to 8192 rows and 8 heads of 128
+// 458 us (5.95 TB/s; a large read reaches 6.9).  Chunks are bound by the matrix
+// units and what feeds them: 2 x 2048 MLA tokens of 16 heads over up to 16384 rows
+// 1603 us (43% busy), 4096 GQA tokens of 32 heads over 32768 rows 1977 us (44%).
 template <typename S>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::WAVES > 4 ? 2 : 1))) void attend_kernel(AttendLaunch a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -840,7 +846,15 @@ hipError_t launch_shape(const AttendLaunch& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The query rows a workgroup takes follow from how many the sequences bring.
+// The query rows a workgroup takes follow from how many the sequences bring
+// (attend_tile); how its waves share them was measured:
+//  * few rows: the waves split a tile's cached rows, and for MLA its values' columns
+//    (one token of 16 heads over 1531 rows: 11.8 us, without the columns' split 16;
+//    64 tokens over 32768: 280 and 286 us);
+//  * many rows: two tiles of 16 queries a wave halve the reads of LDS per product.
+// Four tiles in LDS: with three, single tokens wait for memory (those 64 MLA tokens
+// 340 us against 280, 128 GQA tokens over up to 8192 rows 559 against 455); smaller
+// tiles, more of them (32 rows, 7 or 9 tiles, GQA): 490 and 466 us.
 template <bool MLA, int DP>
 hipError_t launch_tile(const AttendLaunch& a, hipStream_t s) {
   constexpr bool WIDE = MLA || DP > 128;   // rows of 1 KiB: tiles of 32
@@ -848,10 +862,10 @@ hipError_t launch_tile(const AttendLaunch& a, hipStream_t s) {
     case 16: return launch_shape<Shape<MLA, DP, 1, 1, WIDE ? 2 : 4, MLA ? 2 : 1, WIDE ? 32 : 64, 4>>(a, s);
     case 32: return launch_shape<Shape<MLA, DP, 1, 2, 2, MLA ? 2 : 1, WIDE ? 32 : 64, 4>>(a, s);
     case 64: return launch_shape<Shape<MLA, DP, 1, 4, 1, MLA ? 2 : 1, WIDE ? 32 : 64, 4>>(a, s);
-    case 128: return launch_shape<Shape<MLA, DP, 2, 4, 1, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
+    case 128: return launch_shape<Shape<MLA, DP, 2, 4, 1, 1, WIDE ? 32 : 64, 4>>(a, s);
     default:
       if constexpr (WIDE) return hipErrorInvalidValue;   // attend_tile never says so
-      else return launch_shape<Shape<MLA, DP, 2, 8, 1, 1, WIDE ? 32 : 64, DP == 128 ? 3 : 4>>(a, s);
+      else return launch_shape<Shape<MLA, DP, 2, 8, 1, 1, WIDE ? 32 : 64, 4>>(a, s);
   }
 }
 
@@ -914,10 +928,16 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendLaunc
 
 }  // namespace
 
+// The smallest tile that holds all rows a sequence brings, so that its cached rows
+// are read once, up to what the registers hold (MLA and heads above 128: 128 rows).
+// 4096 GQA tokens of 4 heads a KV head over 32768 rows: 2.23 ms in tiles of 256,
+// 3.10 of 128, 4.96 of 64; 333 tokens of 5 heads in a window of 1000: 52, 57, 78 us.
 int attend_tile(bool gqa, int dim, int64_t rows) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 || !gqa || dim > 128 ? 128 : 256;
 }
 
+// One workgroup a CU, since its tiles fill LDS; two where rows of 64 values leave
+// room.
 int attend_groups(bool gqa, int dim, int tile) {
   return gqa && dim <= 64 && tile < 256 ? 512 : 256;
 }
