@@ -58,8 +58,9 @@ enum { LL_TYPE_BF16 = 0, LL_TYPE_F32 = 1 };
 
 /* Create a step on a pool: device buffers for its plan and for the parts of
  * split attention, all sized here.  The pool's head_dim may be at most 256.
- * Errors: LL_EINVAL, LL_EUNSUPPORTED (head_dim above 256, or more sequences
- * times KV heads than one dispatch holds: about 2^23), LL_ENOMEM,
+ * Errors: LL_EINVAL, LL_EUNSUPPORTED (head_dim above 256, page-table rows of
+ * 2^31 - 1024 cached rows or more, or more sequences times KV heads than one
+ * dispatch holds: about 2^23), LL_ENOMEM,
  * LL_EDEVICE, LL_EPOISONED. */
 ll_status ll_step_create(ll_pool* pool, const ll_step_desc* desc, ll_step** out);
 

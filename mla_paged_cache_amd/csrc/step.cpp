@@ -242,6 +242,9 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
     return fail(LL_EINVAL, "max_tokens must lie in 1 .. 2^22, and max_tokens * num_heads in 1 .. 2^25");
   if (p->gqa && p->head_chunks * 8 > ll::kMaxHeadDim)
     return fail(LL_EUNSUPPORTED, "head_dim %d is above %d", p->head_chunks * 8, ll::kMaxHeadDim);
+  // the kernels count cached rows in 32 bits, up to a tile past the last one
+  if (int64_t{p->desc.max_pages_per_seq} * p->P > INT32_MAX - 1024)
+    return fail(LL_EUNSUPPORTED, "a sequence may hold more than 2^31 - 1024 rows");
   std::unique_ptr<ll_step> s(new ll_step());
   s->device = p->desc.device;
   s->heads = d->num_heads;

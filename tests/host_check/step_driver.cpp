@@ -315,7 +315,7 @@ int run(bool gqa, int P, int seed) {
     CHECK(ll_step_append(steps[i].h, &ad, nullptr) == LL_EINVAL);   // not begun
   }
   std::map<int, Seq> b = w.books();
-  int begun = 0, refused = 0, stale = 0;
+  int begun = 0, refused = 0, stale = 0, behind = 0;
   for (int op = 0; op < 500; ++op) {
     const int kind = below(10);
     if (kind == 0) {
@@ -342,6 +342,19 @@ int run(bool gqa, int P, int seed) {
         ll_append_desc d = append_desc(w, kTokens);
         if (done && m.begun && std::find(m.seqs.begin(), m.seqs.end(), id) != m.seqs.end() && std::count(keep.begin(), keep.begin() + q.len, 0))
           CHECK(ll_step_append(m.h, &d, nullptr) == LL_EINVAL);
+      }
+      // and a begin right behind it settles them
+      const int64_t kept = std::count(keep.begin(), keep.begin() + q.len, 1), pos = q.pos;
+      const int32_t two = 2;
+      StepModel& m = steps[1];
+      if (done && below(2) && ll_step_begin(m.h, &id, &two, 1, 1, nullptr) == LL_OK) {
+        m.begun = true;
+        m.seqs = {id}, m.counts = {2}, m.tokens = 2;
+        m.tile = ll::attend_tile(gqa, w.dim, 2 * (w.heads / w.kv_heads));
+        m.as_begun = w.books();
+        CHECK(m.as_begun[id].len == kept + 2 && m.as_begun[id].pos == pos + 2);
+        check_plan(w, m, m.as_begun);
+        ++behind;
       }
     } else {
       StepModel& m = steps[below(2)];
@@ -456,7 +469,7 @@ int run(bool gqa, int P, int seed) {
       }
     }
   }
-  CHECK(begun > 50 && refused > 30 && stale > 5);
+  CHECK(begun > 50 && refused > 30 && stale > 5 && behind > 3);
   // capture: the whole capacity, and the tile stays from then on
   StepModel& m = steps[1];
   const int32_t none = 0;

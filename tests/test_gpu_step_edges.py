@@ -136,6 +136,70 @@ def test_every_tile_size(kind, count):
     c.pool.close()
 
 
+@pytest.mark.parametrize("dim", [16, 48, 80, 112, 144, 192, 240])
+@pytest.mark.parametrize("count", [1, 9, 45])
+def test_head_widths_between_the_powers_of_two(dim, count):
+    c = _cache(True, 2, dim, 16, [170, count], seed=dim)
+    step = c.pool.step(6, max_tokens=2 * count)
+    T = step.begin([1, 0], [count, count], grow=False)
+    q = _queries(c, T, 6)
+    out, lse = step.attend(0, q, lse=True)
+    c.check_attend(out, lse, q, [1, 0], [count, count], 0, dim ** -0.5)
+    step.close()
+    c.pool.close()
+
+
+@pytest.mark.parametrize("gqa", [False, True])
+def test_queries_or_rows_alone(gqa):
+    """append without rows or without queries does that part of the whole call."""
+    c = Cache(gqa, 16, [50], seed=5, kv_heads=2, dim=64, rot=64, room=20)
+    step = c.pool.step(5 if not gqa else 6, max_tokens=9)
+    T = step.begin([0], [9])
+    g = np.random.default_rng(4)
+    a = bf16(g.standard_normal((T, 2, 64) if gqa else (T, 512))).cuda()
+    b = bf16(g.standard_normal((T, 2, 64) if gqa else (T, 64))).cuda()
+    q = bf16(g.standard_normal((T, 6 if gqa else 5, 64))).cuda()
+    both = step.append(0, a, b, q=q)
+    rows = [c.rows(p, 0, 0, 50) for p in range(len(c.planes))]
+    for p in range(len(c.planes)):
+        plant(c, p, 0, 0, 55, slice(None), 3.0)
+    assert torch.equal(step.append(0, q=q), both)
+    assert not np.array_equal(c.rows(0, 0, 0, 50), rows[0])   # no row was written
+    assert step.append(0, a, b) is None
+    for p in range(len(c.planes)):
+        assert np.array_equal(c.rows(p, 0, 0, 50), rows[p])
+    step.close()
+    c.pool.close()
+
+
+@pytest.mark.parametrize("gqa", [False, True])
+@pytest.mark.parametrize("P", [1, 16])
+def test_a_begin_right_behind_an_eviction(gqa, P):
+    """Nothing reads the sequence in between: at page size 1 its length is still on
+    the device."""
+    c = Cache(gqa, P, [300, 40], seed=P, kv_heads=2, dim=64, rot=64, room=40, spare=-(-360 // P) + 4)
+    step = c.pool.step(4, max_tokens=8)
+    g = np.random.default_rng(6)
+    keep = (g.random(300) > 0.4).astype(np.uint8)
+    want = [c.rows(p, 0, 0)[keep == 1] for p in range(len(c.planes))]
+    mask = torch.from_numpy(keep).cuda()
+    q = _queries(c, 5, 4)
+    a = bf16(g.standard_normal((5, 2, 64) if gqa else (5, 512))).cuda()
+    b = bf16(g.standard_normal((5, 2, 64) if gqa else (5, 64))).cuda()
+    c.pool.evict([0], mask, [0])
+    step.begin([0, 1], [3, 2])
+    step.append(0, a, b)
+    out, lse = step.attend(0, q, scale=0.1, lse=True)
+    torch.cuda.synchronize()
+    n = int(keep.sum())
+    assert c.pool.seq_get(0)[:2] == (n + 3, 303)
+    for p in range(len(c.planes)):
+        assert np.array_equal(c.rows(p, 0, 0, 0, n), want[p])
+    c.check_attend(out, lse, q, [0, 1], [3, 2], 0, 0.1)
+    step.close()
+    c.pool.close()
+
+
 @pytest.mark.parametrize("gqa,heads,kv,dim,P,lens,counts,window", [
     (False, 16, 1, 576, 64, [40007], [1], 0),
     (False, 8, 1, 576, 16, [9000, 5, 20001], [1, 1, 2], 0),
