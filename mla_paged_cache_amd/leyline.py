@@ -712,23 +712,35 @@ class Step:
         return self.tokens
 
     def _rows(self, t, name: str, tail, dtype):
-        """Token count of a [tokens][*tail] tensor on the pool's device."""
+        """(tokens, address, token stride, head stride) of a [tokens][*tail] tensor on
+        the pool's device (tail: heads and width, or a width alone)."""
+        # once per tensor of every call: each attribute is read once
         try:
-            ok = t.dtype is dtype and t.shape[1:] == tail and t.device == self.device and t.stride(-1) == 1
-        except (AttributeError, IndexError):   # no tensor, or one without axes
+            if len(tail) == 2:
+                n, h, d = t.shape
+                ts, hs, one = t.stride()
+                ok = h == tail[0] and d == tail[1]
+            else:
+                n, d = t.shape
+                ts, one = t.stride()
+                hs, ok = 0, d == tail[0]
+            ok = ok and one == 1 and t.dtype is dtype and t.device == self.device
+        except (AttributeError, TypeError, ValueError):   # no tensor, or one of other axes
             ok = False
         if not ok:
             raise ValueError(f"{name}: need a {dtype} tensor [tokens]{list(tail)} on {self.device} with a dense last axis")
-        return t.shape[0]
+        return n, t.data_ptr(), ts, hs
 
     def _weight(self, w, name: str, n: int):
+        """(address, LL_TYPE_*) of a norm's weight."""
         try:
-            ok = w.dtype in (self._bf16, self._f32) and w.shape == (n,) and w.device == self.device and w.stride(0) == 1
+            dt = w.dtype
+            ok = (dt is self._bf16 or dt is self._f32) and w.shape == (n,) and w.device == self.device and w.is_contiguous()
         except AttributeError:   # no tensor
             ok = False
         if not ok:
             raise ValueError(f"{name}: need a dense bf16 or float32 tensor [{n}] on {self.device}")
-        return w.data_ptr()
+        return w.data_ptr(), 1 if dt is self._f32 else 0
 
     def append(self, layer: int, a=None, b=None, norm=None, q=None, q_out=None, q_norm=None, eps: float = 1e-6,
                stream=None):
@@ -739,39 +751,31 @@ class Step:
         [T][heads][head_dim].  norm / q_norm: RMS-norm weights (bf16 or float32) of
         c_kv or the K heads / the query heads (GQA).  Returns q_out (new when not
         given; q itself turns the queries in place), or None without q."""
-        bf16, gqa = self._bf16, self.gqa
+        bf16 = self._bf16
         room = 1 << 62
         a_ptr = a_ts = a_hs = b_ptr = b_ts = b_hs = 0
         if a is not None and b is not None:
-            room = min(self._rows(a, "a", self._a_tail, bf16), self._rows(b, "b", self._b_tail, bf16))
-            a_ptr, b_ptr = a.data_ptr(), b.data_ptr()
-            if gqa:
-                a_ts, a_hs, _ = a.stride()
-                b_ts, b_hs, _ = b.stride()
-            else:
-                a_ts, b_ts = a.stride(0), b.stride(0)
+            room, a_ptr, a_ts, a_hs = self._rows(a, "a", self._a_tail, bf16)
+            n, b_ptr, b_ts, b_hs = self._rows(b, "b", self._b_tail, bf16)
+            room = min(room, n)
         elif a is not None or b is not None:
             raise ValueError("a and b go together")
         norm_ptr = qn_ptr = f32 = 0
         if norm is not None:
-            norm_ptr = self._weight(norm, "norm", self._dv)
-            f32 = 1 if norm.dtype is self._f32 else 0
+            norm_ptr, f32 = self._weight(norm, "norm", self._dv)
         q_ptr = q_ts = q_hs = o_ptr = o_ts = o_hs = 0
         if q is not None:
-            room = min(room, self._rows(q, "q", self._r_tail, bf16))
-            q_ptr = q.data_ptr()
-            q_ts, q_hs, _ = q.stride()
+            n, q_ptr, q_ts, q_hs = self._rows(q, "q", self._r_tail, bf16)
+            room = min(room, n)
             if q_out is None:
                 q_out = self._torch.empty(q.shape, dtype=bf16, device=self.device)
-            elif q_out is not q:
-                room = min(room, self._rows(q_out, "q_out", self._r_tail, bf16))
-            o_ptr = q_out.data_ptr()
-            o_ts, o_hs, _ = q_out.stride()
+            n, o_ptr, o_ts, o_hs = self._rows(q_out, "q_out", self._r_tail, bf16)
+            room = min(room, n)
             if q_norm is not None:
-                qn_ptr = self._weight(q_norm, "q_norm", self._dr)
-                if norm is not None and q_norm.dtype is not norm.dtype:
+                qn_ptr, kind = self._weight(q_norm, "q_norm", self._dr)
+                if norm is not None and kind != f32:
                     raise ValueError("norm and q_norm must have one dtype")
-                f32 = 1 if q_norm.dtype is self._f32 else 0
+                f32 = kind
         elif q_out is not None or q_norm is not None:
             raise ValueError("q_out and q_norm need q")
         try:
@@ -803,34 +807,31 @@ class Step:
         if self.gqa:
             if q_pe is not None:
                 raise ValueError("q_pe is for MLA pools only")
-            room = self._rows(q, "q", self._o_tail, bf16)
+            room, q_ptr, q_ts, q_hs = self._rows(q, "q", self._o_tail, bf16)
         elif q_pe is None:
-            room = self._rows(q, "q", self._q_tail, bf16)
-            p_ptr = q.data_ptr() + 2 * KV_LORA_RANK
-            p_ts, p_hs, _ = q.stride()
+            room, q_ptr, q_ts, q_hs = self._rows(q, "q", self._q_tail, bf16)
+            p_ptr, p_ts, p_hs = q_ptr + 2 * KV_LORA_RANK, q_ts, q_hs
         else:
-            room = min(self._rows(q, "q", self._o_tail, bf16), self._rows(q_pe, "q_pe", self._r_tail, bf16))
-            p_ptr = q_pe.data_ptr()
-            p_ts, p_hs, _ = q_pe.stride()
-        q_ts, q_hs, _ = q.stride()
+            room, q_ptr, q_ts, q_hs = self._rows(q, "q", self._o_tail, bf16)
+            n, p_ptr, p_ts, p_hs = self._rows(q_pe, "q_pe", self._r_tail, bf16)
+            room = min(room, n)
         if out is None:
             out = self._torch.empty((q.shape[0], *self._o_tail), dtype=bf16, device=self.device)
-        else:
-            room = min(room, self._rows(out, "out", self._o_tail, bf16))
-        o_ts, o_hs, _ = out.stride()
+        n, o_ptr, o_ts, o_hs = self._rows(out, "out", self._o_tail, bf16)
+        room = min(room, n)
         l_ptr = 0
         if lse is True:
             lse = self._torch.empty((q.shape[0], self.heads), dtype=self._f32, device=self.device)
         if lse is not None and lse is not False:
-            room = min(room, self._rows(lse, "lse", self._l_tail, self._f32))
+            n, l_ptr, _, _ = self._rows(lse, "lse", self._l_tail, self._f32)
             if not lse.is_contiguous():
                 raise ValueError("lse must be contiguous")
-            l_ptr = lse.data_ptr()
+            room = min(room, n)
         else:
             lse = None
         try:
-            desc = _ATTEND_DESC.pack(room, layer, 1 if causal else 0, window, scale, q.data_ptr(), q_ts, q_hs,
-                                     p_ptr, p_ts, p_hs, out.data_ptr(), o_ts, o_hs, l_ptr)
+            desc = _ATTEND_DESC.pack(room, layer, 1 if causal else 0, window, scale, q_ptr, q_ts, q_hs, p_ptr, p_ts, p_hs,
+                                     o_ptr, o_ts, o_hs, l_ptr)
         except (struct.error, OverflowError) as e:
             raise ValueError(f"layer, window or scale: {e}") from None
         rc = _lib.ll_step_attend(self._h, desc, self._raw_stream(self._dev) if stream is None else stream.cuda_stream)

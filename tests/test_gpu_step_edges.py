@@ -587,3 +587,16 @@ def test_empty_steps_and_refused_begins(gqa):
     with pytest.raises(E):
         step.begin([0], [1])
     step.close()
+
+
+def test_pools_of_2_to_the_31_rows_a_sequence_are_refused():
+    L = need_gpu()
+    k = torch.zeros((1, 2, 256, 1, 16), dtype=torch.bfloat16, device="cuda")
+    for width, ok in ((((1 << 31) - 1024) // 256, False), (((1 << 31) - 1024) // 256 - 1, True)):
+        pool = L.GqaPool(k, k.clone(), torch.full((1, width), -1, dtype=torch.int32, device="cuda"), rotary_dim=16)
+        if ok:
+            pool.step(2, max_tokens=1).close()
+        else:
+            with pytest.raises(L.LeylineError, match="2\\^31"):
+                pool.step(2, max_tokens=1)
+        pool.close()
