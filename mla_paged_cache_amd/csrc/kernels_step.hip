@@ -160,11 +160,17 @@ __device__ __forceinline__ void rotate_band(Vals& x, const Angles<PAIRING>& cs, 
 // before the first is waited for.
 //
 // Bound by the bytes, every value is read once and written once: 24576 tokens of
-// 128 MLA heads whose rotated parts lie in wider heads take 164 us, as a plain
-// copy of those parts does (a dense one of as many bytes: 153 us); 25 thousand
-// tokens of 21 GQA heads of 96 take 30.4 us, 6.3 TB/s.
-template <bool GQA, int PAIRING, int U>
+// 128 MLA heads whose rotated parts lie in wider heads take 155 us (a plain copy of
+// those parts 164, a dense one of as many bytes 153); 25 thousand tokens of 21 GQA
+// heads of 96 take 33.0 us, 5.8 TB/s.
+template <bool GQA, int PAIRING, int U, bool STREAM>
 __global__ __launch_bounds__(256) void append_kernel(AppendLaunch a) {
+  auto load = [](const uint16_t* p) { return *reinterpret_cast<const chunk_t*>(p); };
+  auto store = [](chunk_t v, uint16_t* p) {
+    chunk_t* c = reinterpret_cast<chunk_t*>(p);
+    if constexpr (STREAM) __builtin_nontemporal_store(v, c);
+    else *c = v;
+  };
   const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
   const int lane = threadIdx.x & 63;
   const uint32_t tok = wave / static_cast<uint32_t>(a.waves_per_token);
@@ -177,16 +183,16 @@ __global__ __launch_bounds__(256) void append_kernel(AppendLaunch a) {
   if (!GQA && a.kv_pieces) {
     if (w == 0) {
       const int pe = lane & (kRopeDim / 8 - 1);
-      const chunk_t c = *reinterpret_cast<const chunk_t*>(a.a + t * a.a_ts + lane * 8);
-      const chunk_t d = *reinterpret_cast<const chunk_t*>(a.b + t * a.b_ts + pe * 8);
+      const chunk_t c = load(a.a + t * a.a_ts + lane * 8);
+      const chunk_t d = load(a.b + t * a.b_ts + pe * 8);
       const Angles<PAIRING> an = load_angles<PAIRING>(cs, a.pairs, pe, kRopeDim / 8);
       if (!in_step || row < 0) return;
       Vals x = widen(c), y = widen(d);
       if (a.norm) rms_norm(x, a.norm, a.norm_f32, lane, true, 64, kKvLoraRank, a.eps);
       rotate_band<PAIRING>(y, an, pe, kRopeDim / 8);
-      chunk_t* dst = reinterpret_cast<chunk_t*>(a.k_plane) + int64_t{row} * kRowChunks;
-      dst[lane] = narrow(x);
-      if (lane < kRopeDim / 8) dst[kKvLoraRank / 8 + lane] = narrow(y);
+      uint16_t* dst = a.k_plane + int64_t{row} * kRowElems + lane * 8;
+      store(narrow(x), dst);
+      if (lane < kRopeDim / 8) store(narrow(y), dst + kKvLoraRank);
       return;
     }
     --w;
@@ -205,10 +211,10 @@ __global__ __launch_bounds__(256) void append_kernel(AppendLaunch a) {
     if (p < kv) {
       const int h = min((p < half ? p : p - half) * per_wave + sub, a.kv_heads - 1);
       const uint16_t* src = p < half ? a.a + t * a.a_ts + h * a.a_hs : a.b + t * a.b_ts + h * a.b_hs;
-      c[u] = *reinterpret_cast<const chunk_t*>(src + chunk * 8);
+      c[u] = load(src + chunk * 8);
     } else {
       const int h = min((p - kv) * per_wave + sub, a.heads - 1);
-      c[u] = *reinterpret_cast<const chunk_t*>(a.q + t * a.q_ts + h * a.q_hs + chunk * 8);
+      c[u] = load(a.q + t * a.q_ts + h * a.q_hs + chunk * 8);
     }
   }
   if (!in_step) return;
@@ -227,11 +233,11 @@ __global__ __launch_bounds__(256) void append_kernel(AppendLaunch a) {
     if (p < kv) {
       const int h = (is_v ? p - half : p) * per_wave + sub;
       uint16_t* dst = (is_v ? a.v_plane : a.k_plane) + (int64_t{row} * a.kv_heads + h) * (a.head_chunks * 8);
-      if (h < a.kv_heads && in_head && row >= 0) *reinterpret_cast<chunk_t*>(dst + chunk * 8) = c[u];
+      if (h < a.kv_heads && in_head && row >= 0) store(c[u], dst + chunk * 8);
     } else {
       const int h = (p - kv) * per_wave + sub;
       uint16_t* dst = a.q_out + t * a.qo_ts + h * a.qo_hs;
-      if (h < a.heads && in_head) *reinterpret_cast<chunk_t*>(dst + chunk * 8) = c[u];
+      if (h < a.heads && in_head) store(c[u], dst + chunk * 8);
     }
   }
 }
@@ -246,23 +252,26 @@ hipError_t launch_step_setup(const StepSetupLaunch& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool GQA, int U>
+template <bool GQA, int U, bool STREAM>
 hipError_t launch_pieces(AppendLaunch a, int pairing, hipStream_t s) {
   const int own = GQA ? 0 : a.kv_pieces;   // MLA: the cache row's wave
   a.waves_per_token = own + (a.pieces - own + U - 1) / U;
   const int64_t waves = int64_t{a.capacity} * a.waves_per_token;
   const dim3 g(static_cast<unsigned>((waves + 3) / 4)), b(256);
-  void (*k)(AppendLaunch) = pairing == 0 ? append_kernel<GQA, 0, U> : append_kernel<GQA, 1, U>;
+  void (*k)(AppendLaunch) = pairing == 0 ? append_kernel<GQA, 0, U, STREAM> : append_kernel<GQA, 1, U, STREAM>;
   k<<<g, b, 0, s>>>(a);
   return hipGetLastError();
 }
 
-// Two pieces a wave once one each would fill the chip's 256 x 32 waves: 1152
-// pieces (96 tokens) take 4.1 us one by one and 4.8 us in pairs, 150 thousand take
-// 36.8 and 30.4 us.  MLA: one (its prompts 164 us, in pairs 171 us).
+// Once one piece a wave would fill the chip's 256 x 32 waves, four of them, and
+// stores past the caches: 1152 pieces (96 tokens) take 4.1 us one by one and 4.8 us
+// in pairs; 150 thousand take 50.1 us one by one, 38.2 in pairs, 36.6 by four, and
+// 33.0 by four with streamed stores (streamed loads: 34.6).  MLA: one piece (its
+// prompts 164.6 us, streamed stores 155.0, loads too 159.4, then in pairs 163.1).
 hipError_t launch_append(const AppendLaunch& a, bool gqa, int pairing, hipStream_t s) {
-  if (!gqa) return launch_pieces<false, 1>(a, pairing, s);
-  return int64_t{a.capacity} * a.pieces <= 256 * 32 ? launch_pieces<true, 1>(a, pairing, s) : launch_pieces<true, 2>(a, pairing, s);
+  const bool many = int64_t{a.capacity} * a.pieces > 256 * 32;
+  if (gqa) return many ? launch_pieces<true, 4, true>(a, pairing, s) : launch_pieces<true, 1, false>(a, pairing, s);
+  return many ? launch_pieces<false, 1, true>(a, pairing, s) : launch_pieces<false, 1, false>(a, pairing, s);
 }
 
 }  // namespace ll

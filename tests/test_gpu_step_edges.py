@@ -600,3 +600,52 @@ def test_pools_of_2_to_the_31_rows_a_sequence_are_refused():
             with pytest.raises(L.LeylineError, match="2\\^31"):
                 pool.step(2, max_tokens=1)
         pool.close()
+
+
+@pytest.mark.parametrize("gqa,heads,kv,dim,rot,pairing,norm", [
+    (False, 43, 1, 576, 64, 0, True), (False, 40, 1, 576, 64, 1, False),
+    (True, 15, 3, 96, 32, 0, True), (True, 14, 7, 64, 64, 1, True), (True, 9, 3, 256, 64, 1, False),
+])
+def test_append_of_many_tokens(gqa, heads, kv, dim, rot, pairing, norm):
+    """Prompts of odd lengths, enough heads and tokens for more than one round of
+    the chip's waves (the kernel's other form); one call of rows or queries alone."""
+    say(f"many tokens gqa={gqa} heads={heads}/{kv} dim={dim} pairing={pairing} norm={norm}")
+    lens, counts = [5, 0, 77], [1501, 800, 0]
+    c = Cache(gqa, 16, lens, seed=3, kv_heads=kv, dim=dim, rot=rot, pairing=pairing, room=1600, spare=150)
+    step = c.pool.step(heads, max_tokens=2400)
+    T = step.begin([0, 1, 2], counts)
+    g = np.random.default_rng(5)
+    dq = dim if gqa else 64
+    a = bf16(g.standard_normal((T, kv, dim) if gqa else (T, 512))).cuda()
+    b = bf16(g.standard_normal((T, kv, dim) if gqa else (T, 64))).cuda()
+    wide = bf16(g.standard_normal((T, heads, dq + 8))).cuda()
+    q = wide[..., 8:]
+    w = bf16(g.standard_normal(dim if gqa else 512)).cuda() if norm else None
+    qw = bf16(g.standard_normal(dim)).cuda() if norm and gqa else None
+    out = torch.full((T + 2, heads, dq + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    step.append(0, a, b, norm=w, q=q, q_out=out[:, :, :dq], q_norm=qw, eps=1e-5)
+    torch.cuda.synchronize()
+    ang = S.angles(np.concatenate([lens[i] + np.arange(counts[i]) for i in (0, 1)]), rot, 10000.0)
+    ww, qww = (None if x is None else f64(x) for x in (w, qw))
+    want, size = S.heads(f64(q), qww, 1e-5, ang, pairing, rot)
+    got = f64(out)
+    assert (np.abs(got[:T, :, :dq] - want) <= HALF_STEP * np.abs(want) + 2.0 ** -18 * size).all()
+    assert (got[T:] == 7).all() and (got[..., dq:] == 7).all()
+    lo = 0
+    for i in (0, 1):
+        sl, at = slice(lo, lo + counts[i]), (i, lens[i], lens[i] + counts[i])
+        if gqa:
+            c.check_rows(0, 0, *at, *S.heads(f64(a[sl]), ww, 1e-5, ang[sl], pairing, rot))
+            assert np.array_equal(c.rows(1, 0, *at), f64(b[sl]))
+        else:
+            lat = S.norm(f64(a[sl])[:, None], ww, 1e-5)
+            pe, sp = S.heads(f64(b[sl])[:, None], None, 0, ang[sl], pairing)
+            c.check_rows(0, 0, *at, np.concatenate([lat, pe], -1), np.concatenate([np.abs(lat), sp], -1))
+        lo += counts[i]
+    rows = [c.rows(p, 0, 0) for p in range(len(c.planes))]
+    again = step.append(0, q=q, q_norm=qw, eps=1e-5)
+    assert torch.equal(again, out[:T, :, :dq])
+    step.append(0, a, b, norm=w, eps=1e-5)
+    assert all(np.array_equal(x, c.rows(p, 0, 0)) for p, x in enumerate(rows))
+    step.close()
+    c.pool.close()
