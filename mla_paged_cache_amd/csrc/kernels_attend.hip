@@ -207,6 +207,11 @@ struct Shape {
   static constexpr int PIECES = MLA ? BN / WAVES + (BN / 8 + WAVES - 1) / WAVES : BN * ROWCH / 64 / WAVES;
   static constexpr int KVT = BN / KW;                        // cached rows of a tile per wave
   static constexpr int TILE = 16 * QN * QW;                  // query rows
+  // Below the largest tile a sequence is one tile (attend_tile), and its cached rows
+  // are read once: past the caches 257, 90 and 413 us (64 MLA tokens over up to 32768
+  // rows, one GQA token over 131072, 128 over up to 8192), otherwise 290, 101 and
+  // 458.  Chunks of several tiles read rows again (2130 past the caches, 2004).
+  static constexpr bool ONCE = TILE < (MLA || DP > 128 ? 128 : 256);
   // the sums fill the accumulation registers, which only assembly can ask for
   static constexpr bool ACC = QN * DV / 4 >= 256;
   // then the waves share the weights through LDS, and each sums the columns
@@ -225,14 +230,24 @@ struct Shape {
 // off: the lane's byte offset).  As assembly, because the compiler otherwise waits
 // for every such load before each transposing LDS read; it has no result
 // register, and the kernel waits for it itself (`landed`, then a barrier).
+// ONCE: nothing else of the launch reads the bytes, so that they need not stay in
+// the caches.
+template <bool ONCE>
 __device__ __forceinline__ void load_lds(lds_ptr dst, const void* base, uint32_t off) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
   // (five wait states between a vector instruction that writes `base` and the load)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(at), "v"(off), "s"(base) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
 }
+template <bool ONCE>
 __device__ __forceinline__ void load_lds(lds_ptr dst, const void* src) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(at), "v"(src) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
 }
 
 __device__ __forceinline__ void load_lds4(lds_ptr dst, const void* src) {
@@ -253,13 +268,13 @@ __device__ __forceinline__ void load_mla_piece(int i, uint64_t row, lds_ptr dst,
     // spread over the upper half)
     const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, r))) << 32 |
                         static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, r));
-    load_lds(dst + r * 1024, reinterpret_cast<const void*>(at), static_cast<uint32_t>(lane ^ swizzle<64>(r)) * 16);
+    load_lds<S::ONCE>(dst + r * 1024, reinterpret_cast<const void*>(at), static_cast<uint32_t>(lane ^ swizzle<64>(r)) * 16);
   } else {                      // 8 rows' k_pe
     const int b = (i - S::BN / S::WAVES) * S::WAVES + wave;
     if (S::BN / 8 % S::WAVES != 0 && b >= S::BN / 8) return;
     const int r = b * 8 + (lane >> 3);
     const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(__shfl(hi, r))) << 32 | static_cast<uint32_t>(__shfl(lo, r));
-    load_lds(dst + S::MAIN + b * 1024, reinterpret_cast<const void*>(at + kKvLoraRank * 2 + ((lane & 7) ^ swizzle<8>(r)) * 16));
+    load_lds<S::ONCE>(dst + S::MAIN + b * 1024, reinterpret_cast<const void*>(at + kKvLoraRank * 2 + ((lane & 7) ^ swizzle<8>(r)) * 16));
   }
 }
 // K and V of one KV head (k and v: its first value in row 0; row: the byte
@@ -275,8 +290,8 @@ __device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const u
   const uint64_t off = (static_cast<uint64_t>(static_cast<uint32_t>(__shfl(hi, r))) << 32 |
                         static_cast<uint32_t>(__shfl(lo, r))) + c * 16;
   if (c < live) {
-    load_lds(dst + b * 1024, reinterpret_cast<const char*>(k) + off);
-    load_lds(dst + S::MAIN + b * 1024, reinterpret_cast<const char*>(v) + off);
+    load_lds<S::ONCE>(dst + b * 1024, reinterpret_cast<const char*>(k) + off);
+    load_lds<S::ONCE>(dst + S::MAIN + b * 1024, reinterpret_cast<const char*>(v) + off);
   }
 }
 
