@@ -314,8 +314,8 @@ __device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const u
 // and the item falls back to reading exactly the rows each query sees.
 //
 // One token per sequence is bound by reading the cache: 64 MLA sequences of up to
-// 32768 rows 286 us (5.3 TB/s), 128 GQA ones of up to 8192 rows and 8 heads of 128
-// 458 us (5.95 TB/s; a large read reaches 6.9).  Chunks are bound by the matrix
+// 32768 rows 245 us (6.2 TB/s), 128 GQA ones of up to 8192 rows and 8 heads of 128
+// 408 us (6.7 TB/s; a large read reaches 6.9).  Chunks are bound by the matrix
 // units and what feeds them: 2 x 2048 MLA tokens of 16 heads over up to 16384 rows
 // 1603 us (43% busy), 4096 GQA tokens of 32 heads over 32768 rows 1977 us (44%).
 template <typename S>
@@ -869,7 +869,8 @@ hipError_t launch_shape(const AttendLaunch& a, hipStream_t s) {
 //  * many rows: two tiles of 16 queries a wave halve the reads of LDS per product.
 // Four tiles in LDS: with three, single tokens wait for memory (those 64 MLA tokens
 // 340 us against 280, 128 GQA tokens over up to 8192 rows 559 against 455); smaller
-// tiles, more of them (32 rows, 7 or 9 tiles, GQA): 490 and 466 us.
+// tiles, more of them (32 rows, 7 or 9 tiles, GQA): 490 and 466 us.  (These with
+// rows kept in the caches, see ONCE.)
 template <bool MLA, int DP>
 hipError_t launch_tile(const AttendLaunch& a, hipStream_t s) {
   constexpr bool WIDE = MLA || DP > 128;   // rows of 1 KiB: tiles of 32
