@@ -9,6 +9,7 @@ exceptions.  If the library is missing, importing this module fails loudly.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -225,6 +226,18 @@ def _stream_handle(stream, device: int) -> int:
     if raw is not None:
         return raw(device)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on(stream, device: int):
+    """Context in which new tensors belong to `stream`, where the call that fills
+    them runs (None: the current one).  A block of another stream may have work of
+    that stream still queued on it, and goes back to that stream when dropped."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return torch.cuda.stream(stream)
 
 
 def rope_delta_table(delta: int, rope_dim: int = ROPE_DIM, base: float = 10000.0):
@@ -665,7 +678,11 @@ class Step:
     used; under graph capture they hold max_tokens rows).
 
     Inputs may be views (e.g. of one projection's output): the last axis is dense,
-    the other strides are multiples of 8 values and the data is 16-byte aligned."""
+    the other strides are multiples of 8 values and the data is 16-byte aligned.
+
+    A call runs on `stream` (None: the current one), and results that it allocates
+    belong to that stream.  Inputs made on another one, and results read on another
+    one, are the caller's to order and to keep (torch's record_stream)."""
 
     def __init__(self, pool: Pool, heads: int, max_seqs: int, max_tokens: int):
         import torch
@@ -731,6 +748,13 @@ class Step:
             raise ValueError(f"{name}: need a {dtype} tensor [tokens]{list(tail)} on {self.device} with a dense last axis")
         return n, t.data_ptr(), ts, hs
 
+    def _new(self, shape, dtype, stream):
+        """A result for a call on `stream`."""
+        if stream is None:
+            return self._torch.empty(shape, dtype=dtype, device=self.device)
+        with _on(stream, self._dev):
+            return self._torch.empty(shape, dtype=dtype, device=self.device)
+
     def _weight(self, w, name: str, n: int):
         """(address, LL_TYPE_*) of a norm's weight."""
         try:
@@ -768,7 +792,7 @@ class Step:
             n, q_ptr, q_ts, q_hs = self._rows(q, "q", self._r_tail, bf16)
             room = min(room, n)
             if q_out is None:
-                q_out = self._torch.empty(q.shape, dtype=bf16, device=self.device)
+                q_out = self._new(q.shape, bf16, stream)
             n, o_ptr, o_ts, o_hs = self._rows(q_out, "q_out", self._r_tail, bf16)
             room = min(room, n)
             if q_norm is not None:
@@ -816,12 +840,12 @@ class Step:
             n, p_ptr, p_ts, p_hs = self._rows(q_pe, "q_pe", self._r_tail, bf16)
             room = min(room, n)
         if out is None:
-            out = self._torch.empty((q.shape[0], *self._o_tail), dtype=bf16, device=self.device)
+            out = self._new((q.shape[0], *self._o_tail), bf16, stream)
         n, o_ptr, o_ts, o_hs = self._rows(out, "out", self._o_tail, bf16)
         room = min(room, n)
         l_ptr = 0
         if lse is True:
-            lse = self._torch.empty((q.shape[0], self.heads), dtype=self._f32, device=self.device)
+            lse = self._new((q.shape[0], self.heads), self._f32, stream)
         if lse is not None and lse is not False:
             n, l_ptr, _, _ = self._rows(lse, "lse", self._l_tail, self._f32)
             if not lse.is_contiguous():
