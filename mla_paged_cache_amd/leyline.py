@@ -432,7 +432,8 @@ class Pool:
         if out is not None:
             shape = (self.num_layers, n, self.heads, self.head_dim) if self.gqa else (self.num_layers, n, ROW)
             if out is True:
-                out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+                with _on(stream, self._dev):
+                    out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
             if not isinstance(out, torch.Tensor) or out.dtype != torch.bfloat16 or out.device != self.device \
                     or tuple(out.shape) != shape or not out[0].is_contiguous() or out.stride(0) < out[0].numel():
                 raise ValueError(f"out must be a bf16 tensor {shape} on {self.device} with contiguous layers")
@@ -623,11 +624,12 @@ class KvsMask:
         result).  Returns (death int32 [n][n_pad], status int32 [n]) CUDA
         tensors."""
         import torch
-        logs = rollouts if isinstance(rollouts, _Logs) else self.upload_logs(rollouts)
         dev = self._tdev
-        if out is None:
-            out = (torch.empty((logs.n, n_pad), dtype=torch.int32, device=dev),
-                   torch.empty(logs.n, dtype=torch.int32, device=dev))
+        with _on(stream, self.device):
+            logs = rollouts if isinstance(rollouts, _Logs) else self.upload_logs(rollouts)
+            if out is None:
+                out = (torch.empty((logs.n, n_pad), dtype=torch.int32, device=dev),
+                       torch.empty(logs.n, dtype=torch.int32, device=dev))
         death, status = out
         _require(death, "death", torch.int32, (logs.n, n_pad), dev)
         _require(status, "status", torch.int32, (logs.n,), dev)
@@ -647,8 +649,9 @@ class KvsMask:
         nq, nk = -(-n_pad // block_q), -(-n_pad // block_k)
         kw = dict(dtype=torch.int32, device=death.device)
         if out is None:
-            pn, fn = torch.zeros((n, nq), **kw), torch.zeros((n, nq), **kw)
-            pi, fi = torch.full((n, nq, nk), -1, **kw), torch.full((n, nq, nk), -1, **kw)
+            with _on(stream, self.device):
+                pn, fn = torch.zeros((n, nq), **kw), torch.zeros((n, nq), **kw)
+                pi, fi = torch.full((n, nq, nk), -1, **kw), torch.full((n, nq, nk), -1, **kw)
         else:
             pn, pi, fn, fi = out
             for x, shape in ((pn, (n, nq)), (pi, (n, nq, nk)), (fn, (n, nq)), (fi, (n, nq, nk))):
@@ -664,7 +667,8 @@ class KvsMask:
         self._check_death(death)
         n, n_pad = death.shape
         if out is None:
-            out = torch.empty((n, n_pad, n_pad // 32), dtype=torch.int32, device=death.device)
+            with _on(stream, self.device):
+                out = torch.empty((n, n_pad, n_pad // 32), dtype=torch.int32, device=death.device)
         _require(out, "out", torch.int32, (n, n_pad, n_pad // 32), self._tdev)
         _check(_lib.kvs_dense_mask(self._h, death.data_ptr(), n, n_pad, out.data_ptr(), _stream_handle(stream, self.device)))
         return out

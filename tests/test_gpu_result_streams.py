@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 from gpu_common import need_gpu, say, torch
+from test_gpu_kvs_mask import _logs
 from test_gpu_step import Cache, _queries, bf16, f64
 
 pytestmark = pytest.mark.gpu
@@ -41,4 +42,34 @@ def test_a_steps_results(gqa):
     assert np.array_equal(f64(got_q), want_q)
     c.check_attend(out, lse, q, [0, 1], [1, 2], 0, 0.1)
     step.close()
+    c.pool.close()
+
+
+def test_a_masks_results():
+    """The block mask's indices are filled before the call, on the same stream."""
+    L = need_gpu()
+    rolls = _logs(0, [256, 200, 131], ["window", "half", "pick"], budget=120, turn_lo=4, turn_hi=40, every=3)
+    ctx, side = L.KvsMask(0), torch.cuda.Stream()
+    death, status = ctx.death_times(rolls, 256)
+    lists, bits = ctx.block_mask(death, 16, 16), ctx.dense_mask(death)
+    torch.cuda.synchronize()
+    i32 = torch.int32
+    queue_a_write([(t.shape, i32) for t in (death, status, *lists, bits)])
+    got = [*ctx.death_times(rolls, 256, stream=side), *ctx.block_mask(death, 16, 16, stream=side),
+           ctx.dense_mask(death, stream=side)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, (death, status, *lists, bits)))
+    ctx.close()
+
+
+def test_gathered_rows():
+    c = Cache(False, 16, [300], seed=2, layers=2)
+    side = torch.cuda.Stream()
+    angles = torch.arange(300, dtype=torch.int64, device="cuda")
+    want = c.pool.rope_rows(0, 0, angles, out=True)
+    torch.cuda.synchronize()
+    queue_a_write([(want.shape, torch.bfloat16)])
+    got = c.pool.rope_rows(0, 0, angles, out=True, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
     c.pool.close()
