@@ -136,8 +136,11 @@ typedef struct {
  * first 512 values, shared by all heads; GQA: head h reads KV head
  * h / (num_heads / num_kv_heads).  Rows that a token does not see never reach its
  * result, whatever they hold; a token that sees none gets zeros and lse = -inf, and
-so does one whose scores are all -inf.  out may not overlap q or q_pe.  Results do not depend on the other sequences'
- * contents, and the same call on the same plan gives the same bits.
+ * so does one whose scores are all -inf.  (A seen row with a score of -inf next to
+ * others with finite ones has weight 0; whether 0 times an infinity in its value
+ * makes the result NaN depends on the plan.)  out may not overlap q or q_pe.
+ * Results do not depend on the other sequences' contents, and the same call on the
+ * same plan gives the same bits.
  * Errors: LL_EINVAL (layer, too few tokens, NULL or misaligned pointer or stride, overlapping out
  * rows, a scale that is not finite, window < 0 or without causal, a changed
  * sequence, no begin yet), LL_EDEVICE. */

@@ -132,10 +132,13 @@ __device__ void attend_rows(const AttendLaunch& a, const AttendItem& it, const S
         a.part_ml[at * 2 + 1] = l;
       }
     } else {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = 1.f / l;
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = to_bf16(o.v[2 * i] * inv) | (to_bf16(o.v[2 * i + 1] * inv) << 16);
+      for (int i = 0; i < 4; ++i) {
+        w[i] = to_bf16(o.v[2 * i] * inv) | (to_bf16(o.v[2 * i + 1] * inv) << 16);
+        if (l == 0.f) w[i] = 0u;   // no weight at all: 0, whatever the sum holds (0 times an infinity)
+      }
       if (live) *reinterpret_cast<chunk_t*>(a.out + t * a.o_ts + h * a.o_hs + lane * 8) = chunk_t{w[0], w[1], w[2], w[3]};
       if (a.lse && lane == 0) a.lse[static_cast<int64_t>(t) * a.heads + h] = l == 0.f ? -__builtin_inff() : (m + __log2f(l)) * kLn2;
     }
@@ -830,13 +833,14 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
           a.part_ml[at * 2 + 1] = sum;
         }
       } else {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = 1.f / sum;
         uint16_t* out = a.out + t * a.o_ts + h * a.o_hs;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           if constexpr (S::ACC) asm volatile("" : "+a"(o[d][n]));
-          if (col + d * 16 < dv)
-            *reinterpret_cast<bf16x4*>(out + col + d * 16) = __builtin_convertvector(o[d][n] * inv, bf16x4);
+          // no weight at all: 0, whatever the sum holds (0 times an infinity)
+          const f32x4 x = sum == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o[d][n] * inv;
+          if (col + d * 16 < dv) *reinterpret_cast<bf16x4*>(out + col + d * 16) = __builtin_convertvector(x, bf16x4);
           __builtin_amdgcn_sched_barrier(0);
         }
         if (a.lse && col == 0) a.lse[t * a.heads + h] = sum == 0.f ? -__builtin_inff() : (top + __log2f(sum)) * kLn2;
