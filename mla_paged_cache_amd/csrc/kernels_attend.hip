@@ -229,6 +229,11 @@ struct Shape {
   static_assert(LOADS * (AHEAD - 1) < 64, "the wait counter's range");
 };
 
+// The assembly below declares that it writes m0.  The compiler keeps no value there
+// between its own uses (and warns that a reserved register is declared), but it may
+// share one setting of m0 between several of those, which the declaration ends.
+#pragma clang diagnostic ignored "-Winline-asm"
+
 // 64 x 16 bytes from memory straight into LDS at `dst` + 16 * lane (base: uniform;
 // off: the lane's byte offset).  As assembly, because the compiler otherwise waits
 // for every such load before each transposing LDS read; it has no result
@@ -240,22 +245,22 @@ __device__ __forceinline__ void load_lds(lds_ptr dst, const void* base, uint32_t
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
   // (five wait states between a vector instruction that writes `base` and the load)
   if constexpr (ONCE)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(at), "v"(off), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(at), "v"(off), "s"(base) : "m0", "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "m0", "memory");
 }
 template <bool ONCE>
 __device__ __forceinline__ void load_lds(lds_ptr dst, const void* src) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
   if constexpr (ONCE)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(at), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(at), "v"(src) : "m0", "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "m0", "memory");
 }
 
 __device__ __forceinline__ void load_lds4(lds_ptr dst, const void* src) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "m0", "memory");
 }
 
 // A tile from the cache to LDS: an instruction fills 64 consecutive places, so
@@ -669,39 +674,40 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
             static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds + (tile + S::AHEAD) % S::STAGES * S::STAGE + r0 * 1024)));
         const uint32_t off0 = static_cast<uint32_t>(lane ^ swizzle<64>(r0)) * 16;
         const uint32_t off1 = static_cast<uint32_t>(lane ^ swizzle<64>(r1)) * 16;
+        uint64_t mask;   // the lanes that run, put back after each load
         asm volatile(
-            "s_mov_b32 m0, %26\n\t"
-            "s_nop 1\n\t"
-            "v_mfma_f32_16x16x32_bf16 %0, %16, %18, %0\n\t"
-            "v_mfma_f32_16x16x32_bf16 %1, %16, %19, %1\n\t"
-            "v_mfma_f32_16x16x32_bf16 %2, %16, %20, %2\n\t"
-            "v_mfma_f32_16x16x32_bf16 %3, %16, %21, %3\n\t"
-            "s_mov_b64 exec, %32\n\t"
-            "global_load_lds_dwordx4 %28, %30\n\t"
-            "s_mov_b64 exec, -1\n\t"
-            "v_mfma_f32_16x16x32_bf16 %4, %16, %22, %4\n\t"
-            "v_mfma_f32_16x16x32_bf16 %5, %16, %23, %5\n\t"
-            "v_mfma_f32_16x16x32_bf16 %6, %16, %24, %6\n\t"
-            "v_mfma_f32_16x16x32_bf16 %7, %16, %25, %7\n\t"
             "s_mov_b32 m0, %27\n\t"
-            "v_mfma_f32_16x16x32_bf16 %8, %17, %18, %8\n\t"
-            "v_mfma_f32_16x16x32_bf16 %9, %17, %19, %9\n\t"
-            "v_mfma_f32_16x16x32_bf16 %10, %17, %20, %10\n\t"
-            "v_mfma_f32_16x16x32_bf16 %11, %17, %21, %11\n\t"
-            "s_mov_b64 exec, %32\n\t"
+            "s_nop 1\n\t"
+            "v_mfma_f32_16x16x32_bf16 %0, %17, %19, %0\n\t"
+            "v_mfma_f32_16x16x32_bf16 %1, %17, %20, %1\n\t"
+            "v_mfma_f32_16x16x32_bf16 %2, %17, %21, %2\n\t"
+            "v_mfma_f32_16x16x32_bf16 %3, %17, %22, %3\n\t"
+            "s_and_saveexec_b64 %16, %33\n\t"
             "global_load_lds_dwordx4 %29, %31\n\t"
-            "s_mov_b64 exec, -1\n\t"
-            "v_mfma_f32_16x16x32_bf16 %12, %17, %22, %12\n\t"
-            "v_mfma_f32_16x16x32_bf16 %13, %17, %23, %13\n\t"
-            "v_mfma_f32_16x16x32_bf16 %14, %17, %24, %14\n\t"
-            "v_mfma_f32_16x16x32_bf16 %15, %17, %25, %15\n\t"
+            "s_mov_b64 exec, %16\n\t"
+            "v_mfma_f32_16x16x32_bf16 %4, %17, %23, %4\n\t"
+            "v_mfma_f32_16x16x32_bf16 %5, %17, %24, %5\n\t"
+            "v_mfma_f32_16x16x32_bf16 %6, %17, %25, %6\n\t"
+            "v_mfma_f32_16x16x32_bf16 %7, %17, %26, %7\n\t"
+            "s_mov_b32 m0, %28\n\t"
+            "v_mfma_f32_16x16x32_bf16 %8, %18, %19, %8\n\t"
+            "v_mfma_f32_16x16x32_bf16 %9, %18, %20, %9\n\t"
+            "v_mfma_f32_16x16x32_bf16 %10, %18, %21, %10\n\t"
+            "v_mfma_f32_16x16x32_bf16 %11, %18, %22, %11\n\t"
+            "s_and_saveexec_b64 %16, %33\n\t"
+            "global_load_lds_dwordx4 %30, %32\n\t"
+            "s_mov_b64 exec, %16\n\t"
+            "v_mfma_f32_16x16x32_bf16 %12, %18, %23, %12\n\t"
+            "v_mfma_f32_16x16x32_bf16 %13, %18, %24, %13\n\t"
+            "v_mfma_f32_16x16x32_bf16 %14, %18, %25, %14\n\t"
+            "v_mfma_f32_16x16x32_bf16 %15, %18, %26, %15\n\t"
             "s_nop 9"
             : "+a"(o[i][0]), "+a"(o[i][1]), "+a"(o[i][2]), "+a"(o[i][3]), "+a"(o[i][4]), "+a"(o[i][5]), "+a"(o[i][6]),
               "+a"(o[i][7]), "+a"(o[i + 1][0]), "+a"(o[i + 1][1]), "+a"(o[i + 1][2]), "+a"(o[i + 1][3]), "+a"(o[i + 1][4]),
-              "+a"(o[i + 1][5]), "+a"(o[i + 1][6]), "+a"(o[i + 1][7])
+              "+a"(o[i + 1][5]), "+a"(o[i + 1][6]), "+a"(o[i + 1][7]), "=&s"(mask)
             : "v"(y[b]), "v"(y[b + 1]), "v"(w[0]), "v"(w[1]), "v"(w[2]), "v"(w[3]), "v"(w[4]), "v"(w[5]), "v"(w[6]),
               "v"(w[7]), "s"(to), "s"(to + S::WAVES * 1024), "v"(off0), "v"(off1), "s"(at0), "s"(at1), "s"(lanes)
-            : "memory");
+            : "m0", "scc", "memory");
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
