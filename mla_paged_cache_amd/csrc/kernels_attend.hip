@@ -42,7 +42,7 @@ __device__ __forceinline__ Seen item_share(const AttendLaunch& a, const AttendIt
   const Seen f = rows_seen(a, it, it.row0), l = rows_seen(a, it, last);
   const int shares = it.splits >> 16, c = it.splits & 0xFFFF;
   const int lo = f.lo - f.lo % grain;
-  const int64_t per = (static_cast<int64_t>(l.hi - lo + shares - 1) / shares + grain - 1) / grain * grain;
+  const int64_t per = share_rows(l.hi - lo, shares, grain);
   Seen s;
   s.lo = static_cast<int>(min(lo + c * per, static_cast<int64_t>(l.hi)));
   s.hi = static_cast<int>(min(lo + (c + 1) * per, static_cast<int64_t>(l.hi)));

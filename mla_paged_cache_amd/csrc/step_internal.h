@@ -35,6 +35,12 @@ struct alignas(16) AttendItem {
 };
 static_assert(sizeof(AttendItem) == 32, "two 16-byte words");
 
+// Rows of each of a tile's shares: equal, in multiples of `grain`.  (In 64 bits: the
+// rows alone may come within 1025 of 2^31.)
+constexpr int64_t share_rows(int64_t rows, int64_t shares, int64_t grain) {
+  return ((rows + shares - 1) / shares + grain - 1) / grain * grain;
+}
+
 struct StepCounts {
   int32_t tokens;
   int32_t items;

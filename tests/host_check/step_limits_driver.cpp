@@ -1,0 +1,35 @@
+// The serving step's host side at its limits, on the stand-ins and the small world
+// of step_driver.cpp.  Usage: step_limits_driver <check> (see main).
+#define main step_driver_main
+#include "step_driver.cpp"
+#undef main
+
+#include "../../mla_paged_cache_amd/csrc/pool_internal.h"
+
+namespace {
+
+// Shares of a tile cover its rows in order, whole grains each, also at the longest
+// sequence that a step takes and the most shares that a tile is split into.
+void shares_of_long_tiles() {
+  for (const int64_t rows : {int64_t{1}, int64_t{63}, int64_t{64}, int64_t{65}, int64_t{130816}, int64_t{INT32_MAX} - 1024})
+    for (const int64_t shares : {1, 2, 3, 255, 1025, 2048})
+      for (const int64_t grain : {32, 64}) {
+        const int64_t per = ll::share_rows(rows, shares, grain);
+        CHECK(per > 0 && per % grain == 0 && per * shares >= rows);
+        CHECK(per == grain || (per - grain) * shares < rows);
+      }
+  // 2^31 - 1025 rows in 2048 shares: 1048575.5 rows each, in grains of 64
+  CHECK(ll::share_rows(int64_t{INT32_MAX} - 1024, 2048, 64) == 1048576);
+}
+
+}  // namespace
+
+int main(int argc, char** argv) {
+  const std::map<std::string, void (*)()> checks = {
+      {"shares_of_long_tiles", shares_of_long_tiles},
+  };
+  const auto c = argc == 2 ? checks.find(argv[1]) : checks.end();
+  if (c == checks.end()) return 2;
+  c->second();
+  return 0;
+}
