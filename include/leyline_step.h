@@ -119,7 +119,7 @@ typedef struct {
   int32_t layer;
   int32_t causal;             /* 1: a token sees the rows up to its own; 0: every row of its sequence */
   int64_t window;             /* > 0 (with causal): only the last `window` of those; 0: all */
-  float scale;                /* of the scores, finite */
+  float scale;                /* of the scores; finite, and so is scale * log2 e */
   const void* q;              /* MLA: [T][num_heads][512], in the latent space; GQA: [T][num_heads][head_dim] */
   int64_t q_token_stride, q_head_stride;
   const void* q_pe;           /* MLA: the rotated part [T][num_heads][64]; GQA: NULL */

@@ -15,7 +15,6 @@
 namespace ll {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kAttendThreads = 256;
 

@@ -538,7 +538,8 @@ ll_status ll_step_attend(ll_step* s, const ll_attend_desc* d, void* stream) try 
   if (d->layer < 0 || d->layer >= p->desc.num_layers) return fail(LL_EINVAL, "layer %d out of range", d->layer);
   if (d->causal != 0 && d->causal != 1) return fail(LL_EINVAL, "causal must be 0 or 1");
   if (d->window < 0 || (d->window > 0 && !d->causal)) return fail(LL_EINVAL, "window must be >= 0, and needs causal");
-  if (!std::isfinite(d->scale)) return fail(LL_EINVAL, "scale is not finite");
+  // (the kernels keep scores in base 2)
+  if (!std::isfinite(d->scale * ll::kLog2e)) return fail(LL_EINVAL, "scale, times log2 e, is not finite");
   const int64_t T = capturing ? s->max_tokens : s->tokens;
   if (T == 0) return LL_OK;
   if ((rc = check_plane(d->q, used(d->q_token_stride, T), used(d->q_head_stride, s->heads), "q"))) return rc;

@@ -128,6 +128,7 @@ struct AttendLaunch {
 };
 
 constexpr int kMaxHeadDim = 256;
+constexpr float kLog2e = 1.4426950408889634f;
 
 hipError_t launch_step_setup(const StepSetupLaunch& a, hipStream_t s);
 hipError_t launch_append(const AppendLaunch& a, bool gqa, int pairing, hipStream_t s);

@@ -22,10 +22,33 @@ void shares_of_long_tiles() {
   CHECK(ll::share_rows(int64_t{INT32_MAX} - 1024, 2048, 64) == 1048576);
 }
 
+// Scores are kept in base 2: a scale whose product with log2 e is no number any more
+// would make 0 times infinity of a score of 0.
+void scales() {
+  for (const bool gqa : {false, true}) {
+    World w(gqa, 16);
+    int32_t s0 = -1, one = 1;
+    CHECK(ll_seq_alloc(w.pool, 30, &s0, nullptr) == LL_OK);
+    const ll_step_desc d{w.heads, 1, kTokens};
+    ll_step* s = nullptr;
+    CHECK(ll_step_create(w.pool, &d, &s) == LL_OK && ll_step_begin(s, &s0, &one, 1, 0, nullptr) == LL_OK);
+    for (const float sign : {1.f, -1.f}) {
+      ll_attend_desc t = attend_desc(w, 1);
+      t.scale = sign * 2.3e38f;
+      CHECK(ll_step_attend(s, &t, nullptr) == LL_OK);
+      t.scale = sign * 2.4e38f;   // * 1.4427 = 3.46e38, above 3.403e38
+      CHECK(ll_step_attend(s, &t, nullptr) == LL_EINVAL);
+    }
+    ll_step_destroy(s);
+    ll_pool_destroy(w.pool);
+  }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
   const std::map<std::string, void (*)()> checks = {
+      {"scales", scales},
       {"shares_of_long_tiles", shares_of_long_tiles},
   };
   const auto c = argc == 2 ? checks.find(argv[1]) : checks.end();

@@ -8,7 +8,7 @@ import pytest
 
 from test_host_step import CLANG, CSRC, FLAGS, HC, SAN
 
-CHECKS = ["shares_of_long_tiles"]
+CHECKS = ["scales", "shares_of_long_tiles"]
 
 
 @pytest.fixture(scope="module")
