@@ -388,7 +388,9 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
   // host memory that the commit below needs, before anything changes
   for (int32_t i = 0; i < n; ++i) {
     ll::SeqState& q = p->seqs[seq_ids[i]];
-    q.pages.reserve(q.pages.size() + static_cast<size_t>(ss[i].new_pages));
+    const size_t pages = q.pages.size() + static_cast<size_t>(ss[i].new_pages);
+    // reserve alone would make room for exactly these, and move the list every time
+    if (pages > q.pages.capacity()) q.pages.reserve(std::max(pages, 2 * q.pages.capacity()));
   }
 
   // --- upload and lay out

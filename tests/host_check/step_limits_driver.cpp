@@ -44,10 +44,41 @@ void scales() {
   }
 }
 
+// One token after another at page size 1: a begin's host work does not grow with
+// the pages that the sequence holds, so its page list moves a few times only.
+void growth() {
+  constexpr int kPages = 6000;
+  static char plane[32];
+  void* p = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(plane) + 15) & ~uintptr_t{15});   // never touched
+  std::vector<int32_t> table(kPages, -1);
+  ll_gqa_pool_desc d{};
+  d.num_layers = 1, d.page_size = 1, d.num_pages = kPages, d.max_seqs = 1, d.max_pages_per_seq = kPages;
+  d.num_kv_heads = 1, d.head_dim = 16, d.rotary_dim = 16, d.rope_pairing = LL_ROPE_HALF, d.rope_base = 10000.0;
+  d.k_layer_base = &p, d.v_layer_base = &p, d.page_table = table.data();
+  ll_pool* pool = nullptr;
+  CHECK(ll_pool_create_gqa(&d, &pool) == LL_OK);
+  int32_t seq = -1, one = 1;
+  CHECK(ll_seq_alloc(pool, 1000, &seq, nullptr) == LL_OK);
+  const ll_step_desc sd{1, 1, 4};
+  ll_step* s = nullptr;
+  CHECK(ll_step_create(pool, &sd, &s) == LL_OK);
+  int moves = 0;
+  const int32_t* at = pool->seqs[seq].pages.data();
+  for (int i = 0; i < 5000; ++i) {
+    CHECK(ll_step_begin(s, &seq, &one, 1, 1, nullptr) == LL_OK);
+    if (pool->seqs[seq].pages.data() != at) ++moves;
+    at = pool->seqs[seq].pages.data();
+  }
+  CHECK(pool->seqs[seq].pages.size() == 6000 && moves <= 3);   // 1000 -> 2000 -> 4000 -> 8000
+  ll_step_destroy(s);
+  ll_pool_destroy(pool);
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
   const std::map<std::string, void (*)()> checks = {
+      {"growth", growth},
       {"scales", scales},
       {"shares_of_long_tiles", shares_of_long_tiles},
   };

@@ -8,7 +8,7 @@ import pytest
 
 from test_host_step import CLANG, CSRC, FLAGS, HC, SAN
 
-CHECKS = ["scales", "shares_of_long_tiles"]
+CHECKS = ["growth", "scales", "shares_of_long_tiles"]
 
 
 @pytest.fixture(scope="module")
