@@ -336,6 +336,7 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
   if ((rc = ll::pool_enter(p))) return rc;
   const int64_t P = p->P;
   std::vector<char> seen(static_cast<size_t>(p->desc.max_seqs), 0);
+  std::vector<int32_t> gain;   // the sequences that get pages
   int64_t tokens = 0, need = 0, most = 0;
   for (int32_t i = 0; i < n; ++i) {
     const int32_t q = seq_ids[i];
@@ -348,7 +349,10 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
       const int64_t pages = ceil_div(ss.len + counts[i], P);
       if (pages > p->desc.max_pages_per_seq)
         return fail(LL_ERANGE, "entry %d: %lld rows exceed the page-table row", i, (long long)(ss.len + counts[i]));
-      need += pages - ceil_div(ss.len, P);
+      if (const int64_t more = pages - ceil_div(ss.len, P)) {
+        need += more;
+        gain.push_back(q);
+      }
     } else if (counts[i] > ss.len) {
       return fail(LL_EINVAL, "entry %d: %d tokens, but sequence %d holds %lld rows", i, counts[i], q, (long long)ss.len);
     }
@@ -358,7 +362,9 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
   if (tokens > s->max_tokens) return fail(LL_EINVAL, "%lld tokens, but the step holds %d", (long long)tokens, s->max_tokens);
   if (need > p->free.count())
     return fail(LL_ENOMEM, "need %lld fresh pages, %lld free", (long long)need, (long long)p->free.count());
-  if ((rc = ll::pool_fresh_tables(p, seq_ids, static_cast<size_t>(n)))) return rc;
+  // Page lists that the commit below extends have to be up to date (behind an
+  // eviction this waits for the device); the kernels read the device's own.
+  if ((rc = ll::pool_fresh_tables(p, gain.data(), gain.size()))) return rc;
 
   // --- plan (host only, no state change yet)
   std::vector<int32_t> fresh;

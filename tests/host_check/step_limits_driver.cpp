@@ -74,11 +74,54 @@ void growth() {
   ll_pool_destroy(pool);
 }
 
+// A device-planned eviction leaves the host's page list of its sequences out of
+// date.  A begin that gives a sequence no page has no use for it and waits for no
+// copy; one that does brings it up to date, behind rows grown in between too.
+void tables_behind_an_eviction() {
+  for (const bool gqa : {false, true})
+    for (const int P : {1, 4, 16}) {
+      World w(gqa, P);
+      int32_t id = -1;
+      const int64_t n = std::min(16 * P + 5, 30 * P);
+      CHECK(ll_seq_alloc(w.pool, n, &id, nullptr) == LL_OK);
+      std::vector<uint8_t> keep(static_cast<size_t>(n), 1);
+      keep[1] = 0;
+      for (int64_t i = n - P / 2 - 1; i < n; ++i) keep[static_cast<size_t>(i)] = 0;   // leaves room in the last page
+      const int64_t kept = std::count(keep.begin(), keep.end(), 1), off = 0;
+      CHECK(kv_evict_compact(w.pool, &id, 1, keep.data(), &off, nullptr) == LL_OK);
+      const ll_step_desc d{w.heads, 1, kTokens};
+      ll_step* s = nullptr;
+      CHECK(ll_step_create(w.pool, &d, &s) == LL_OK);
+      int32_t three = 3, one = 1, none = 0, many = 2 * P;
+      CHECK(ll_step_begin(s, &id, &three, 1, 0, nullptr) == LL_OK);
+      const ll::SeqState& q = w.pool->seqs[id];
+      CHECK(q.stale && q.len == kept);
+      CHECK(ll_step_begin(s, &id, &none, 1, 1, nullptr) == LL_OK && q.stale);
+      int64_t grown = 0;
+      if ((kept + P - 1) / P == (kept + P) / P) {   // one row more is in a page that is there
+        CHECK(ll_step_begin(s, &id, &one, 1, 1, nullptr) == LL_OK && q.stale && q.len == kept + 1);
+        grown = 1;
+      }
+      CHECK(ll_step_begin(s, &id, &many, 1, 1, nullptr) == LL_OK && !q.stale);
+      StepModel m;
+      m.h = s, m.begun = true, m.seqs = {id}, m.counts = {many}, m.tokens = many;
+      m.tile = ll::attend_tile(gqa, w.dim, int64_t{many} * (w.heads / w.kv_heads));
+      const std::map<int, Seq> b = w.books();
+      CHECK(b.at(id).len == kept + grown + many && b.at(id).pos == n + grown + many);
+      check_plan(w, m, b);   // the list against the device's row, rows and items
+      int64_t n_free = 0;
+      CHECK(ll_pool_free_pages(w.pool, &n_free) == LL_OK && n_free == static_cast<int64_t>(w.free_pages(b).size()));
+      ll_step_destroy(s);
+      ll_pool_destroy(w.pool);
+    }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
   const std::map<std::string, void (*)()> checks = {
       {"growth", growth},
+      {"tables_behind_an_eviction", tables_behind_an_eviction},
       {"scales", scales},
       {"shares_of_long_tiles", shares_of_long_tiles},
   };

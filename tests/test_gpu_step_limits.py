@@ -41,3 +41,46 @@ def test_scores_that_are_all_minus_infinity(kind, count, n, causal):
     assert (f64(out) == 0).all() and (f64(lse) == -INF).all()
     step.close()
     c.pool.close()
+
+
+@pytest.mark.parametrize("gqa", [False, True])
+@pytest.mark.parametrize("P", [1, 16])
+def test_begins_behind_an_eviction_that_need_no_page(gqa, P):
+    """The host's page list stays out of date until a begin needs it: the last rows
+    asked again, a row in a page that is there, then rows in new pages."""
+    c = Cache(gqa, P, [300], seed=P, kv_heads=2, dim=64, rot=64, room=80, spare=-(-380 // P) + 4)
+    step = c.pool.step(4, max_tokens=40)
+    g = np.random.default_rng(8)
+    keep = (g.random(300) > 0.4).astype(np.uint8)
+    while P > 1 and keep.sum() % P != P // 2:
+        keep[np.flatnonzero(keep)[0]] = 0
+    want = [c.rows(p, 0, 0)[keep == 1] for p in range(len(c.planes))]
+    n = int(keep.sum())
+    c.pool.evict([0], torch.from_numpy(keep).cuda(), [0])
+    outs = []
+    for count, grow in ((3, False), (1, True), (40, True)):
+        T = step.begin([0], [count], grow=grow)
+        q = _queries(c, T, 4, seed=count)
+        if grow:
+            a = bf16(g.standard_normal((T, 2, 64) if gqa else (T, 512))).cuda()
+            b = bf16(g.standard_normal((T, 2, 64) if gqa else (T, 64))).cuda()
+            step.append(0, a, b)
+        outs.append((count, q, *step.attend(0, q, scale=0.1, lse=True)))
+    torch.cuda.synchronize()
+    assert c.pool.seq_get(0)[:2] == (n + 41, 341)
+    for p in range(len(c.planes)):
+        assert np.array_equal(c.rows(p, 0, 0, 0, n), want[p])
+    count, q, out, lse = outs[-1]
+    c.check_attend(out, lse, q, [0], [count], 0, 0.1)
+    # the first two, against the rows that were there then
+    for (count, q, out, lse), rows in zip(outs, (n, n + 1)):
+        k = c.rows(0, 0, 0, 0, rows)
+        v = c.rows(1, 0, 0, 0, rows) if gqa else k[..., :512]
+        for h in range(4):
+            x = h // (4 // k.shape[1])
+            o, l, w, slack = S.attend(f64(q)[:, h], k[:, x], v[:, x], rows - count, 0.1)
+            ds = k.shape[-1] * F32 * slack[:, None] + 8 * F32 * (1 + np.abs(l[:, None]))
+            assert (np.abs(f64(out)[:, h] - o) <= HALF_STEP * (np.abs(o) + w) + (2 * ds + rows * F32) * w + 1e-30).all()
+            assert (np.abs(f64(lse)[:, h] - l) <= ds[:, 0] + rows * F32).all()
+    step.close()
+    c.pool.close()
