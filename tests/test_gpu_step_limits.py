@@ -84,3 +84,35 @@ def test_begins_behind_an_eviction_that_need_no_page(gqa, P):
             assert (np.abs(f64(lse)[:, h] - l) <= ds[:, 0] + rows * F32).all()
     step.close()
     c.pool.close()
+
+
+@pytest.mark.parametrize("gqa,pairing", [(False, 0), (False, 1), (True, 0), (True, 1)])
+def test_append_at_a_far_position(gqa, pairing):
+    """An eviction keeps positions: of 2^20 + 77 rows 40 stay, and the next tokens
+    are rows 40 on at positions 2^20 + 77 on."""
+    n, held, T, heads = (1 << 20) + 77, 40, 5, 6
+    c = Cache(gqa, 256, [0], kv_heads=1, dim=32, rot=32, pairing=pairing, base=500000.0, room=n + 512, spare=n // 256 + 2)
+    c.pool.seq_set_pages(0, list(range(-(-n // 256))), n)
+    keep = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    keep[torch.arange(held, device="cuda") * 25000] = 1
+    c.pool.evict([0], keep, [0])
+    step = c.pool.step(heads, max_tokens=T)
+    assert step.begin([0], [T]) == T
+    assert c.pool.seq_get(0)[:2] == (held + T, n + T)
+    g = np.random.default_rng(1)
+    ang = S.angles(n + np.arange(T), 32 if gqa else 64, 500000.0)
+    a, b = (bf16(g.standard_normal((T, 1, 32) if gqa else (T, w))).cuda() for w in (512, 64))
+    q = bf16(g.standard_normal((T, heads, 32 if gqa else 64))).cuda()
+    qo = step.append(0, a, b, q=q)
+    torch.cuda.synchronize()
+    if gqa:
+        c.check_rows(0, 0, 0, held, held + T, *S.heads(f64(a), None, 0, ang, pairing, 32))
+        assert np.array_equal(c.rows(1, 0, 0, held, held + T), f64(b))
+    else:
+        pe, size = S.heads(f64(b)[:, None], None, 0, ang, pairing)
+        lat = f64(a)[:, None]
+        c.check_rows(0, 0, 0, held, held + T, np.concatenate([lat, pe], -1), np.concatenate([np.abs(lat), size], -1))
+    want, size = S.heads(f64(q), None, 0, ang, pairing)
+    assert (np.abs(f64(qo) - want) <= HALF_STEP * np.abs(want) + 2.0 ** -18 * size).all()
+    step.close()
+    c.pool.close()
