@@ -32,7 +32,11 @@
  * Graphs.  append and attend may be captured (begin may not: LL_EUNSUPPORTED).
  * They then cover the whole capacity of the step and read its current plan from
  * device memory: begin the next tokens, on the stream the graph runs on, and
- * replay.  Nothing orders a replay but its stream: the replays of a step, its
+ * replay.  Eager calls between are planned for their own tokens.  A graph's
+ * attention keeps the tiles (query rows that a workgroup takes) of the begin before
+ * the step's first capture, whatever later begins bring: capture behind a begin
+ * like those that the graph will replay, and keep a step of fitting max_tokens for
+ * each kind (single tokens, prompts).  Nothing orders a replay but its stream: the replays of a step, its
  * begins and the pool's other calls have to follow one another on one stream or
  * be ordered by the caller, since one step has one workspace.
  */

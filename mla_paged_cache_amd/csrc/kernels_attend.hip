@@ -209,8 +209,9 @@ struct Shape {
   static constexpr int PIECES = MLA ? BN / WAVES + (BN / 8 + WAVES - 1) / WAVES : BN * ROWCH / 64 / WAVES;
   static constexpr int KVT = BN / KW;                        // cached rows of a tile per wave
   static constexpr int TILE = 16 * QN * QW;                  // query rows
-  // Below the largest tile a sequence is one tile (attend_tile), and its cached rows
-  // are read once: past the caches 257, 90 and 413 us (64 MLA tokens over up to 32768
+  // Below the largest tile a sequence is one tile (attend_tile; a graph that replays
+  // more than it was captured behind is the exception), and its cached rows are read
+  // once: past the caches 257, 90 and 413 us (64 MLA tokens over up to 32768
   // rows, one GQA token over 131072, 128 over up to 8192), otherwise 290, 101 and
   // 458.  Chunks of several tiles read rows again (2130 past the caches, 2004).
   static constexpr bool ONCE = TILE < (MLA || DP > 128 ? 128 : 256);

@@ -28,7 +28,10 @@ __device__ __forceinline__ int seq_of_token(const StepSeq* seqs, int n, int t) {
 __global__ __launch_bounds__(256) void step_setup_kernel(StepSetupLaunch a) {
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
-  if (t == 0) *a.dst_counts = a.counts;
+  if (t == 0) {
+    *a.dst_counts = a.counts;
+    *a.dst_own_counts = a.own_counts;
+  }
   for (int64_t i = t; i < int64_t{a.counts.tokens} * a.pairs; i += stride) {
     const int tok = static_cast<int>(i / a.pairs);
     const int j = static_cast<int>(i - int64_t{tok} * a.pairs);
@@ -51,9 +54,13 @@ __global__ __launch_bounds__(256) void step_setup_kernel(StepSetupLaunch a) {
       a.rows[tok] = in_pool ? (page << a.page_shift) + (r & ((1 << a.page_shift) - 1)) : -1;
     }
   }
-  const chunk_t* src = reinterpret_cast<const chunk_t*>(a.src_items);
-  chunk_t* dst = reinterpret_cast<chunk_t*>(a.dst_items);
-  for (int64_t i = t; i < int64_t{a.counts.items} * 2; i += stride) dst[i] = src[i];
+  auto copy = [&](const AttendItem* from, AttendItem* to, int n) {
+    const chunk_t* src = reinterpret_cast<const chunk_t*>(from);
+    chunk_t* dst = reinterpret_cast<chunk_t*>(to);
+    for (int64_t i = t; i < int64_t{n} * 2; i += stride) dst[i] = src[i];
+  };
+  copy(a.src_items, a.dst_items, a.counts.items);
+  copy(a.src_own, a.dst_own_items, a.own_counts.items);
   // a wave per sequence
   for (int64_t i = t >> 6; i < a.counts.seqs; i += stride >> 6) {
     const StepSeq s = a.src_seqs[i];
@@ -246,7 +253,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendLaunch a) {
 
 hipError_t launch_step_setup(const StepSetupLaunch& a, hipStream_t s) {
   const int64_t work = std::max<int64_t>({int64_t{a.counts.tokens} * a.pairs, int64_t{a.counts.items} * 2,
-                                          int64_t{a.counts.seqs} * 64, 1});
+                                          int64_t{a.own_counts.items} * 2, int64_t{a.counts.seqs} * 64, 1});
   const int64_t blocks = std::min<int64_t>((work + 255) / 256, 4096);
   step_setup_kernel<<<dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s>>>(a);
   return hipGetLastError();

@@ -30,6 +30,15 @@ constexpr int64_t kMaxStride = int64_t{1} << 32;
 constexpr int64_t kPartValues = int64_t{1} << 25;
 constexpr int64_t kMaxShares = 2048;
 
+// A plan of the attention: the current begin's, in tiles of `tile` query rows.
+struct Plan {
+  int32_t tile = 16;
+  int64_t items = 0;
+  int64_t shares = 0;            // of them shares of split tiles, which a second kernel joins
+  ll::StepCounts* d_counts = nullptr;
+  ll::AttendItem* d_items = nullptr;
+};
+
 }  // namespace
 
 struct ll_step {
@@ -38,13 +47,15 @@ struct ll_step {
   int32_t heads = 0, kv_heads = 1, group = 1;
   int32_t max_seqs = 0, max_tokens = 0;
   int32_t value_dim = 0;         // width of an output head
-  int32_t tile = 16;             // query rows per attention item
-  bool captured = false;         // a graph holds this step's attention: the tile stays
-  int64_t max_items = 0;
-  // device: [counts | items | rows | tab | theta | parts]
+  int64_t max_items = 0;         // of a plan
+  bool captured = false;         // a graph holds plans[0]: its tile stays
+  // What graphs read, and eager calls too unless a graph holds another tile than
+  // they would take: they have a plan of their own then.  One at a time uses the
+  // partial results.
+  Plan plans[2];
+  int eager = 0;
+  // device: [counts, items, twice | rows | tab | theta | parts]
   char* d_buf = nullptr;
-  ll::StepCounts* d_counts = nullptr;
-  ll::AttendItem* d_items = nullptr;
   int32_t* d_rows = nullptr;
   float* d_tab = nullptr;
   double* d_theta = nullptr;
@@ -55,8 +66,6 @@ struct ll_step {
   std::vector<int32_t> seqs;
   std::vector<uint64_t> gens;
   int64_t tokens = 0;
-  int64_t items = 0;
-  int64_t shares = 0;            // of them shares of split tiles, which a second kernel joins
 };
 
 namespace {
@@ -266,8 +275,11 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
     at = ll::align_up(at + bytes, 256);
     return o;
   };
-  const size_t o_counts = take(sizeof(ll::StepCounts));
-  const size_t o_items = take(sizeof(ll::AttendItem) * static_cast<size_t>(s->max_items));
+  size_t o_counts[2], o_items[2];
+  for (int k = 0; k < 2; ++k) {
+    o_counts[k] = take(sizeof(ll::StepCounts));
+    o_items[k] = take(sizeof(ll::AttendItem) * static_cast<size_t>(s->max_items));
+  }
   const size_t o_rows = take(sizeof(int32_t) * static_cast<size_t>(d->max_tokens));
   const size_t o_tab = take(sizeof(float) * 2 * pairs * static_cast<size_t>(d->max_tokens));
   const size_t o_theta = take(sizeof(double) * pairs);
@@ -280,8 +292,10 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
     (void)hipGetLastError();
     return fail(LL_ENOMEM, "cannot allocate %zu bytes for the step", at);
   }
-  s->d_counts = reinterpret_cast<ll::StepCounts*>(s->d_buf + o_counts);
-  s->d_items = reinterpret_cast<ll::AttendItem*>(s->d_buf + o_items);
+  for (int k = 0; k < 2; ++k) {
+    s->plans[k].d_counts = reinterpret_cast<ll::StepCounts*>(s->d_buf + o_counts[k]);
+    s->plans[k].d_items = reinterpret_cast<ll::AttendItem*>(s->d_buf + o_items[k]);
+  }
   s->d_rows = reinterpret_cast<int32_t*>(s->d_buf + o_rows);
   s->d_tab = reinterpret_cast<float*>(s->d_buf + o_tab);
   s->d_theta = reinterpret_cast<double*>(s->d_buf + o_theta);
@@ -289,7 +303,8 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
   s->d_part_ml = reinterpret_cast<float*>(s->d_buf + o_ml);
   const ll::StepCounts none{};
   hipError_t e = hipMemcpy(s->d_theta, p->theta.data(), pairs * sizeof(double), hipMemcpyHostToDevice);
-  if (e == hipSuccess) e = hipMemcpy(s->d_counts, &none, sizeof none, hipMemcpyHostToDevice);
+  for (const Plan& x : s->plans)
+    if (e == hipSuccess) e = hipMemcpy(x.d_counts, &none, sizeof none, hipMemcpyHostToDevice);
   if (e != hipSuccess) {
     (void)hipFree(s->d_buf);
     return fail(LL_EDEVICE, "step setup: %s", hipGetErrorString(e));
@@ -386,11 +401,14 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
     tok += counts[i];
     at += x.new_pages;
   }
-  const int tile = s->captured ? s->tile : ll::attend_tile(p->gqa, s->value_dim, most * s->group);
-  std::vector<ll::AttendItem> items;
-  const int64_t shares = plan_items(s, tile, ss, &items);
-  if (static_cast<int64_t>(items.size()) > s->max_items)
-    return fail(LL_EINVAL, "the step's attention needs %zu items, more than %lld", items.size(), (long long)s->max_items);
+  // a graph's plan keeps its tile; eager calls take the one for these tokens
+  const int tile = ll::attend_tile(p->gqa, s->value_dim, most * s->group);
+  const int graph_tile = s->captured ? s->plans[0].tile : tile;
+  std::vector<ll::AttendItem> items, own;
+  const int64_t shares = plan_items(s, graph_tile, ss, &items);
+  const int64_t own_shares = tile == graph_tile ? 0 : plan_items(s, tile, ss, &own);
+  if (const size_t n_items = std::max(items.size(), own.size()); static_cast<int64_t>(n_items) > s->max_items)
+    return fail(LL_EINVAL, "the step's attention needs %zu items, more than %lld", n_items, (long long)s->max_items);
   // host memory that the commit below needs, before anything changes
   for (int32_t i = 0; i < n; ++i) {
     ll::SeqState& q = p->seqs[seq_ids[i]];
@@ -405,28 +423,36 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
   const size_t b_seq = ll::align_up(ss.size() * sizeof(ll::StepSeq), 256);
   const size_t b_it = ll::align_up(items.size() * sizeof(ll::AttendItem), 256);
   const size_t b_pg = ll::align_up(fresh.size() * sizeof(int32_t), 256);
-  if ((rc = ll::pool_stage(p, b_seq + b_it + b_pg + 256, &sg))) return rc;
+  const size_t b_own = ll::align_up(own.size() * sizeof(ll::AttendItem), 256);
+  if ((rc = ll::pool_stage(p, b_seq + b_it + b_pg + b_own + 256, &sg))) return rc;
   if (!ss.empty()) std::memcpy(sg->host, ss.data(), ss.size() * sizeof(ll::StepSeq));
   if (!items.empty()) std::memcpy(sg->host + b_seq, items.data(), items.size() * sizeof(ll::AttendItem));
   if (!fresh.empty()) std::memcpy(sg->host + b_seq + b_it, fresh.data(), fresh.size() * sizeof(int32_t));
-  sg->used = b_seq + b_it + b_pg;
+  if (!own.empty()) std::memcpy(sg->host + b_seq + b_it + b_pg, own.data(), own.size() * sizeof(ll::AttendItem));
+  sg->used = b_seq + b_it + b_pg + b_own;
   if ((rc = ll::pool_upload(p, sg, st))) return rc;
   ll::StepSetupLaunch a{};
   a.counts.tokens = static_cast<int32_t>(tokens);
   a.counts.items = static_cast<int32_t>(items.size());
   a.counts.seqs = n;
   a.counts.shares = static_cast<int32_t>(shares);
+  a.own_counts = a.counts;
+  a.own_counts.items = static_cast<int32_t>(own.size());
+  a.own_counts.shares = static_cast<int32_t>(own_shares);
   a.src_seqs = reinterpret_cast<const ll::StepSeq*>(sg->dev);
   a.src_items = reinterpret_cast<const ll::AttendItem*>(sg->dev + b_seq);
   a.fresh = reinterpret_cast<const int32_t*>(sg->dev + b_seq + b_it);
+  a.src_own = reinterpret_cast<const ll::AttendItem*>(sg->dev + b_seq + b_it + b_pg);
   a.theta = s->d_theta;
   a.pairs = static_cast<int32_t>(p->theta.size());
   a.page_shift = p->page_shift;
   a.max_pages_per_seq = p->desc.max_pages_per_seq;
   a.num_pages = p->desc.num_pages;
   a.page_table = p->desc.page_table;
-  a.dst_counts = s->d_counts;
-  a.dst_items = s->d_items;
+  a.dst_counts = s->plans[0].d_counts;
+  a.dst_items = s->plans[0].d_items;
+  a.dst_own_counts = s->plans[1].d_counts;
+  a.dst_own_items = s->plans[1].d_items;
   a.rows = s->d_rows;
   a.tab = s->d_tab;
   hipError_t e = ll::launch_step_setup(a, st);
@@ -448,10 +474,14 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
     gens[i] = q.gen;
   }
   s->gens = std::move(gens);
-  s->tile = tile;
+  s->plans[0].tile = graph_tile;
+  s->plans[0].items = static_cast<int64_t>(items.size());
+  s->plans[0].shares = shares;
+  s->plans[1].tile = tile;
+  s->plans[1].items = static_cast<int64_t>(own.size());
+  s->plans[1].shares = own_shares;
+  s->eager = tile == graph_tile ? 0 : 1;
   s->tokens = tokens;
-  s->items = static_cast<int64_t>(items.size());
-  s->shares = shares;
   s->begun = true;
   return LL_OK;
 } catch (...) {
@@ -491,7 +521,7 @@ ll_status ll_step_append(ll_step* s, const ll_append_desc* d, void* stream) try 
     if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return fail(LL_EINVAL, "eps must be finite and not negative");
   }
   ll::AppendLaunch a{};
-  a.counts = s->d_counts;
+  a.counts = s->plans[0].d_counts;
   a.rows = s->d_rows;
   a.tab = s->d_tab;
   a.pairs = static_cast<int32_t>(p->theta.size());
@@ -560,14 +590,15 @@ ll_status ll_step_attend(ll_step* s, const ll_attend_desc* d, void* stream) try 
   if ((rc = check_output(d->out_token_stride, d->out_head_stride, T, s->heads, s->value_dim, "out"))) return rc;
   if (reinterpret_cast<uintptr_t>(d->lse) & 3) return fail(LL_EINVAL, "lse is not 4-byte aligned");
   ll::AttendLaunch a{};
-  a.counts = s->d_counts;
-  a.items = s->d_items;
-  a.n_items = static_cast<int32_t>(capturing ? s->max_items : s->items);
-  a.n_shares = static_cast<int32_t>(capturing ? max_slots(s, s->tile) : s->shares);
-  a.join_blocks = static_cast<int32_t>(ceil_div(int64_t{s->tile} * s->value_dim, 1024));
+  const Plan& plan = s->plans[capturing ? 0 : s->eager];
+  a.counts = plan.d_counts;
+  a.items = plan.d_items;
+  a.n_items = static_cast<int32_t>(capturing ? s->max_items : plan.items);
+  a.n_shares = static_cast<int32_t>(capturing ? max_slots(s, plan.tile) : plan.shares);
+  a.join_blocks = static_cast<int32_t>(ceil_div(int64_t{plan.tile} * s->value_dim, 1024));
   a.kv_heads = s->kv_heads;
   a.group = s->group;
-  a.tile = s->tile;
+  a.tile = plan.tile;
   a.causal = d->causal;
   a.window = static_cast<int32_t>(std::min<int64_t>(d->window, INT32_MAX));
   a.scale = d->scale;

@@ -62,6 +62,10 @@ struct StepSetupLaunch {
   int32_t* page_table;
   StepCounts* dst_counts;
   AttendItem* dst_items;
+  StepCounts own_counts;         // the eager calls' own plan of the attention, where a graph holds
+  const AttendItem* src_own;     // another tile (own_counts.items: 0 otherwise)
+  StepCounts* dst_own_counts;
+  AttendItem* dst_own_items;
   int32_t* rows;                 // [tokens] physical row, -1: none
   float* tab;                    // [tokens][2][pairs] float32 cos, then sin
 };

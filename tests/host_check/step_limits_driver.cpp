@@ -116,10 +116,76 @@ void tables_behind_an_eviction() {
     }
 }
 
+// A graph keeps the tile that it was captured with; eager calls on the same step are
+// planned for what they bring, before and after, and a later graph joins the first.
+void eager_calls_beside_a_graph() {
+  for (const bool gqa : {false, true}) {
+    World w(gqa, 16);
+    int32_t id = -1, one = 1, many = 70;
+    CHECK(ll_seq_alloc(w.pool, 300, &id, nullptr) == LL_OK);
+    const ll_step_desc d{w.heads, 1, kTokens};
+    ll_step* s = nullptr;
+    CHECK(ll_step_create(w.pool, &d, &s) == LL_OK);
+    const int group = w.heads / w.kv_heads;
+    const int small = ll::attend_tile(gqa, w.dim, group), big = ll::attend_tile(gqa, w.dim, int64_t{many} * group);
+    CHECK(small != big);
+    StepModel m;
+    m.h = s, m.begun = true, m.seqs = {id};
+    auto begin = [&](int32_t count) {
+      CHECK(ll_step_begin(s, &id, &count, 1, 0, nullptr) == LL_OK);
+      m.counts = {count}, m.tokens = count;
+    };
+    auto eager = [&](int tile) {
+      const ll_attend_desc t = attend_desc(w, m.tokens);
+      CHECK(ll_step_attend(s, &t, nullptr) == LL_OK && g_attend.tile == tile);
+      return g_attend;
+    };
+    auto capture = [&](int tile) {
+      g_capturing = true;
+      const ll_attend_desc t = attend_desc(w, kTokens);
+      CHECK(ll_step_attend(s, &t, nullptr) == LL_OK && g_attend.tile == tile);
+      g_capturing = false;
+      return g_attend;
+    };
+    begin(many);
+    eager(big);
+    begin(one);
+    const ll::AttendLaunch first = eager(small), graph = capture(small);
+    CHECK(graph.items == first.items && graph.counts == first.counts && graph.n_items > first.n_items);
+    for (int turn = 0; turn < 2; ++turn) {
+      begin(one);   // as the graph: one plan for both
+      CHECK(g_setup.own_counts.items == 0);
+      const ll::AttendLaunch same = eager(small);
+      CHECK(same.items == graph.items && same.counts == graph.counts);
+      m.tile = small;
+      check_plan(w, m, w.books());
+      begin(many);   // more than the graph's: a plan each
+      m.tile = small;
+      check_plan(w, m, w.books());
+      CHECK(g_setup.counts.items <= graph.n_items && g_setup.counts.shares <= graph.n_shares);
+      const ll::StepSetupLaunch both = g_setup;
+      const ll::AttendLaunch own = eager(big), again = capture(small);
+      CHECK(again.items == graph.items && again.counts == graph.counts && again.n_items == graph.n_items);
+      CHECK(own.items == both.dst_own_items && own.counts == both.dst_own_counts && own.items != graph.items);
+      CHECK(own.n_items == both.own_counts.items && own.n_shares == both.own_counts.shares);
+      CHECK(both.own_counts.tokens == many && both.own_counts.seqs == 1);
+      // the same checks of the eager plan
+      std::vector<ll::AttendItem> items(both.src_own, both.src_own + both.own_counts.items);
+      g_setup.counts = both.own_counts;
+      g_setup.dst_items = items.data();
+      m.tile = big;
+      check_plan(w, m, w.books());
+    }
+    ll_step_destroy(s);
+    ll_pool_destroy(w.pool);
+  }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
   const std::map<std::string, void (*)()> checks = {
+      {"eager_calls_beside_a_graph", eager_calls_beside_a_graph},
       {"growth", growth},
       {"tables_behind_an_eviction", tables_behind_an_eviction},
       {"scales", scales},

@@ -116,3 +116,46 @@ def test_append_at_a_far_position(gqa, pairing):
     assert (np.abs(f64(qo) - want) <= HALF_STEP * np.abs(want) + 2.0 ** -18 * size).all()
     step.close()
     c.pool.close()
+
+
+@pytest.mark.parametrize("gqa", [False, True])
+@pytest.mark.parametrize("captured,eager", [(1, 70), (70, 1)])
+def test_eager_calls_beside_a_graph(gqa, captured, eager):
+    """A step whose attention a graph holds: its eager calls give the bits of a step
+    that no graph holds, the graph's replays go on, in turn and behind each other."""
+    say(f"eager beside a graph gqa={gqa} captured={captured} eager={eager}")
+    c = Cache(gqa, 16, [900, 333], seed=11, kv_heads=2, dim=128, rot=128)
+    heads, cap = 8, 80
+    step, other = (c.pool.step(heads, max_seqs=2, max_tokens=cap) for _ in range(2))
+    q, dv = _queries(c, cap, heads), 128 if gqa else 512
+    out = torch.zeros((cap, heads, dv), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((cap, heads), dtype=torch.float32, device="cuda")
+
+    def both(s, count):
+        T = s.begin([1, 0], [count, count // 7], grow=False)
+        return T, s.attend(0, q, scale=0.09, lse=True)
+    _, want = both(other, eager)   # (also loads the kernels)
+    step.begin([1, 0], [captured, captured // 7], grow=False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    stream = torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        step.attend(0, q, scale=0.09, out=out, lse=lse)
+    for turn in range(3):
+        T, got = both(step, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0][:T].view(torch.int16), want[0][:T].view(torch.int16))
+        assert torch.equal(got[1][:T], want[1][:T])
+        for count in (captured, eager):   # replays of the size captured, and of the other
+            out.fill_(7.0)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(stream):
+                T = step.begin([1, 0], [count, count // 7], grow=False)
+                graph.replay()
+                graph.replay()
+            torch.cuda.synchronize()
+            c.check_attend(out[:T], lse[:T], q[:T], [1, 0], [count, count // 7], 0, 0.09)
+            assert (out[T:] == 7).all()
+    for s in (step, other):
+        s.close()
+    c.pool.close()

@@ -8,7 +8,7 @@ import pytest
 
 from test_host_step import CLANG, CSRC, FLAGS, HC, SAN
 
-CHECKS = ["growth", "tables_behind_an_eviction", "scales", "shares_of_long_tiles"]
+CHECKS = ["eager_calls_beside_a_graph", "growth", "tables_behind_an_eviction", "scales", "shares_of_long_tiles"]
 
 
 @pytest.fixture(scope="module")
