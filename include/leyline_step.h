@@ -115,7 +115,7 @@ typedef struct {
  * to float32.  a = b = NULL leaves the cache alone, q = NULL the queries.  q_out
  * may be q, and may not overlap the inputs otherwise.
  * Errors: LL_EINVAL (layer, too few tokens, NULL or misaligned pointer or stride, overlapping
- * q_out rows, negative eps, a changed sequence, no begin yet), LL_EDEVICE. */
+ * q_out rows, q_out = q with other strides, negative eps, a changed sequence, no begin yet), LL_EDEVICE. */
 ll_status ll_step_append(ll_step* step, const ll_append_desc* desc, void* stream);
 
 typedef struct {

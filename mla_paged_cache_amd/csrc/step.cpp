@@ -512,6 +512,9 @@ ll_status ll_step_append(ll_step* s, const ll_append_desc* d, void* stream) try 
     if ((rc = check_plane(d->q, used(d->q_token_stride, T), used(d->q_head_stride, s->heads), "q"))) return rc;
     if ((rc = check_plane(d->q_out, used(d->q_out_token_stride, T), used(d->q_out_head_stride, s->heads), "q_out"))) return rc;
     if ((rc = check_output(d->q_out_token_stride, d->q_out_head_stride, T, s->heads, D, "q_out"))) return rc;
+    if (d->q_out == d->q && (used(d->q_token_stride, T) != used(d->q_out_token_stride, T) ||
+                             used(d->q_head_stride, s->heads) != used(d->q_out_head_stride, s->heads)))
+      return fail(LL_EINVAL, "q_out is q, but its strides are others");
   }
   if (d->q_norm && !p->gqa) return fail(LL_EINVAL, "q_norm is for GQA / MHA pools only");
   if (d->norm || d->q_norm) {

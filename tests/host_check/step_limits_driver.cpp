@@ -181,6 +181,33 @@ void eager_calls_beside_a_graph() {
   }
 }
 
+// q_out = q turns the queries in place, so both are laid out alike (a stride that no
+// second token or head uses says nothing).
+void queries_in_place() {
+  for (const bool gqa : {false, true}) {
+    World w(gqa, 16);
+    int32_t id = -1, two = 2, one = 1;
+    CHECK(ll_seq_alloc(w.pool, 30, &id, nullptr) == LL_OK);
+    const ll_step_desc d{w.heads, 1, kTokens};
+    ll_step* s = nullptr;
+    CHECK(ll_step_create(w.pool, &d, &s) == LL_OK && ll_step_begin(s, &id, &two, 1, 0, nullptr) == LL_OK);
+    ll_append_desc a = append_desc(w, 2);
+    a.q_out = const_cast<void*>(a.q);
+    CHECK(ll_step_append(s, &a, nullptr) == LL_OK);
+    a.q_out_token_stride += 64;
+    CHECK(ll_step_append(s, &a, nullptr) == LL_EINVAL);
+    a.q_out_token_stride -= 64;
+    a.q_head_stride = 0;   // one query for every head
+    CHECK(ll_step_append(s, &a, nullptr) == LL_EINVAL);
+    a.q_head_stride = a.q_out_head_stride;
+    CHECK(ll_step_begin(s, &id, &one, 1, 0, nullptr) == LL_OK);
+    a.q_out_token_stride += 64;   // of one token
+    CHECK(ll_step_append(s, &a, nullptr) == LL_OK);
+    ll_step_destroy(s);
+    ll_pool_destroy(w.pool);
+  }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
@@ -188,6 +215,7 @@ int main(int argc, char** argv) {
       {"eager_calls_beside_a_graph", eager_calls_beside_a_graph},
       {"growth", growth},
       {"tables_behind_an_eviction", tables_behind_an_eviction},
+      {"queries_in_place", queries_in_place},
       {"scales", scales},
       {"shares_of_long_tiles", shares_of_long_tiles},
   };

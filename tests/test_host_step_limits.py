@@ -8,7 +8,8 @@ import pytest
 
 from test_host_step import CLANG, CSRC, FLAGS, HC, SAN
 
-CHECKS = ["eager_calls_beside_a_graph", "growth", "tables_behind_an_eviction", "scales", "shares_of_long_tiles"]
+CHECKS = ["eager_calls_beside_a_graph", "growth", "tables_behind_an_eviction", "queries_in_place", "scales",
+          "shares_of_long_tiles"]
 
 
 @pytest.fixture(scope="module")
