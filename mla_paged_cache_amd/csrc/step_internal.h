@@ -35,9 +35,10 @@ struct alignas(16) AttendItem {
 };
 static_assert(sizeof(AttendItem) == 32, "two 16-byte words");
 
-// Rows of each of a tile's shares: equal, in multiples of `grain`.  (In 64 bits: the
-// rows alone may come within 1025 of 2^31.)
-constexpr int64_t share_rows(int64_t rows, int64_t shares, int64_t grain) {
+// Rows of each of a tile's shares: equal, in multiples of `grain`.  (Rows may come
+// within 1025 of 2^31, and shares are at most 2048: every sum here stays below 2^32,
+// and a division of 64 bits would cost each workgroup about 150 instructions.)
+constexpr uint32_t share_rows(uint32_t rows, uint32_t shares, uint32_t grain) {
   return ((rows + shares - 1) / shares + grain - 1) / grain * grain;
 }
 
