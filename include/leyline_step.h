@@ -36,9 +36,19 @@
  * attention keeps the tiles (query rows that a workgroup takes) of the begin before
  * the step's first capture, whatever later begins bring: capture behind a begin
  * like those that the graph will replay, and keep a step of fitting max_tokens for
- * each kind (single tokens, prompts).  Nothing orders a replay but its stream: the replays of a step, its
- * begins and the pool's other calls have to follow one another on one stream or
- * be ordered by the caller, since one step has one workspace.
+ * each kind (single tokens, prompts).  Nothing orders a replay but its stream: the
+ * replays of a step, its begins and the pool's other calls have to follow one
+ * another on one stream or be ordered by the caller, since one step has one
+ * workspace.  A graph is not replayed once its step or its pool has ended, nor on
+ * sequences that something else has changed since the step's begin (a replay cannot
+ * refuse them; it stays inside the pool, but may write rows of other sequences).
+ *
+ * One begin, one tile: the attention of all its sequences runs in tiles that fit the
+ * one with the most tokens.  Single tokens beside a long chunk are faster in a begin
+ * and calls of their own, by a second step.
+ *
+ * A stream that a call ran on has to exist until a call on another stream, or the
+ * end of the pool, has followed.
  */
 #ifndef LEYLINE_STEP_H
 #define LEYLINE_STEP_H

@@ -219,8 +219,8 @@ struct Shape {
   static constexpr bool ACC = QN * DV / 4 >= 256;
   // then the waves share the weights through LDS, and each sums the columns
   // [wave * DV / QW ...) of all queries: the values are read from LDS once, not by
-  // every wave (a 2048-token MLA chunk of 16 heads over 16384 rows, two sequences:
-  // 1846 us with each wave summing its own queries, 1732 us so)
+  // every wave (MLA chunks of 2048 and 1917 tokens of 16 heads over up to 16384
+  // rows: 1846 us with each wave summing its own queries, 1732 us so)
   static constexpr int WEIGHTS = STAGES * STAGE + WAVES * PAGES * BN * 4;   // where these lie in LDS
   static constexpr int KEEPS = WEIGHTS + TILE * BN * 2;                     // two tiles' scalings, and which waves have any
   static constexpr int LDS = ACC ? KEEPS + 2 * (TILE * 4 + 16) : WEIGHTS;
@@ -313,8 +313,8 @@ __device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const u
 // cached rows goes through LDS.
 //
 // The running maximum is only a reference: it moves (and the sums are scaled)
-// when a score exceeds it by more than 2^8, so weights stay below 2^8 and most
-// tiles scale nothing.  Sums are float32; a weight is rounded to bf16 (relative
+// when a score (in base 2) exceeds it by more than 8, so weights stay below 2^8 and
+// most tiles scale nothing.  Sums are float32; a weight is rounded to bf16 (relative
 // 2^-9 on average) because the matrix units multiply bf16 by bf16.
 //
 // In a tile of which some query sees only a part, unseen weights are 0; since 0
@@ -322,10 +322,12 @@ __device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const u
 // and the item falls back to reading exactly the rows each query sees.
 //
 // One token per sequence is bound by reading the cache: 64 MLA sequences of up to
-// 32768 rows 245 us (6.2 TB/s), 128 GQA ones of up to 8192 rows and 8 heads of 128
-// 408 us (6.7 TB/s; a large read reaches 6.9).  Chunks are bound by the matrix
-// units and what feeds them: 2 x 2048 MLA tokens of 16 heads over up to 16384 rows
-// 1603 us (43% busy), 4096 GQA tokens of 32 heads over 32768 rows 1977 us (44%).
+// 32768 rows 269 us (5.7 TB/s), 128 GQA ones of up to 8192 rows and 8 heads of 128
+// 418 us (6.5 TB/s; a large read reaches 6.9).  Chunks are bound by the matrix units
+// and what feeds them: 2048 and 1917 MLA tokens of 16 heads over up to 16384 rows
+// 1683 us (43% busy), 4096 GQA tokens of 32 heads over 32768 rows 2148 us (44%).
+// These are medians of the first twelve calls; the fastest took 250, 412, 1580 and
+// 1970 us, for the chunks the last one, from which on they stay there.
 template <typename S>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::WAVES > 4 ? 2 : 1))) void attend_kernel(AttendLaunch a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -957,7 +959,8 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendLaunc
 // The smallest tile that holds all rows a sequence brings, so that its cached rows
 // are read once, up to what the registers hold (MLA and heads above 128: 128 rows).
 // 4096 GQA tokens of 4 heads a KV head over 32768 rows: 2.23 ms in tiles of 256,
-// 3.10 of 128, 4.96 of 64; 333 tokens of 5 heads in a window of 1000: 52, 57, 78 us.
+// 3.10 of 128, 4.96 of 64; seven chunks of up to 333 tokens, 5 heads a
+// KV head, in a window of 1000: 52, 57, 78 us.
 int attend_tile(bool gqa, int dim, int64_t rows) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 || !gqa || dim > 128 ? 128 : 256;
 }

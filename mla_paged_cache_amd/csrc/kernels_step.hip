@@ -166,10 +166,10 @@ __device__ __forceinline__ void rotate_band(Vals& x, const Angles<PAIRING>& cs, 
 // one that some other lane holds, so that all of a wave's loads are under way
 // before the first is waited for.
 //
-// Bound by the bytes, every value is read once and written once: 24576 tokens of
+// Bound by the bytes, every value is read once and written once: 24183 tokens of
 // 128 MLA heads whose rotated parts lie in wider heads take 155 us (a plain copy of
-// those parts 164, a dense one of as many bytes 153); 25 thousand tokens of 21 GQA
-// heads of 96 take 33.0 us, 5.8 TB/s.
+// those parts 164, a dense one of as many bytes 153); 23705 tokens of 21 GQA heads
+// of 96 take 33.5 us, 5.7 TB/s.
 template <bool GQA, int PAIRING, int U, bool STREAM>
 __global__ __launch_bounds__(256) void append_kernel(AppendLaunch a) {
   auto load = [](const uint16_t* p) { return *reinterpret_cast<const chunk_t*>(p); };
@@ -272,7 +272,7 @@ hipError_t launch_pieces(AppendLaunch a, int pairing, hipStream_t s) {
 
 // Once one piece a wave would fill the chip's 256 x 32 waves, four of them, and
 // stores past the caches: 1152 pieces (96 tokens) take 4.1 us one by one and 4.8 us
-// in pairs; 150 thousand take 50.1 us one by one, 38.2 in pairs, 36.6 by four, and
+// in pairs; 142 thousand take 50.1 us one by one, 38.2 in pairs, 36.6 by four, and
 // 33.0 by four with streamed stores (streamed loads: 34.6).  MLA: one piece (its
 // prompts 164.6 us, streamed stores 155.0, loads too 159.4, then in pairs 163.1).
 hipError_t launch_append(const AppendLaunch& a, bool gqa, int pairing, hipStream_t s) {

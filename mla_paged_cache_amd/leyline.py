@@ -686,7 +686,10 @@ class Step:
 
     A call runs on `stream` (None: the current one), and results that it allocates
     belong to that stream.  Inputs made on another one, and results read on another
-    one, are the caller's to order and to keep (torch's record_stream)."""
+    one, are the caller's to order and to keep (torch's record_stream).
+
+    A graph that holds calls of a step needs the step, which owns their workspace:
+    keep it open for as long as the graph is replayed."""
 
     def __init__(self, pool: Pool, heads: int, max_seqs: int, max_tokens: int):
         import torch
