@@ -748,7 +748,7 @@ class Step:
                 n, d = t.shape
                 ts, one = t.stride()
                 hs, ok = 0, d == tail[0]
-            ok = ok and one == 1 and t.dtype is dtype and t.device == self.device
+            ok = ok and (one == 1 or n == 0) and t.dtype is dtype and t.device == self.device
         except (AttributeError, TypeError, ValueError):   # no tensor, or one of other axes
             ok = False
         if not ok:
