@@ -5,20 +5,18 @@
 //   out = sum_j exp(s_j - m) v_j / l,       lse = m + log l.
 // One pass over the rows keeps m, l and the unscaled sum of v, in float32; when m
 // grows, l and the sum are scaled down.  Scores are kept in base 2 (times
-// log2 e), so that each exponential is one instruction.
+// log2 e), so that each exponential is one instruction.  With a cap,
+//   s_j = cap * tanh(scale * q . k_j / cap).
 #include <atomic>
 #include <type_traits>
 
-#include "device_common.h"
+#include "matrix_common.h"
 #include "step_internal.h"
 
 namespace ll {
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kAttendThreads = 256;
-
-__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // The cached rows [lo, hi) that query row r of an item's sequence sees, and the
 // item's share of the rows its whole tile needs.
@@ -56,28 +54,6 @@ __device__ __forceinline__ int64_t physical_row(const AttendLaunch& a, int seq, 
   return (static_cast<int64_t>(page) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
 }
 
-struct Vals {
-  float v[8];
-};
-__device__ __forceinline__ Vals load8(const uint16_t* p, bool live) {
-  chunk_t c{0u, 0u, 0u, 0u};
-  if (live) c = *reinterpret_cast<const chunk_t*>(p);
-  Vals r;
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = bf16_lo(w[i]);
-    r.v[2 * i + 1] = bf16_hi(w[i]);
-  }
-  return r;
-}
-__device__ __forceinline__ float dot8(const Vals& x, const Vals& y) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x.v[i], y.v[i], s);
-  return s;
-}
-
 // One query row at a time per wave, one cached row at a time: a lane holds 8
 // values of the head (MLA: of the latent part, and of k_pe in lanes 0..7).
 // Reads exactly the rows that the query sees.
@@ -112,7 +88,7 @@ __device__ void attend_rows(const AttendLaunch& a, const AttendItem& it, const S
         x = dot8(q, k) + dot8(qp, load8(p + kKvLoraRank, lane < 8));
       }
       for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d);
-      x *= a.scale * kLog2e;
+      x = a.cap > 0.f ? a.cap * kLog2e * tanh_any(x * (a.scale / a.cap)) : x * (a.scale * kLog2e);
       const float m2 = fmaxf(m, x);
       const float keep = m == m2 ? 1.f : exp2_(m - m2);
       const float p = x == -__builtin_inff() ? 0.f : exp2_(x - m2);
@@ -144,13 +120,6 @@ __device__ void attend_rows(const AttendLaunch& a, const AttendItem& it, const S
   }
 }
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) char* lds_ptr;
-
 // A tile of cached rows in LDS: regions of ROWCH 16-byte chunks per row, chunk c
 // of row r at place c ^ swizzle(r), so that both ways of reading it touch the 64
 // banks evenly.  The scores' operand is one chunk of 16 rows per 16 lanes; the
@@ -167,23 +136,6 @@ __device__ __forceinline__ int swizzle(int r) {
     const int h = (r >> 1) & 7;
     return (((h & 3) ^ ((h >> 1) & 2)) << 1) | (h >> 2);
   }
-}
-
-__device__ __forceinline__ bf16x8 lds_chunk(lds_ptr p) {
-  return *reinterpret_cast<__attribute__((address_space(3))) bf16x8*>(p);
-}
-// 16 lanes read 4 rows x 16 columns (8 bytes each) and get them transposed: lane
-// i the 4 rows of column i.
-__device__ __forceinline__ s16x4 lds_columns(lds_ptr p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4*>(p));
-}
-
-// Bits kNotFinite of the result are set where one of the chunk's values has all
-// exponent bits set: one more in its lowest exponent bit then reaches the sign's.
-constexpr uint32_t kNotFinite = 0x80008000u;
-__device__ __forceinline__ uint32_t exponents(chunk_t c) {
-  const chunk_t e = (c & 0x7F807F80u) + 0x00800080u;
-  return e.x | e.y | e.z | e.w;
 }
 
 // How a workgroup does one item: QW waves side by side over the query rows (QN
@@ -228,40 +180,6 @@ struct Shape {
   static_assert(BN * ROWCH / 64 % WAVES == 0 && AHEAD >= 2, "as many loads for every wave; the next tile is there early");
   static_assert(LOADS * (AHEAD - 1) < 64, "the wait counter's range");
 };
-
-// The assembly below declares that it writes m0.  The compiler keeps no value there
-// between its own uses (and warns that a reserved register is declared), but it may
-// share one setting of m0 between several of those, which the declaration ends.
-#pragma clang diagnostic ignored "-Winline-asm"
-
-// 64 x 16 bytes from memory straight into LDS at `dst` + 16 * lane (base: uniform;
-// off: the lane's byte offset).  As assembly, because the compiler otherwise waits
-// for every such load before each transposing LDS read; it has no result
-// register, and the kernel waits for it itself (`landed`, then a barrier).
-// ONCE: nothing else of the launch reads the bytes, so that they need not stay in
-// the caches.
-template <bool ONCE>
-__device__ __forceinline__ void load_lds(lds_ptr dst, const void* base, uint32_t off) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
-  // (five wait states between a vector instruction that writes `base` and the load)
-  if constexpr (ONCE)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(at), "v"(off), "s"(base) : "m0", "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "m0", "memory");
-}
-template <bool ONCE>
-__device__ __forceinline__ void load_lds(lds_ptr dst, const void* src) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
-  if constexpr (ONCE)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(at), "v"(src) : "m0", "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "m0", "memory");
-}
-
-__device__ __forceinline__ void load_lds4(lds_ptr dst, const void* src) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst)));
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "m0", "memory");
-}
 
 // A tile from the cache to LDS: an instruction fills 64 consecutive places, so
 // each lane fetches the chunk that the swizzle puts at its place.  Lane r holds
@@ -328,7 +246,7 @@ __device__ __forceinline__ void load_gqa_piece(int i, const uint16_t* k, const u
 // 1683 us (43% busy), 4096 GQA tokens of 32 heads over 32768 rows 2148 us (44%).
 // These are medians of the first twelve calls; the fastest took 250, 412, 1580 and
 // 1970 us, for the chunks the last one, from which on they stay there.
-template <typename S>
+template <typename S, bool CAP>
 __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::WAVES > 4 ? 2 : 1))) void attend_kernel(AttendLaunch a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   constexpr int QN = S::QN, KT = S::KVT / 16, KK = S::DK / 32;
@@ -382,6 +300,9 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
       }
   }
   c2 = nothing ? 1.f : fabsf(c2);
+  // capped scores come out of the tanh in base 2
+  const float to_cap = CAP ? fabsf(a.scale / a.cap) : 0.f, cap2 = CAP ? a.cap * kLog2e : 0.f;
+  if constexpr (CAP) c2 = 1.f;
 
   f32x4 o[DT][ON];
   float m[QN], l[QN];
@@ -503,6 +424,34 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   bool rows_only = false;
   for (int tile = 0; tile < tiles; ++tile) {
     const int j0 = share.lo + tile * S::BN;
+    if constexpr (CAP) {
+      float most = 0.f;
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int n = 0; n < QN; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[k][n][e] *= to_cap;
+            most = fmaxf(most, fabsf(s[k][n][e]));
+          }
+      // (a NaN takes either way: both give NaN)
+      if (__any(most > 0.5f)) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+          for (int n = 0; n < QN; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[k][n][e] = cap2 * tanh_any(s[k][n][e]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+          for (int n = 0; n < QN; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[k][n][e] = cap2 * tanh_small(s[k][n][e]);
+      }
+    }
     if (j0 < full_lo || j0 + S::BN > full_hi) {   // some query does not see all of the tile
       uint32_t bits = 0;
 #pragma unroll 8
@@ -857,20 +806,25 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   }
 }
 
-template <typename S>
-hipError_t launch_shape(const AttendLaunch& a, hipStream_t s) {
+template <typename S, bool CAP>
+hipError_t launch_kernel(const AttendLaunch& a, hipStream_t s) {
   constexpr int lds = S::LDS;
   static std::atomic<bool> set[64];   // per device: hipFuncSetAttribute is not cheap
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_kernel<S>), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_kernel<S, CAP>), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  attend_kernel<S><<<dim3(static_cast<unsigned>(int64_t{a.n_items} * a.kv_heads)), dim3(S::THREADS), lds, s>>>(a);
+  attend_kernel<S, CAP><<<dim3(static_cast<unsigned>(int64_t{a.n_items} * a.kv_heads)), dim3(S::THREADS), lds, s>>>(a);
   return hipGetLastError();
+}
+
+template <typename S>
+hipError_t launch_shape(const AttendLaunch& a, hipStream_t s) {
+  return a.cap > 0.f ? launch_kernel<S, true>(a, s) : launch_kernel<S, false>(a, s);
 }
 
 // The query rows a workgroup takes follow from how many the sequences bring

@@ -61,6 +61,8 @@ __global__ __launch_bounds__(256) void step_setup_kernel(StepSetupLaunch a) {
   };
   copy(a.src_items, a.dst_items, a.counts.items);
   copy(a.src_own, a.dst_own_items, a.own_counts.items);
+  const chunk_t* seqs = reinterpret_cast<const chunk_t*>(a.src_seqs);
+  for (int64_t i = t; i < int64_t{a.counts.seqs} * 3; i += stride) reinterpret_cast<chunk_t*>(a.dst_seqs)[i] = seqs[i];
   // a wave per sequence
   for (int64_t i = t >> 6; i < a.counts.seqs; i += stride >> 6) {
     const StepSeq s = a.src_seqs[i];

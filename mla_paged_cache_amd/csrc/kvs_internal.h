@@ -6,7 +6,11 @@
 
 #include <cstdint>
 
+struct kvs_ctx;
+
 namespace ll {
+
+int32_t kvs_device(const kvs_ctx* ctx);   // the context's device
 
 // One rollout of a death-time call.
 struct alignas(16) KvsRollout {

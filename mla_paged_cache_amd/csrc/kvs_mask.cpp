@@ -48,6 +48,8 @@ struct kvs_ctx {
   hipStream_t events_stream = nullptr;  // the stream of the call that recorded events_done
 };
 
+int32_t ll::kvs_device(const kvs_ctx* ctx) { return ctx->device; }
+
 namespace {
 
 using ll::fail;

@@ -14,61 +14,17 @@
 #include <new>
 #include <vector>
 
-#include "../../include/leyline_step.h"
-#include "host_common.h"
-#include "pool_internal.h"
-#include "step_internal.h"
+#include "../../include/leyline_weight.h"
+#include "step_host.h"
 
 namespace {
 
-using ll::ceil_div;
-using ll::fail;
+using namespace ll;
 
-constexpr int64_t kMaxStride = int64_t{1} << 32;
 // Partial results of split tiles: values that the step's buffer holds (128 MiB),
 // and shares (times KV heads) at most.
 constexpr int64_t kPartValues = int64_t{1} << 25;
 constexpr int64_t kMaxShares = 2048;
-
-// A plan of the attention: the current begin's, in tiles of `tile` query rows.
-struct Plan {
-  int32_t tile = 16;
-  int64_t items = 0;
-  int64_t shares = 0;            // of them shares of split tiles, which a second kernel joins
-  ll::StepCounts* d_counts = nullptr;
-  ll::AttendItem* d_items = nullptr;
-};
-
-}  // namespace
-
-struct ll_step {
-  ll_pool* pool = nullptr;       // cleared when the pool ends
-  int32_t device = 0;
-  int32_t heads = 0, kv_heads = 1, group = 1;
-  int32_t max_seqs = 0, max_tokens = 0;
-  int32_t value_dim = 0;         // width of an output head
-  int64_t max_items = 0;         // of a plan
-  bool captured = false;         // a graph holds plans[0]: its tile stays
-  // What graphs read, and eager calls too unless a graph holds another tile than
-  // they would take: they have a plan of their own then.  One at a time uses the
-  // partial results.
-  Plan plans[2];
-  int eager = 0;
-  // device: [counts, items, twice | rows | tab | theta | parts]
-  char* d_buf = nullptr;
-  int32_t* d_rows = nullptr;
-  float* d_tab = nullptr;
-  double* d_theta = nullptr;
-  float* d_part_o = nullptr;
-  float* d_part_ml = nullptr;
-  // the step begun last
-  bool begun = false;
-  std::vector<int32_t> seqs;
-  std::vector<uint64_t> gens;
-  int64_t tokens = 0;
-};
-
-namespace {
 
 int64_t tiles_of(int64_t q_rows, int tile) { return ceil_div(q_rows, tile); }
 
@@ -165,43 +121,6 @@ int64_t plan_items(const ll_step* s, int tile, const std::vector<ll::StepSeq>& s
   return slot;
 }
 
-ll_status check_step(const ll_step* s) {
-  if (!s) return fail(LL_EINVAL, "step is NULL");
-  if (!s->pool) return fail(LL_EINVAL, "the step's pool has been destroyed");
-  return ll::pool_check(s->pool);
-}
-
-// The step still fits its sequences.
-ll_status check_current(const ll_step* s) {
-  if (!s->begun) return fail(LL_EINVAL, "the step has not begun");
-  for (size_t i = 0; i < s->seqs.size(); ++i)
-    if (s->pool->seqs[s->seqs[i]].gen != s->gens[i])
-      return fail(LL_EINVAL, "sequence %d has changed since the step began", s->seqs[i]);
-  return LL_OK;
-}
-
-ll_status is_capturing(hipStream_t st, bool* out) {
-  hipStreamCaptureStatus c = hipStreamCaptureStatusNone;
-  hipError_t e = hipStreamIsCapturing(st, &c);
-  if (e != hipSuccess) {
-    (void)hipGetLastError();
-    return fail(LL_EUNSUPPORTED, "the stream's capture state: %s", hipGetErrorString(e));
-  }
-  *out = c != hipStreamCaptureStatusNone;
-  return LL_OK;
-}
-
-// A stride that no second token or head uses says nothing.
-int64_t used(int64_t stride, int64_t n) { return n > 1 ? stride : 0; }
-
-ll_status check_plane(const void* p, int64_t ts, int64_t hs, const char* name) {
-  if (!p) return fail(LL_EINVAL, "%s is NULL", name);
-  if (reinterpret_cast<uintptr_t>(p) & 15) return fail(LL_EINVAL, "%s is not 16-byte aligned", name);
-  if ((ts & 7) || (hs & 7) || ts < 0 || hs < 0 || ts > kMaxStride || hs > kMaxStride)
-    return fail(LL_EINVAL, "%s: strides must be multiples of 8 values in [0, 2^32]", name);
-  return LL_OK;
-}
-
 // Rows of an output may not overlap: either tokens lie outside heads or heads
 // outside tokens.
 ll_status check_output(int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t width, const char* name) {
@@ -210,26 +129,6 @@ ll_status check_output(int64_t ts, int64_t hs, int64_t tokens, int64_t heads, in
   const bool head_major = t >= width && (tokens == 1 ? h >= width : h >= (tokens - 1) * ts + width);
   if (!token_major && !head_major) return fail(LL_EINVAL, "%s: rows overlap", name);
   return LL_OK;
-}
-
-// The caller's buffers hold every token that the call may touch: the step's, or
-// under capture (later begins are replayed) as many as the step can have.
-ll_status check_room(const ll_step* s, int64_t tokens, bool capturing) {
-  const int64_t need = capturing ? s->max_tokens : s->tokens;
-  if (tokens < need) return fail(LL_EINVAL, "buffers for %lld tokens, but the call may touch %lld", (long long)tokens, (long long)need);
-  return LL_OK;
-}
-
-// Eager calls follow the pool's earlier work; a captured one is the caller's to
-// order.
-ll_status start(ll_step* s, hipStream_t st, bool capturing) {
-  return capturing ? LL_OK : ll::pool_begin_call(s->pool, st);
-}
-
-void finish(ll_step* s, hipStream_t st, bool capturing) {
-  if (capturing) return;
-  s->pool->last_stream = st;
-  s->pool->unevented = true;
 }
 
 }  // namespace
@@ -264,6 +163,7 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
   s->value_dim = p->gqa ? p->head_chunks * 8 : ll::kKvLoraRank;
   s->seqs.reserve(static_cast<size_t>(d->max_seqs));
   s->gens.reserve(static_cast<size_t>(d->max_seqs));
+  s->lens.reserve(static_cast<size_t>(d->max_seqs));
   const int tile = ll::attend_tile(p->gqa, s->value_dim, int64_t{d->max_tokens} * s->group);
   s->max_items = int64_t{d->max_tokens} * s->group / 16 + d->max_seqs + kMaxShares / kv_heads;
   if (s->max_items * kv_heads > ll::kMaxDispatchItems / 512)   // of up to 512 threads
@@ -280,6 +180,7 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
     o_counts[k] = take(sizeof(ll::StepCounts));
     o_items[k] = take(sizeof(ll::AttendItem) * static_cast<size_t>(s->max_items));
   }
+  const size_t o_seqs = take(sizeof(StepSeq) * static_cast<size_t>(d->max_seqs));
   const size_t o_rows = take(sizeof(int32_t) * static_cast<size_t>(d->max_tokens));
   const size_t o_tab = take(sizeof(float) * 2 * pairs * static_cast<size_t>(d->max_tokens));
   const size_t o_theta = take(sizeof(double) * pairs);
@@ -296,6 +197,7 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
     s->plans[k].d_counts = reinterpret_cast<ll::StepCounts*>(s->d_buf + o_counts[k]);
     s->plans[k].d_items = reinterpret_cast<ll::AttendItem*>(s->d_buf + o_items[k]);
   }
+  s->d_seqs = reinterpret_cast<StepSeq*>(s->d_buf + o_seqs);
   s->d_rows = reinterpret_cast<int32_t*>(s->d_buf + o_rows);
   s->d_tab = reinterpret_cast<float*>(s->d_buf + o_tab);
   s->d_theta = reinterpret_cast<double*>(s->d_buf + o_theta);
@@ -455,6 +357,7 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
   a.dst_own_items = s->plans[1].d_items;
   a.rows = s->d_rows;
   a.tab = s->d_tab;
+  a.dst_seqs = s->d_seqs;
   hipError_t e = ll::launch_step_setup(a, st);
   if (e != hipSuccess) return ll::pool_device_fail(p, e, "step_setup_kernel launch");
   if ((rc = ll::pool_end_call(p, sg, st))) return rc;
@@ -463,6 +366,7 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
   for (int32_t pg : fresh) p->free.take(pg);
   p->free.advance_hint();
   s->seqs.assign(seq_ids, seq_ids + n);
+  s->lens.resize(static_cast<size_t>(n));
   for (int32_t i = 0; i < n; ++i) {
     ll::SeqState& q = p->seqs[seq_ids[i]];
     if (grow && counts[i] > 0) {
@@ -472,7 +376,9 @@ ll_status ll_step_begin(ll_step* s, const int32_t* seq_ids, const int32_t* count
       q.gen = ++p->epoch;
     }
     gens[i] = q.gen;
+    s->lens[i] = q.len;
   }
+  s->most = most;
   s->gens = std::move(gens);
   s->plans[0].tile = graph_tile;
   s->plans[0].items = static_cast<int64_t>(items.size());
@@ -565,7 +471,11 @@ ll_status ll_step_append(ll_step* s, const ll_append_desc* d, void* stream) try 
   return ll::pool_host_exception(s ? s->pool : nullptr);
 }
 
-ll_status ll_step_attend(ll_step* s, const ll_attend_desc* d, void* stream) try {
+ll_status ll_step_attend(ll_step* s, const ll_attend_desc* d, void* stream) {
+  return ll_step_attend_capped(s, d, 0.f, stream);
+}
+
+ll_status ll_step_attend_capped(ll_step* s, const ll_attend_desc* d, float cap, void* stream) try {
   ll_status rc = check_step(s);
   if (rc) return rc;
   if (!d) return fail(LL_EINVAL, "NULL argument");
@@ -576,11 +486,7 @@ ll_status ll_step_attend(ll_step* s, const ll_attend_desc* d, void* stream) try 
   bool capturing = false;
   if ((rc = is_capturing(st, &capturing))) return rc;
   if ((rc = check_room(s, d->tokens, capturing))) return rc;
-  if (d->layer < 0 || d->layer >= p->desc.num_layers) return fail(LL_EINVAL, "layer %d out of range", d->layer);
-  if (d->causal != 0 && d->causal != 1) return fail(LL_EINVAL, "causal must be 0 or 1");
-  if (d->window < 0 || (d->window > 0 && !d->causal)) return fail(LL_EINVAL, "window must be >= 0, and needs causal");
-  // (the kernels keep scores in base 2)
-  if (!std::isfinite(d->scale * ll::kLog2e)) return fail(LL_EINVAL, "scale, times log2 e, is not finite");
+  if ((rc = check_scores(p, d->layer, d->causal, d->window, d->scale, cap))) return rc;
   const int64_t T = capturing ? s->max_tokens : s->tokens;
   if (T == 0) return LL_OK;
   if ((rc = check_plane(d->q, used(d->q_token_stride, T), used(d->q_head_stride, s->heads), "q"))) return rc;
@@ -605,6 +511,7 @@ ll_status ll_step_attend(ll_step* s, const ll_attend_desc* d, void* stream) try 
   a.causal = d->causal;
   a.window = static_cast<int32_t>(std::min<int64_t>(d->window, INT32_MAX));
   a.scale = d->scale;
+  a.cap = cap;
   a.dim = s->value_dim;
   a.k_plane = static_cast<const uint16_t*>(p->layer_ptrs[static_cast<size_t>(d->layer)]);
   a.v_plane = p->gqa ? static_cast<const uint16_t*>(p->layer_ptrs[static_cast<size_t>(p->desc.num_layers + d->layer)]) : nullptr;

@@ -69,6 +69,7 @@ struct StepSetupLaunch {
   AttendItem* dst_own_items;
   int32_t* rows;                 // [tokens] physical row, -1: none
   float* tab;                    // [tokens][2][pairs] float32 cos, then sin
+  StepSeq* dst_seqs;             // [counts.seqs]
 };
 
 // One layer's rows and queries.
@@ -113,6 +114,7 @@ struct AttendLaunch {
   int32_t causal;
   int32_t window;                // 0: none
   float scale;                   // natural scores
+  float cap;                     // > 0: scores are cap * tanh(scale q k / cap); 0: scale q k
   int32_t dim;                   // GQA head_dim
   const uint16_t* k_plane;       // MLA: the layer's rows
   const uint16_t* v_plane;

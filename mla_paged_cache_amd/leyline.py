@@ -1,5 +1,5 @@
-"""Python binding of libleyline.so (include/leyline.h, include/leyline_step.h):
-argument marshalling only.
+"""Python binding of libleyline.so (include/leyline.h, include/leyline_step.h,
+include/leyline_weight.h, include/leyline_train.h): argument marshalling only.
 
 Every step of the splice / evict path runs in the library's HIP kernels and
 C++ host planner; this module turns torch tensors into device pointers and
@@ -41,6 +41,10 @@ EXPORTS = (
 
 # Every symbol include/leyline_step.h declares.
 STEP_EXPORTS = ("ll_step_create", "ll_step_destroy", "ll_step_begin", "ll_step_append", "ll_step_attend")
+
+# Every symbol include/leyline_weight.h and include/leyline_train.h declare.
+WEIGHT_EXPORTS = ("ll_step_attend_capped", "ll_step_weigh", "ll_keep_heaviest")
+TRAIN_EXPORTS = ("kvs_attend_workspace", "kvs_attend", "kvs_attend_backward")
 
 
 class LeylineError(RuntimeError):
@@ -132,6 +136,10 @@ class _StepDesc(ctypes.Structure):
 # ll_append_desc and ll_attend_desc, packed in their C layout
 _APPEND_DESC = struct.Struct("@qii Pqq Pqq P Pqq Pqq P f4x")
 _ATTEND_DESC = struct.Struct("@qiiq f4x Pqq Pqq Pqq P")
+# ll_weigh_desc, kvs_attend_desc and what kvs_attend_backward_desc has behind it
+_WEIGH_DESC = struct.Struct("@qiiq ff Pqq Pqq P P q f4x")
+_TRAIN_DESC = struct.Struct("@iiq iiiff4x P Pqqq Pqqq Pqqq Pqqq P Pq")
+_TRAIN_GRADS = struct.Struct("@Pqqq Pqqq Pqqq Pqqq")
 
 
 def _load():
@@ -173,6 +181,12 @@ def _load():
         "ll_step_begin": (i32, [vp, vp, vp, i32, i32, vp]),
         "ll_step_append": (i32, [vp, vp, vp]),
         "ll_step_attend": (i32, [vp, vp, vp]),
+        "ll_step_attend_capped": (i32, [vp, vp, ctypes.c_float, vp]),
+        "ll_step_weigh": (i32, [vp, vp, vp]),
+        "ll_keep_heaviest": (i32, [vp, vp, i32, vp, i64, i64, vp, vp, i64, vp, vp, vp]),
+        "kvs_attend_workspace": (i32, [vp, i32, P(i64)]),
+        "kvs_attend": (i32, [vp, vp, vp]),
+        "kvs_attend_backward": (i32, [vp, vp, vp]),
         "ll_last_error": (ctypes.c_char_p, []),
         "ll_status_str": (ctypes.c_char_p, [i32]),
     }
@@ -417,6 +431,51 @@ class Pool:
         _check(_lib.kv_evict_compact(self._h, s_ptr, len(s_arr), keep.data_ptr(),
                                      o_arr.ctypes.data if len(o_arr) else None, _stream_handle(stream, self._dev)))
 
+    def _weights(self, w, name: str):
+        """Address and rows of a float32 tensor [max_seqs][rows]."""
+        import torch
+        if not isinstance(w, torch.Tensor) or w.dtype != torch.float32 or w.device != self.device or w.dim() != 2 \
+                or w.shape[0] != self.max_seqs or not w.is_contiguous():
+            raise ValueError(f"{name}: need a contiguous float32 tensor [{self.max_seqs}][rows] on {self.device}")
+        return w.data_ptr(), w.shape[1]
+
+    def keep_heaviest(self, seqs, budgets, weights, sinks: int = 0, recent: int = 0, keep=None, kept_weights=None,
+                      stream=None):
+        """Keep masks of the heaviest rows (ll_keep_heaviest): of sequence seqs[i]
+        min(budgets[i], its rows) rows, the first `sinks` and the last `recent` ones
+        before all others, ties to the earlier row.  weights: float32 [max_seqs][rows]
+        (see Step.weigh).  kept_weights: the tensor that gets the weights moved as the
+        eviction moves the rows (weights itself: in place; None: no one does).  Returns
+        (keep, offsets) as evict(seqs, keep, offsets) takes them; keep: a uint8 tensor
+        with room for the masks, new when not given."""
+        import torch
+        s_arr, s_ptr = _i32_array(seqs)
+        b_arr = np.ascontiguousarray(np.asarray(budgets, dtype=np.int64)).reshape(-1)
+        if len(b_arr) != len(s_arr):
+            raise ValueError(f"{len(s_arr)} sequences but {len(b_arr)} budgets")
+        w_ptr, w_rows = self._weights(weights, "weights")
+        o_ptr = None
+        if kept_weights is not None:
+            o_ptr, o_rows = self._weights(kept_weights, "kept_weights")
+            if o_rows != w_rows:
+                raise ValueError("kept_weights and weights must have one shape")
+        lens = np.zeros(len(s_arr), np.int64)
+        if len(s_arr):
+            _check(_lib.ll_seq_lengths(self._h, s_ptr, len(s_arr), lens.ctypes.data))
+        total = int(lens.sum())
+        offsets = np.cumsum(lens) - lens
+        if keep is None:
+            with _on(stream, self._dev):
+                keep = torch.empty(total, dtype=torch.uint8, device=self.device)
+        elif not isinstance(keep, torch.Tensor) or keep.dtype != torch.uint8 or keep.device != self.device \
+                or not keep.is_contiguous() or keep.numel() < total:
+            raise ValueError(f"keep must be a contiguous uint8 tensor of {total} bytes or more on {self.device}")
+        if total:
+            _check(_lib.ll_keep_heaviest(self._h, s_ptr, len(s_arr), b_arr.ctypes.data, int(sinks), int(recent), w_ptr,
+                                         o_ptr, w_rows, keep.data_ptr(), offsets.ctypes.data,
+                                         _stream_handle(stream, self._dev)))
+        return keep, offsets
+
     def rope_rows(self, seq: int, row_begin: int, angles, out=None, stream=None):
         """Turn the RoPE bands of rows [row_begin, row_begin + len(angles)) of
         a sequence by their own angle steps (angles: int64 CUDA tensor).  With
@@ -567,7 +626,8 @@ class _Logs:
 
 class KvsMask:
     """KV-streams trainer-side attention mask on one device: death times from
-    the engine's eviction logs, then a block mask or a dense bit mask.
+    the engine's eviction logs, then a block mask, a dense bit mask, or the
+    attention under them and its gradient (include/leyline_train.h).
 
     A log is a list of (time, keep) events per rollout, keep being the mask the
     engine passed to its eviction call (uint8 over the rows held then)."""
@@ -672,6 +732,128 @@ class KvsMask:
         _require(out, "out", torch.int32, (n, n_pad, n_pad // 32), self._tdev)
         _check(_lib.kvs_dense_mask(self._h, death.data_ptr(), n, n_pad, out.data_ptr(), _stream_handle(stream, self.device)))
         return out
+
+
+    # -- the trainer's attention
+    def _heads(self, t, name: str, shape):
+        """(address, rollout, token and head stride) of a bf16 tensor of `shape`
+        [n][n_pad][heads][width] on this device with a dense last axis."""
+        import torch
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != self._tdev \
+                or tuple(t.shape) != shape or (t.stride(3) != 1 and t.numel()):
+            raise ValueError(f"{name}: need a bf16 tensor {list(shape)} on {self._tdev} with a dense last axis")
+        return (t.data_ptr(), *t.stride()[:3])
+
+    def _attend_desc(self, q, k, v, death, scale, cap, out, lse, backward: bool, stream):
+        """The packed kvs_attend_desc, with `out` and `lse` (new where None) and the
+        workspace that it names."""
+        import torch
+        self._check_death(death)
+        if not all(isinstance(t, torch.Tensor) and t.dim() == 4 for t in (q, k, v)):
+            raise ValueError("q, k and v must be 4-D tensors [n][n_pad][heads][width]")
+        n, n_pad = death.shape
+        heads, kv_heads, dk, dv = q.shape[2], k.shape[2], q.shape[3], v.shape[3]
+        q_s = self._heads(q, "q", (n, n_pad, heads, dk))
+        k_s = self._heads(k, "k", (n, n_pad, kv_heads, dk))
+        v_s = self._heads(v, "v", (n, n_pad, kv_heads, dv))
+        with _on(stream, self.device):
+            if out is None:
+                out = torch.empty((n, n_pad, heads, dv), dtype=torch.bfloat16, device=self._tdev)
+            if lse is None:
+                lse = torch.empty((n, n_pad, heads), dtype=torch.float32, device=self._tdev)
+            o_s = self._heads(out, "out", (n, n_pad, heads, dv))
+            _require(lse, "lse", torch.float32, (n, n_pad, heads), self._tdev)
+
+            def pack(work, size):
+                try:
+                    return _TRAIN_DESC.pack(n, heads, n_pad, kv_heads, dk, dv, scale, cap, death.data_ptr(), *q_s, *k_s,
+                                            *v_s, *o_s, lse.data_ptr(), work, size)
+                except (struct.error, OverflowError) as e:
+                    raise ValueError(f"sizes, scale or cap: {e}") from None
+
+            size = ctypes.c_int64()
+            _check(_lib.kvs_attend_workspace(pack(0, 0), 1 if backward else 0, ctypes.byref(size)))
+            work = torch.empty(size.value, dtype=torch.uint8, device=self._tdev)
+        return pack(work.data_ptr(), size.value), out, lse, work
+
+    def attend(self, q, k, v, death, scale: float | None = None, cap: float = 0.0, out=None, lse=None, stream=None):
+        """Attention under death times (kvs_attend): query t of a rollout sees key s iff
+        s <= t < death[s].  q [n][n_pad][heads][key width], k [n][n_pad][KV heads][key
+        width], v [n][n_pad][KV heads][value width], bf16 views with a dense last axis and
+        the other strides multiples of 8 values; death as death_times gives it.  scale
+        defaults to the key width ** -0.5; cap > 0: scores are cap * tanh(scale * q . k /
+        cap).  Returns (out [n][n_pad][heads][value width], lse float32
+        [n][n_pad][heads]).  Nothing of it is differentiable: see attention."""
+        if scale is None:
+            scale = q.shape[-1] ** -0.5
+        desc, out, lse, work = self._attend_desc(q, k, v, death, scale, cap, out, lse, False, stream)
+        _check(_lib.kvs_attend(self._h, desc, _stream_handle(stream, self.device)))
+        return out, lse
+
+    def attend_backward(self, dout, q, k, v, out, lse, death, scale: float | None = None, cap: float = 0.0, grads=None,
+                        stream=None):
+        """The gradients (dq, dk, dv) of attend for the gradient dout of its out
+        (kvs_attend_backward); out and lse are what attend returned for the same inputs.
+        grads: three bf16 tensors shaped as q, k and v to write; new ones when not given."""
+        import torch
+        if out is None or lse is None:
+            raise ValueError("out and lse of the forward pass must be given")
+        if scale is None:
+            scale = q.shape[-1] ** -0.5
+        desc, out, lse, work = self._attend_desc(q, k, v, death, scale, cap, out, lse, True, stream)
+        g_s = self._heads(dout, "dout", tuple(out.shape))
+        if grads is None:
+            with _on(stream, self.device):
+                grads = tuple(torch.empty(t.shape, dtype=torch.bfloat16, device=self._tdev) for t in (q, k, v))
+        dq, dk, dv = grads
+        desc += _TRAIN_GRADS.pack(*g_s, *self._heads(dq, "dq", tuple(q.shape)), *self._heads(dk, "dk", tuple(k.shape)),
+                                  *self._heads(dv, "dv", tuple(v.shape)))
+        _check(_lib.kvs_attend_backward(self._h, desc, _stream_handle(stream, self.device)))
+        return dq, dk, dv
+
+    def attention(self, q, k, v, death, scale: float | None = None, cap: float = 0.0):
+        """attend with a gradient: out, differentiable in q, k and v, on the current
+        stream.  Not for graph capture, forward or backward: there attend and
+        attend_backward are called themselves, so that no autograd state of an eager pass
+        takes part."""
+        return _attention_function().apply(self, q, k, v, death, scale, cap)
+
+
+_ATTENTION = None
+
+
+def _attention_function():
+    global _ATTENTION
+    if _ATTENTION is not None:
+        return _ATTENTION
+    import torch
+
+    def eager():
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("attention cannot be captured: call attend and attend_backward")
+
+    class Attention(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, kvs, q, k, v, death, scale, cap):
+            eager()
+            out, lse = kvs.attend(q, k, v, death, scale, cap)
+            ctx.kvs, ctx.scale, ctx.cap = kvs, scale, cap
+            ctx.save_for_backward(q, k, v, death, out, lse)
+            return out
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dout):
+            eager()
+            q, k, v, death, out, lse = ctx.saved_tensors
+            # a gradient may come as any view, e.g. one value broadcast
+            dout = dout.contiguous()
+            if dout.data_ptr() % 16:
+                dout = dout.clone()
+            return (None, *ctx.kvs.attend_backward(dout, q, k, v, out, lse, death, ctx.scale, ctx.cap), None, None, None)
+
+    _ATTENTION = Attention
+    return Attention
 
 
 class Step:
@@ -819,16 +1001,9 @@ class Step:
             _check(rc)
         return q_out
 
-    def attend(self, layer: int, q, q_pe=None, scale: float | None = None, causal: bool = True, window: int = 0,
-               out=None, lse=None, stream=None):
-        """Attention of the step's tokens over one layer (ll_step_attend).
-
-        MLA: q [T][heads][576] (latent part, then the rotated part), or q
-        [T][heads][512] with q_pe [T][heads][64]; the result is [T][heads][512] in
-        the latent space, and scale must be given.  GQA: q and the result are
-        [T][heads][head_dim], scale defaults to head_dim ** -0.5.  window > 0: a
-        token sees the last `window` rows up to its own.  lse=True (or a dense
-        float32 tensor [T][heads]) also returns the log sum exp: (out, lse)."""
+    def _queries(self, q, q_pe, scale):
+        """(scale, tokens, then address, token and head stride of q and of q_pe) of an
+        attention's queries."""
         bf16 = self._bf16
         if scale is None:
             if not self.gqa:
@@ -846,6 +1021,21 @@ class Step:
             room, q_ptr, q_ts, q_hs = self._rows(q, "q", self._o_tail, bf16)
             n, p_ptr, p_ts, p_hs = self._rows(q_pe, "q_pe", self._r_tail, bf16)
             room = min(room, n)
+        return scale, room, q_ptr, q_ts, q_hs, p_ptr, p_ts, p_hs
+
+    def attend(self, layer: int, q, q_pe=None, scale: float | None = None, causal: bool = True, window: int = 0,
+               out=None, lse=None, stream=None, cap: float = 0.0):
+        """Attention of the step's tokens over one layer (ll_step_attend; with a cap:
+        ll_step_attend_capped, scores cap * tanh(scale * q . k / cap)).
+
+        MLA: q [T][heads][576] (latent part, then the rotated part), or q
+        [T][heads][512] with q_pe [T][heads][64]; the result is [T][heads][512] in
+        the latent space, and scale must be given.  GQA: q and the result are
+        [T][heads][head_dim], scale defaults to head_dim ** -0.5.  window > 0: a
+        token sees the last `window` rows up to its own.  lse=True (or a dense
+        float32 tensor [T][heads]) also returns the log sum exp: (out, lse)."""
+        bf16 = self._bf16
+        scale, room, q_ptr, q_ts, q_hs, p_ptr, p_ts, p_hs = self._queries(q, q_pe, scale)
         if out is None:
             out = self._new((q.shape[0], *self._o_tail), bf16, stream)
         n, o_ptr, o_ts, o_hs = self._rows(out, "out", self._o_tail, bf16)
@@ -865,7 +1055,37 @@ class Step:
                                      o_ptr, o_ts, o_hs, l_ptr)
         except (struct.error, OverflowError) as e:
             raise ValueError(f"layer, window or scale: {e}") from None
-        rc = _lib.ll_step_attend(self._h, desc, self._raw_stream(self._dev) if stream is None else stream.cuda_stream)
+        st = self._raw_stream(self._dev) if stream is None else stream.cuda_stream
+        if cap:
+            try:
+                rc = _lib.ll_step_attend_capped(self._h, desc, cap, st)
+            except ctypes.ArgumentError as e:
+                raise ValueError(f"cap: {e}") from None
+        else:
+            rc = _lib.ll_step_attend(self._h, desc, st)
         if rc:
             _check(rc)
         return out if lse is None else (out, lse)
+
+    def weigh(self, layer: int, q, lse, weights, q_pe=None, scale: float | None = None, causal: bool = True,
+              window: int = 0, cap: float = 0.0, decay: float = 1.0, stream=None):
+        """Add the attention that each cached row of the step's sequences gets from the
+        step's tokens in one layer, over all heads, to weights (ll_step_weigh): a float32
+        tensor [the pool's max_seqs][rows], zeros at first, row s of sequence s.  q, q_pe,
+        scale, causal, window and cap as in the attend that gave lse; decay multiplies
+        what was there (0: it counts nothing).  Returns weights."""
+        scale, room, q_ptr, q_ts, q_hs, p_ptr, p_ts, p_hs = self._queries(q, q_pe, scale)
+        n, l_ptr, _, _ = self._rows(lse, "lse", self._l_tail, self._f32)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+        room = min(room, n)
+        w_ptr, w_rows = self._pool._weights(weights, "weights")
+        try:
+            desc = _WEIGH_DESC.pack(room, layer, 1 if causal else 0, window, scale, cap, q_ptr, q_ts, q_hs, p_ptr, p_ts,
+                                    p_hs, l_ptr, w_ptr, w_rows, decay)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"layer, window, scale, cap or decay: {e}") from None
+        rc = _lib.ll_step_weigh(self._h, desc, self._raw_stream(self._dev) if stream is None else stream.cuda_stream)
+        if rc:
+            _check(rc)
+        return weights
