@@ -152,7 +152,7 @@ def test_oracle_attention_and_gradients(cap):
     e, grads = 1e-6, W.gradients(q, k, v, dout, seen, 0.4, cap)
     for i in range(3):
         u = g.standard_normal(grads[i].shape)
-        f = [float((W.attend(*[x + s * e * u * (j == i) for j, x in enumerate((q, k, v))], seen, 0.4, cap)[0] * dout).sum())
+        f = [float((W.attend(*[x + s * e * u if j == i else x for j, x in enumerate((q, k, v))], seen, 0.4, cap)[0] * dout).sum())
              for s in (1, -1)]
         assert abs((f[0] - f[1]) / (2 * e) - (grads[i] * u).sum()) < 1e-6
     w, _, _ = W.weigh(q, k, lse, seen, 0.4, cap)
