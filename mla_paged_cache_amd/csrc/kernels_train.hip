@@ -36,20 +36,248 @@ __device__ void train_row(const TrainLaunch& a, int r, int q, int h, int lane) {
     a.lse[(static_cast<int64_t>(r) * a.n_pad + q) * a.heads + h] = l == 0.f ? -__builtin_inff() : (m + __log2f(l)) * kLn2;
 }
 
-__global__ __launch_bounds__(256) void train_rows_kernel(TrainLaunch a) {
-  int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int q = static_cast<int>(unit % a.n_pad);
-  unit /= a.n_pad;
-  const int r = static_cast<int>(unit / a.heads), h = static_cast<int>(unit % a.heads);
-  if (r < a.n) train_row(a, r, q, h, threadIdx.x & 63);
+// What the workspace says of blocks of 64 tokens (and for the backward pass delta), a
+// wave per block and unit.  Units: 0 the keys' death times; then the KV heads' values;
+// backward also their keys, then every head's dout (with delta) and its queries.
+template <bool BACKWARD>
+__global__ __launch_bounds__(256) void train_scan_kernel(TrainLaunch a) {
+  const int lane = threadIdx.x & 63;
+  const int units = 1 + (BACKWARD ? 2 * a.kv_heads + 2 * a.heads : a.kv_heads);
+  int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int b = static_cast<int>(id % a.blocks);
+  id /= a.blocks;
+  const int r = static_cast<int>(id / units);
+  int unit = static_cast<int>(id % units);
+  if (r >= a.n) return;
+  const int t0 = b * kTrainBlock, rows = min(kTrainBlock, a.n_pad - t0);
+  if (unit == 0) {
+    int first = -1, last = -1;
+    if (lane < rows) {
+      const int d = min(a.death[static_cast<int64_t>(r) * a.n_pad + t0 + lane], a.n_pad);
+      first = last = d > t0 + lane ? d : -1;
+    }
+    for (int x = 32; x >= 1; x >>= 1) {
+      first = min(first, __shfl_xor(first, x));
+      last = max(last, __shfl_xor(last, x));
+    }
+    if (lane == 0) a.keys[static_cast<int64_t>(r) * a.blocks + b] = KeyBlock{first, last};
+    return;
+  }
+  --unit;
+  const int64_t kv_at = static_cast<int64_t>(r) * a.kv_heads * a.blocks + b, at_ = static_cast<int64_t>(r) * a.heads * a.blocks + b;
+  Heads x, y{};
+  uint32_t* odd;
+  int width = a.dv, h;
+  bool sum = false;
+  if (unit < a.kv_heads) {
+    x = a.v, h = unit, odd = a.odd_v + kv_at + static_cast<int64_t>(h) * a.blocks;
+  } else if ((unit -= a.kv_heads) < a.kv_heads) {
+    x = a.k, h = unit, odd = a.odd_k + kv_at + static_cast<int64_t>(h) * a.blocks, width = a.dk;
+  } else if ((unit -= a.kv_heads) < a.heads) {
+    x = a.dout, y = a.out, h = unit, odd = a.odd_do + at_ + static_cast<int64_t>(h) * a.blocks, sum = true;
+  } else {
+    unit -= a.heads;
+    x = a.q, h = unit, odd = a.odd_q + at_ + static_cast<int64_t>(h) * a.blocks, width = a.dk;
+  }
+  // 8, 16 or 32 lanes a row
+  const int shift = width <= 64 ? 3 : width <= 128 ? 4 : 5, c = (lane & ((1 << shift) - 1)) * 8;
+  uint32_t bits = 0;
+  for (int t = lane >> shift; t < kTrainBlock; t += 64 >> shift) {   // (whole waves: the sums go across lanes)
+    const bool live = t < rows && c < width;
+    chunk_t v{0u, 0u, 0u, 0u};
+    if (live) v = *reinterpret_cast<const chunk_t*>(at(x, r, t0 + t, h) + c);
+    bits |= exponents(v);
+    if (BACKWARD && sum) {
+      float d = dot8(load8(at(x, r, min(t0 + t, a.n_pad - 1), h) + c, live), load8(at(y, r, min(t0 + t, a.n_pad - 1), h) + c, live));
+      for (int k = 1 << shift >> 1; k >= 1; k >>= 1) d += __shfl_xor(d, k);
+      if (c == 0 && t < rows) a.delta[(static_cast<int64_t>(r) * a.heads + h) * a.n_pad + t0 + t] = d;
+    }
+  }
+  const bool any = __any((bits & kNotFinite) != 0);
+  if (lane == 0) *odd = any;
+}
+
+// The flash kernel.  A workgroup takes 32 * WAVES queries of a head, a wave 32 of them,
+// and goes through the keys that some of them see, BN at a time, which it reads into LDS
+// while it works on those before.  Scores are computed transposed (S^T = K Q^T), so that
+// a lane holds 16 keys' scores of one query: the softmax runs along a lane's own
+// registers (and the lane 32 further), and the weights, rounded to bf16, are the operand
+// of O^T = V^T P^T as they lie.  V^T comes from the transposing LDS reads.
+//
+// The running maximum is only a reference: it moves when a score (in base 2) exceeds it
+// by more than 8, so weights stay below 2^8 and most tiles scale nothing.
+template <int DK, int DV, int BN, int WAVES, bool CAP>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 192 ? 1 : 2))) void train_kernel(TrainLaunch a) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  using KR = Rows<DK>;
+  using VR = Rows<DV>;
+  constexpr int STAGE = BN * (KR::BYTES + VR::BYTES) + kTrainBlock * 4;   // keys, values, death times
+  constexpr int KB = BN / 32, KK = DK / 16, DB = DV / 32, PARTS = kTrainBlock / BN;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // the heads of one KV head and rollout side by side, the longest tiles first
+  const int pairs = a.n * a.kv_heads, pair = blockIdx.x % pairs, rest = blockIdx.x / pairs;
+  const int r = pair / a.kv_heads, kvh = pair % a.kv_heads, h = kvh * a.group + rest % a.group;
+  const int tiles = (a.n_pad + 32 * WAVES - 1) / (32 * WAVES), tile = tiles - 1 - rest / a.group;
+  const int q0 = tile * 32 * WAVES, q1 = min(q0 + 32 * WAVES, a.n_pad) - 1;
+  const int mine = q0 + wave * 32 + (lane & 31);   // this lane's query
+  const lds_ptr lds = (lds_ptr)smem;
+  const int live_k = a.dk / 8, live_v = a.dv / 8;
+  const uint16_t* const kp = at(a.k, r, 0, kvh);
+  const uint16_t* const vp = at(a.v, r, 0, kvh);
+  const int32_t* const death = a.death + static_cast<int64_t>(r) * a.n_pad;
+
+  bf16x8 q[KK];
+  load_operand(q, at(a.q, r, min(mine, a.n_pad - 1), h), mine < a.n_pad, live_k, lane);
+  const float c = fold_scale<CAP>(q, a.scale, a.cap);
+  const float c2 = CAP ? 1.f : c, cap2 = a.cap * kLog2e;
+
+  if (live_k < KR::CH || live_v < VR::CH) {
+    for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
+    __syncthreads();
+  }
+  auto load = [&](int block, int part, int stage) {
+    const lds_ptr dst = lds + stage * STAGE;
+    const int k0 = block * kTrainBlock + part * BN;
+    KR::template load<BN, WAVES>(dst, kp, a.k.ts, k0, a.n_pad - 1, live_k, wave, lane);
+    VR::template load<BN, WAVES>(dst + BN * KR::BYTES, vp, a.v.ts, k0, a.n_pad - 1, live_v, wave, lane);
+    if (wave == 0) load_lds4(dst + BN * (KR::BYTES + VR::BYTES), death + min(k0 + lane, a.n_pad - 1));
+  };
+
+  f32x16 o[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+  float m = -__builtin_inff(), l = 0.f;
+
+  KeyWalk walk{a.keys + static_cast<int64_t>(r) * a.blocks, a.odd_v + (static_cast<int64_t>(r) * a.kv_heads + kvh) * a.blocks,
+               q0, q1, q1 / kTrainBlock + 1};
+  bool all = false, next_all = false;
+  int block = walk.first(&all, lane), part = 0, stage = 0;
+  if (block >= 0) load(block, 0, 0);
+  while (block >= 0 && !walk.rows_only) {
+    int next = block, next_part = part + 1;
+    next_all = all;
+    if (PARTS == 1 || next_part == PARTS) {
+      next = walk.next(&next_all, lane);
+      next_part = 0;
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's part of the tile
+    __syncthreads();                      // everyone's; and nobody reads the other stage any more
+    if (next >= 0) load(next, next_part, stage ^ 1);
+    const lds_ptr ks = lds + stage * STAGE, vs = ks + BN * KR::BYTES;
+    const int k0 = block * kTrainBlock + part * BN;
+
+    f32x16 s[KB];
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KK; ++k) s[b] = mfma(KR::straight(ks, b * 32, k, lane), q[k], s[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      if constexpr (CAP) {
+        tanh_all(s[b], c);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] *= cap2;
+      }
+      if (!all) {
+        const int* const d = reinterpret_cast<const int*>(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int k = b * 32 + product_row(i, lane);
+          if (k0 + k > mine || mine >= d[k]) s[b][i] = -__builtin_inff();
+        }
+      }
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+    top *= c2;
+    if (__any(top > m + 8.f)) {
+      const float x = fmaxf(fmaxf(top, m), __shfl_xor(fmaxf(top, m), 32));
+      const float keep = x == m ? 1.f : exp2_(m - x);
+      m = x;
+      l *= keep;
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] *= keep;
+    }
+    const float ref = m == -__builtin_inff() ? 0.f : m;   // nothing seen yet: every weight is 0
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[b][i] = exp2_(__builtin_fmaf(s[b][i], c2, -ref));
+        l += s[b][i];
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const bf16x8 p = operand(s[b], x);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[d] = mfma(VR::columns(vs, b * 32 + x * 16, d, lane), p, o[d]);
+      }
+    }
+    block = next, part = next_part, all = next_all, stage ^= 1;
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // loads on their way into LDS
+  if (walk.rows_only) {
+    for (int i = q0 + wave; i <= q1; i += WAVES) train_row(a, r, i, h, lane);
+    return;
+  }
+  l += __shfl_xor(l, 32);
+  if (mine >= a.n_pad) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* const out = place(a.out, r, mine, h);
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int col = d * 32 + product_row(i, lane);
+      f32x4 x{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+      // no weight at all: 0, whatever the sum holds (0 times an infinity)
+      x = l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : x * inv;
+      if (col < a.dv) *reinterpret_cast<bf16x4*>(out + col) = __builtin_convertvector(x, bf16x4);
+    }
+  if (lane < 32)
+    a.lse[(static_cast<int64_t>(r) * a.n_pad + mine) * a.heads + h] = l == 0.f ? -__builtin_inff() : (m + __log2f(l)) * kLn2;
+}
+
+template <int DK, int DV, int BN, int WAVES, bool CAP>
+hipError_t launch_shape(const TrainLaunch& a, hipStream_t s) {
+  constexpr int lds = 2 * (BN * (DK + DV) * 2 + kTrainBlock * 4);
+  hipError_t e = allow_lds<train_kernel<DK, DV, BN, WAVES, CAP>>(lds);
+  if (e != hipSuccess) return e;
+  const int64_t groups = int64_t{a.n} * a.heads * ((a.n_pad + 32 * WAVES - 1) / (32 * WAVES));
+  train_kernel<DK, DV, BN, WAVES, CAP><<<dim3(static_cast<unsigned>(groups)), dim3(64 * WAVES), lds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int DK, int DV, int BN, int WAVES>
+hipError_t launch_cap(const TrainLaunch& a, hipStream_t s) {
+  return a.cap == 0.f ? launch_shape<DK, DV, BN, WAVES, false>(a, s) : launch_shape<DK, DV, BN, WAVES, true>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_train(const TrainLaunch& a, hipStream_t s) {
-  const int64_t waves = int64_t{a.n} * a.heads * a.n_pad;
-  train_rows_kernel<<<dim3(static_cast<unsigned>((waves + 3) / 4)), dim3(256), 0, s>>>(a);
+hipError_t launch_train_scan(const TrainLaunch& a, bool backward, hipStream_t s) {
+  const int64_t units = 1 + (backward ? 2 * a.kv_heads + 2 * a.heads : a.kv_heads);
+  const dim3 g(static_cast<unsigned>((a.n * units * a.blocks + 3) / 4));
+  if (backward) train_scan_kernel<true><<<g, dim3(256), 0, s>>>(a);
+  else train_scan_kernel<false><<<g, dim3(256), 0, s>>>(a);
   return hipGetLastError();
+}
+
+hipError_t launch_train(const TrainLaunch& a, hipStream_t s) {
+  hipError_t e = launch_train_scan(a, false, s);
+  if (e != hipSuccess) return e;
+  if (a.dk <= 64 && a.dv <= 64) return launch_cap<64, 64, 64, 4>(a, s);
+  if (a.dk <= 128 && a.dv <= 128) return launch_cap<128, 128, 64, 4>(a, s);
+  if (a.dk <= 192 && a.dv <= 128) return launch_cap<192, 128, 32, 4>(a, s);
+  return launch_cap<256, 256, 32, 4>(a, s);
 }
 
 }  // namespace ll

@@ -2,12 +2,26 @@
 // backward (kernels_train_back.hip).
 #pragma once
 
+#include <atomic>
+
 #include "matrix_common.h"
 #include "step_internal.h"
 #include "train_internal.h"
 
 namespace ll {
 namespace {
+
+// Let a kernel take that much LDS; once per device and kernel, since it is not cheap.
+template <void (*K)(TrainLaunch)>
+hipError_t allow_lds(int bytes) {
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess || (dev >= 0 && dev < 64 && set[dev])) return e;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(K), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess && dev >= 0 && dev < 64) set[dev] = true;
+  return e;
+}
 
 __device__ __forceinline__ const uint16_t* at(const Heads& x, int r, int t, int h) {
   return x.p + r * x.rs + t * x.ts + h * x.hs;
@@ -42,6 +56,159 @@ __device__ __forceinline__ void add8(Vals& o, float w, const Vals& x) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) o.v[i] = __builtin_fmaf(w, x.v[i], o.v[i]);
 }
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// ---- a tile of rows in LDS, and the operands of 32x32x16 products out of it
+//
+// D values a row, in 16-byte chunks; chunk c of row r lies at place(r, c) of the row,
+// so that both ways of reading a tile touch the 64 banks evenly:
+//  * straight, 32 rows at one chunk per half wave; the hardware serves lanes 0-3,
+//    12-15, 20-27 together, and those rows differ in their last four bits;
+//  * transposing, 4 rows and 4 neighbouring chunks per half wave.
+// Rows of 128 or 384 bytes start at every other multiple of 128 bytes, which is the
+// fourth bit of difference there.
+template <int D>
+struct Rows {
+  static constexpr int CH = D / 8, BYTES = D * 2;
+  static_assert(CH == 8 || CH == 16 || CH == 24 || CH == 32, "the swizzles below");
+  static __device__ __forceinline__ int place(int r, int c) {
+    if constexpr (CH % 16 == 0) return c ^ ((r & 3) << 2 | (r >> 2 & 3));
+    else return c ^ ((r >> 1 & 1) << 2 | (r >> 2 & 3));
+  }
+  // Rows [row0, row0 + N) of a head (x: its row 0, ts: values from row to row) into
+  // LDS, by WAVES waves; rows past `last` repeat it, chunks past `live` are left alone.
+  template <int N, int WAVES>
+  static __device__ __forceinline__ void load(lds_ptr dst, const uint16_t* x, int64_t ts, int row0, int last, int live,
+                                              int wave, int lane) {
+    constexpr int LOADS = N * CH / 64;
+    static_assert(LOADS % WAVES == 0, "as many for every wave");
+#pragma unroll
+    for (int i = 0; i < LOADS / WAVES; ++i) {
+      const int b = i * WAVES + wave;
+      const int r = (b * 64 + lane) / CH, c = place(r, (b * 64 + lane) % CH);
+      if (c < live) load_lds<false>(dst + b * 1024, x + min(row0 + r, last) * ts + c * 8);
+    }
+  }
+  // Row r0 + (lane & 31), values 16 k + 8 (lane >> 5) on: an operand of S = X Y^T.
+  static __device__ __forceinline__ bf16x8 straight(lds_ptr x, int r0, int k, int lane) {
+    const int r = r0 + (lane & 31);
+    return lds_chunk(x + r * BYTES + (place(r, 2 * k + (lane >> 5)) << 4));
+  }
+  // Column 32 d + (lane & 31) of the rows that a lane of the 32x32 products holds:
+  // r0 + 4 (lane >> 5) + {0 .. 3, 8 .. 11}.
+  static __device__ __forceinline__ bf16x8 columns(lds_ptr x, int r0, int d, int lane) {
+    const int li = lane & 15, c = d * 4 + (lane >> 4 & 1) * 2 + (li >> 1 & 1);
+    const int r = r0 + (lane >> 5) * 4 + (li >> 2), q = r + 8;
+    const s16x4 y0 = lds_columns(x + r * BYTES + (place(r, c) << 4) + (li & 1) * 8);
+    const s16x4 y1 = lds_columns(x + q * BYTES + (place(q, c) << 4) + (li & 1) * 8);
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
+
+// Row of a 32x32 product's value i in a lane.
+__device__ __forceinline__ int product_row(int i, int lane) { return (i >> 2) * 8 + (lane >> 5) * 4 + (i & 3); }
+
+// Values 8 x .. 8 x + 7 of a product as the operand of the next one.
+__device__ __forceinline__ bf16x8 operand(const f32x16& p, int x) {
+  typedef float f32x8 __attribute__((ext_vector_type(8)));
+  f32x8 y;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = p[8 * x + i];
+  return __builtin_convertvector(y, bf16x8);
+}
+
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// A row (of q, k, v or dout) as a lane's operand: KK steps of 16 values, this lane's 8
+// of each; a row that is not there and chunks past `live` count as 0.
+template <int KK>
+__device__ __forceinline__ void load_operand(bf16x8 (&x)[KK], const uint16_t* row, bool there, int live, int lane) {
+#pragma unroll
+  for (int k = 0; k < KK; ++k) {
+    const int c = 2 * k + (lane >> 5);
+    chunk_t v{0u, 0u, 0u, 0u};
+    if (there && c < live) v = *reinterpret_cast<const chunk_t*>(row + c * 8);
+    x[k] = __builtin_bit_cast(bf16x8, v);
+  }
+}
+
+// A negative scale turns the queries' signs; one too small to tell scores apart counts
+// as 0, and so do the queries then.  Returns what a product is multiplied by: to base 2,
+// or under a cap to the tanh's argument.
+template <bool CAP, int KK>
+__device__ __forceinline__ float fold_scale(bf16x8 (&q)[KK], float scale, float cap) {
+  const float c = CAP ? scale / cap : scale * kLog2e;
+  const bool nothing = !(fabsf(c) >= 1e-37f);
+  if (c < 0.f || nothing) {
+    const uint32_t keep = nothing ? 0u : ~0u, flip = nothing ? 0u : 0x80008000u;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      chunk_t v = __builtin_bit_cast(chunk_t, q[k]);
+      v = (v & keep) ^ flip;
+      q[k] = __builtin_bit_cast(bf16x8, v);
+    }
+  }
+  return nothing ? 1.f : fabsf(c);
+}
+
+// tanh of each product times c: all of a wave's in the short form where that holds.
+__device__ __forceinline__ void tanh_all(f32x16& s, float c) {
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    s[i] *= c;
+    most = fmaxf(most, fabsf(s[i]));
+  }
+  if (__any(most > 0.5f)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = tanh_any(s[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = tanh_small(s[i]);
+  }
+}
+
+// The blocks of keys that queries [q0, q1] see, 64 blocks looked at together: lane x
+// looks at block base + x.  Every wave of a workgroup goes through the same ones.
+struct KeyWalk {
+  const KeyBlock* keys;          // of the rollout
+  const uint32_t* odd;           // of the rollout and KV head: blocks with values that are not finite
+  int q0, q1, blocks;            // blocks: those that begin at q1 or before
+  int base = 0;
+  uint64_t seen = 0, whole = 0;
+  bool rows_only = false;        // a block that is seen in part holds such a value
+
+  __device__ __forceinline__ void look(int lane) {
+    const int b = base + lane;
+    KeyBlock x{0, -1};
+    if (b < blocks) x = keys[b];
+    const bool some = x.last > q0, all = some && b * kTrainBlock + kTrainBlock - 1 <= q0 && x.first > q1;
+    bool bad = false;
+    if (some && !all) bad = odd[b] != 0;
+    seen = __ballot(some);
+    whole = __ballot(all);
+    rows_only |= __any(bad);
+  }
+  // The next block, or -1; `all`: every query sees every key of it.
+  __device__ __forceinline__ int next(bool* all, int lane) {
+    while (seen == 0) {
+      base += 64;
+      if (base >= blocks) return -1;
+      look(lane);
+    }
+    const int x = __builtin_ctzll(seen);
+    seen &= seen - 1;
+    *all = whole >> x & 1;
+    return base + x;
+  }
+  __device__ __forceinline__ int first(bool* all, int lane) {
+    base = -64;
+    return next(all, lane);
+  }
+};
 
 }  // namespace
 }  // namespace ll

@@ -44,6 +44,7 @@ struct TrainLaunch {
   float* delta;                  // [n][heads][n_pad]: sum of dout * out
 };
 
+hipError_t launch_train_scan(const TrainLaunch& a, bool backward, hipStream_t s);
 hipError_t launch_train(const TrainLaunch& a, hipStream_t s);
 hipError_t launch_train_back(const TrainLaunch& a, hipStream_t s);
 
