@@ -10,19 +10,6 @@
 namespace ll {
 namespace {
 
-// delta of every query and head, a wave each.
-__global__ __launch_bounds__(256) void train_delta_kernel(TrainLaunch a) {
-  const int lane = threadIdx.x & 63;
-  int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int h = static_cast<int>(unit % a.heads);
-  unit /= a.heads;
-  const int r = static_cast<int>(unit / a.n_pad), q = static_cast<int>(unit % a.n_pad);
-  if (r >= a.n) return;
-  const bool lv = lane * 8 < a.dv;
-  const float d = wave_sum(dot8(load8(at(a.dout, r, q, h) + lane * 8, lv), load8(at(a.out, r, q, h) + lane * 8, lv)));
-  if (lane == 0) a.delta[(static_cast<int64_t>(r) * a.heads + h) * a.n_pad + q] = d;
-}
-
 // One pair that is seen: the weight p and the gradient ds of its product.
 struct Pair {
   float p, ds;
@@ -75,30 +62,278 @@ __device__ void train_dkv_row(const TrainLaunch& a, int r, int k, int kvh, int l
   if (lv) store8(place(a.dv_, r, k, kvh) + lane * 8, gv, 1.f);
 }
 
-__global__ __launch_bounds__(256) void train_dq_rows_kernel(TrainLaunch a) {
-  int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int q = static_cast<int>(unit % a.n_pad);
-  unit /= a.n_pad;
-  const int r = static_cast<int>(unit / a.heads), h = static_cast<int>(unit % a.heads);
-  if (r < a.n) train_dq_row(a, r, q, h, threadIdx.x & 63);
+// A product's values as weights and their gradients: p from the score (s: scaled or
+// under the cap's tanh already; c2 to base 2), ds from dp.  What is not seen counts 0.
+//
+// dq: a workgroup takes 32 * WAVES queries of a head and goes along the keys that they
+// see, as the forward kernel does: S^T = K Q^T and dP^T = V dO^T with the queries in
+// registers, then dQ^T += K^T dS^T, K^T from the transposing LDS reads.
+template <int DK, int DV, int BN, int WAVES, bool CAP>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 192 ? 1 : 2))) void train_dq_kernel(TrainLaunch a) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  using KR = Rows<DK>;
+  using VR = Rows<DV>;
+  constexpr int STAGE = BN * (KR::BYTES + VR::BYTES) + kTrainBlock * 4;   // keys, values, death times
+  constexpr int KB = BN / 32, KK = DK / 16, VK = DV / 16, DB = DK / 32, PARTS = kTrainBlock / BN;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int pairs = a.n * a.kv_heads, pair = blockIdx.x % pairs, rest = blockIdx.x / pairs;
+  const int r = pair / a.kv_heads, kvh = pair % a.kv_heads, h = kvh * a.group + rest % a.group;
+  const int tiles = (a.n_pad + 32 * WAVES - 1) / (32 * WAVES), tile = tiles - 1 - rest / a.group;
+  const int q0 = tile * 32 * WAVES, q1 = min(q0 + 32 * WAVES, a.n_pad) - 1;
+  const int mine = q0 + wave * 32 + (lane & 31), row = min(mine, a.n_pad - 1);
+  const lds_ptr lds = (lds_ptr)smem;
+  const int live_k = a.dk / 8, live_v = a.dv / 8;
+  const uint16_t* const kp = at(a.k, r, 0, kvh);
+  const uint16_t* const vp = at(a.v, r, 0, kvh);
+  const int32_t* const death = a.death + static_cast<int64_t>(r) * a.n_pad;
+
+  bf16x8 q[KK], g[VK];
+  load_operand(q, at(a.q, r, row, h), mine < a.n_pad, live_k, lane);
+  load_operand(g, at(a.dout, r, row, h), mine < a.n_pad, live_v, lane);
+  const float c = fold_scale<CAP>(q, a.scale, a.cap);
+  const float c2 = CAP ? a.cap * kLog2e : c;
+  const float lse = a.lse[(static_cast<int64_t>(r) * a.n_pad + row) * a.heads + h];
+  const float ref = lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;   // no weight: every p is 0
+  const float delta = a.delta[(static_cast<int64_t>(r) * a.heads + h) * a.n_pad + row];
+
+  if (live_k < KR::CH || live_v < VR::CH) {
+    for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
+    __syncthreads();
+  }
+  auto load = [&](int block, int part, int stage) {
+    const lds_ptr dst = lds + stage * STAGE;
+    const int k0 = block * kTrainBlock + part * BN;
+    KR::template load<BN, WAVES>(dst, kp, a.k.ts, k0, a.n_pad - 1, live_k, wave, lane);
+    VR::template load<BN, WAVES>(dst + BN * KR::BYTES, vp, a.v.ts, k0, a.n_pad - 1, live_v, wave, lane);
+    if (wave == 0) load_lds4(dst + BN * (KR::BYTES + VR::BYTES), death + min(k0 + lane, a.n_pad - 1));
+  };
+  f32x16 o[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+
+  KeyWalk walk{a.keys + static_cast<int64_t>(r) * a.blocks, a.odd_k + (static_cast<int64_t>(r) * a.kv_heads + kvh) * a.blocks,
+               q0, q1, q1 / kTrainBlock + 1};
+  bool all = false, next_all = false;
+  int block = walk.first(&all, lane), part = 0, stage = 0;
+  if (block >= 0) load(block, 0, 0);
+  while (block >= 0 && !walk.rows_only) {
+    int next = block, next_part = part + 1;
+    next_all = all;
+    if (PARTS == 1 || next_part == PARTS) {
+      next = walk.next(&next_all, lane);
+      next_part = 0;
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's part of the tile
+    __syncthreads();                      // everyone's; and nobody reads the other stage any more
+    if (next >= 0) load(next, next_part, stage ^ 1);
+    const lds_ptr ks = lds + stage * STAGE, vs = ks + BN * KR::BYTES;
+    const int k0 = block * kTrainBlock + part * BN;
+    const int* const dt = reinterpret_cast<const int*>(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES));
+#pragma unroll 1
+    for (int b = 0; b < KB; ++b) {
+      f32x16 s, dp;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KK; ++k) s = mfma(KR::straight(ks, b * 32, k, lane), q[k], s);
+#pragma unroll
+      for (int k = 0; k < VK; ++k) dp = mfma(VR::straight(vs, b * 32, k, lane), g[k], dp);
+      if constexpr (CAP) tanh_all(s, c);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float slope = CAP ? 1.f - s[i] * s[i] : 1.f;
+        float p = exp2_(__builtin_fmaf(s[i], c2, -ref));
+        p *= (dp[i] - delta) * (a.scale * slope);
+        if (!all) {
+          const int k = b * 32 + product_row(i, lane);
+          if (k0 + k > mine || mine >= dt[k]) p = 0.f;
+        }
+        s[i] = p;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const bf16x8 ds = operand(s, x);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[d] = mfma(KR::columns(ks, b * 32 + x * 16, d, lane), ds, o[d]);
+      }
+    }
+    block = next, part = next_part, all = next_all, stage ^= 1;
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // loads on their way into LDS
+  if (walk.rows_only) {
+    for (int i = q0 + wave; i <= q1; i += WAVES) train_dq_row(a, r, i, h, lane);
+    return;
+  }
+  if (mine >= a.n_pad) return;
+  uint16_t* const out = place(a.dq, r, mine, h);
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int col = d * 32 + product_row(i, lane);
+      f32x4 x{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+      if (lse == -__builtin_inff()) x = f32x4{0.f, 0.f, 0.f, 0.f};   // no weight at all, whatever the keys hold
+      if (col < a.dk) *reinterpret_cast<bf16x4*>(out + col) = __builtin_convertvector(x, bf16x4);
+    }
 }
-__global__ __launch_bounds__(256) void train_dkv_rows_kernel(TrainLaunch a) {
-  int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int k = static_cast<int>(unit % a.n_pad);
-  unit /= a.n_pad;
-  const int r = static_cast<int>(unit / a.kv_heads), h = static_cast<int>(unit % a.kv_heads);
-  if (r < a.n) train_dkv_row(a, r, k, h, threadIdx.x & 63);
+
+// dk and dv: a workgroup takes 32 * WAVES keys of a KV head, a wave 32 of them in
+// registers, and goes along the queries that see some of them, of each head that shares
+// them, BN at a time through LDS: S = Q K^T and dP = dO V^T with a lane per key, then
+// dV^T += dO^T P and dK^T += Q^T dS, dO^T and Q^T from the transposing LDS reads.
+template <int DK, int DV, int BN, int WAVES, bool CAP>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 128 ? 1 : 2))) void train_dkv_kernel(TrainLaunch a) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  using QR = Rows<DK>;
+  using GR = Rows<DV>;
+  constexpr int STAGE = BN * (QR::BYTES + GR::BYTES) + 2 * 256;   // queries, dout, lse, delta
+  constexpr int KK = DK / 16, VK = DV / 16, KD = DK / 32, VD = DV / 32;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int pairs = a.n * a.kv_heads, pair = blockIdx.x % pairs;
+  const int r = pair / a.kv_heads, kvh = pair % a.kv_heads;
+  const int k0 = blockIdx.x / pairs * 32 * WAVES, k1 = min(k0 + 32 * WAVES, a.n_pad) - 1;   // the first see the most queries
+  const int mine = k0 + wave * 32 + (lane & 31), row = min(mine, a.n_pad - 1);              // this lane's key
+  const lds_ptr lds = (lds_ptr)smem;
+  const int live_k = a.dk / 8, live_v = a.dv / 8;
+
+  bf16x8 k[KK], v[VK];
+  load_operand(k, at(a.k, r, row, kvh), mine < a.n_pad, live_k, lane);
+  load_operand(v, at(a.v, r, row, kvh), mine < a.n_pad, live_v, lane);
+  const float c = fold_scale<CAP>(k, a.scale, a.cap);
+  const float c2 = CAP ? a.cap * kLog2e : c;
+  int end = 0;   // this lane's key is seen by queries [mine, end)
+  if (mine < a.n_pad) end = min(a.death[static_cast<int64_t>(r) * a.n_pad + mine], a.n_pad);
+  // of all keys of the workgroup: the last query that sees one, and up to which all do
+  int last = 0, first = INT32_MAX;
+  for (int b = k0 / kTrainBlock; b <= k1 / kTrainBlock; ++b) {
+    const KeyBlock x = a.keys[static_cast<int64_t>(r) * a.blocks + b];
+    last = max(last, x.last);
+    first = min(first, x.first);
+  }
+  if (k1 != k0 + 32 * WAVES - 1) first = 0;   // the last keys of a rollout: some lanes have none
+
+  if (live_k < QR::CH || live_v < GR::CH) {
+    for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
+    __syncthreads();
+  }
+  // step i: queries [t0 + i % tiles * BN ...) of head i / tiles
+  const int t0 = k0, tiles = last > t0 ? (last - t0 + BN - 1) / BN : 0, steps = tiles * a.group;
+  auto load = [&](int i, int stage) {
+    const lds_ptr dst = lds + stage * STAGE;
+    const int h = kvh * a.group + i / tiles, q0 = t0 + i % tiles * BN;
+    QR::template load<BN, WAVES>(dst, at(a.q, r, 0, h), a.q.ts, q0, a.n_pad - 1, live_k, wave, lane);
+    GR::template load<BN, WAVES>(dst + BN * QR::BYTES, at(a.dout, r, 0, h), a.dout.ts, q0, a.n_pad - 1, live_v, wave, lane);
+    const int64_t q = min(q0 + lane, a.n_pad - 1);
+    if (wave == 0) load_lds4(dst + BN * (QR::BYTES + GR::BYTES), a.lse + (static_cast<int64_t>(r) * a.n_pad + q) * a.heads + h);
+    if (wave == 1) load_lds4(dst + BN * (QR::BYTES + GR::BYTES) + 256, a.delta + (static_cast<int64_t>(r) * a.heads + h) * a.n_pad + q);
+  };
+  // a tile of queries that sees the keys in part, with a value that is not finite
+  bool rows_only = false;
+  for (int x = lane; x < a.group * ((last - t0 + kTrainBlock - 1) / kTrainBlock); x += 64) {
+    const int nb = (last - t0 + kTrainBlock - 1) / kTrainBlock, b = t0 / kTrainBlock + x % nb;
+    const int64_t o = (static_cast<int64_t>(r) * a.heads + kvh * a.group + x / nb) * a.blocks + b;
+    const bool all = b * kTrainBlock >= k1 && b * kTrainBlock + kTrainBlock - 1 < first;
+    if (!all && (a.odd_q[o] | a.odd_do[o])) rows_only = true;
+  }
+  rows_only = __any(rows_only);
+  if (rows_only) {
+    for (int i = k0 + wave; i <= k1; i += WAVES) train_dkv_row(a, r, i, kvh, lane);
+    return;
+  }
+
+  f32x16 gk[KD], gv[VD];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+#pragma unroll
+    for (int d = 0; d < KD; ++d) gk[d][i] = 0.f;
+#pragma unroll
+    for (int d = 0; d < VD; ++d) gv[d][i] = 0.f;
+  }
+  if (steps > 0) load(0, 0);
+  for (int i = 0; i < steps; ++i) {
+    const int stage = i & 1, q0 = t0 + i % tiles * BN;
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    if (i + 1 < steps) load(i + 1, stage ^ 1);
+    const lds_ptr qs = lds + stage * STAGE, gs = qs + BN * QR::BYTES;
+    const float* const ls = reinterpret_cast<const float*>(smem + stage * STAGE + BN * (QR::BYTES + GR::BYTES));
+    const bool all = q0 >= k1 && q0 + BN - 1 < first;
+#pragma unroll 1
+    for (int b = 0; b < BN / 32; ++b) {
+      f32x16 s, dp;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) s[x] = dp[x] = 0.f;
+#pragma unroll
+      for (int x = 0; x < KK; ++x) s = mfma(QR::straight(qs, b * 32, x, lane), k[x], s);
+#pragma unroll
+      for (int x = 0; x < VK; ++x) dp = mfma(GR::straight(gs, b * 32, x, lane), v[x], dp);
+      if constexpr (CAP) tanh_all(s, c);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const int t = b * 32 + product_row(x, lane);
+        const float lse = ls[t], ref = lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;
+        const float slope = CAP ? 1.f - s[x] * s[x] : 1.f;
+        float p = exp2_(__builtin_fmaf(s[x], c2, -ref));
+        float ds = p * (dp[x] - ls[64 + t]) * (a.scale * slope);
+        if (!all && (q0 + t < mine || q0 + t >= end)) p = ds = 0.f;
+        s[x] = p;
+        dp[x] = ds;
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const bf16x8 p = operand(s, y), ds = operand(dp, y);
+#pragma unroll
+        for (int d = 0; d < VD; ++d) gv[d] = mfma(GR::columns(gs, b * 32 + y * 16, d, lane), p, gv[d]);
+#pragma unroll
+        for (int d = 0; d < KD; ++d) gk[d] = mfma(QR::columns(qs, b * 32 + y * 16, d, lane), ds, gk[d]);
+      }
+    }
+  }
+  if (mine >= a.n_pad) return;
+  auto store = [&](uint16_t* to, const f32x16& x, int d, int width) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int col = d * 32 + product_row(i, lane);
+      const f32x4 y{x[i], x[i + 1], x[i + 2], x[i + 3]};
+      if (col < width) *reinterpret_cast<bf16x4*>(to + col) = __builtin_convertvector(y, bf16x4);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < KD; ++d) store(place(a.dk_, r, mine, kvh), gk[d], d, a.dk);
+#pragma unroll
+  for (int d = 0; d < VD; ++d) store(place(a.dv_, r, mine, kvh), gv[d], d, a.dv);
+}
+
+template <int DK, int DV, int BN, int WAVES, bool CAP>
+hipError_t launch_shape(const TrainLaunch& a, hipStream_t s) {
+  constexpr int q_lds = 2 * (BN * (DK + DV) * 2 + kTrainBlock * 4), k_lds = 2 * (BN * (DK + DV) * 2 + 512);
+  hipError_t e = allow_lds<train_dq_kernel<DK, DV, BN, WAVES, CAP>>(q_lds);
+  if (e == hipSuccess) e = allow_lds<train_dkv_kernel<DK, DV, BN, WAVES, CAP>>(k_lds);
+  if (e != hipSuccess) return e;
+  const int64_t tiles = (a.n_pad + 32 * WAVES - 1) / (32 * WAVES);
+  train_dkv_kernel<DK, DV, BN, WAVES, CAP><<<dim3(static_cast<unsigned>(a.n * a.kv_heads * tiles)), dim3(64 * WAVES), k_lds, s>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  train_dq_kernel<DK, DV, BN, WAVES, CAP><<<dim3(static_cast<unsigned>(a.n * a.heads * tiles)), dim3(64 * WAVES), q_lds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int DK, int DV, int BN, int WAVES>
+hipError_t launch_cap(const TrainLaunch& a, hipStream_t s) {
+  return a.cap == 0.f ? launch_shape<DK, DV, BN, WAVES, false>(a, s) : launch_shape<DK, DV, BN, WAVES, true>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_train_back(const TrainLaunch& a, hipStream_t s) {
-  const int64_t rows = int64_t{a.n} * a.n_pad;
-  auto grid = [&](int64_t waves) { return dim3(static_cast<unsigned>((waves + 3) / 4)); };
-  train_delta_kernel<<<grid(rows * a.heads), dim3(256), 0, s>>>(a);
-  train_dq_rows_kernel<<<grid(rows * a.heads), dim3(256), 0, s>>>(a);
-  train_dkv_rows_kernel<<<grid(rows * a.kv_heads), dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+  hipError_t e = launch_train_scan(a, true, s);
+  if (e != hipSuccess) return e;
+  if (a.dk <= 64 && a.dv <= 64) return launch_cap<64, 64, 64, 4>(a, s);
+  if (a.dk <= 128 && a.dv <= 128) return launch_cap<128, 128, 64, 4>(a, s);
+  if (a.dk <= 192 && a.dv <= 128) return launch_cap<192, 128, 32, 4>(a, s);
+  return launch_cap<256, 256, 32, 4>(a, s);
 }
 
 }  // namespace ll
