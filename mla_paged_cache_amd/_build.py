@@ -46,16 +46,22 @@ FLAGS = [
     "-fPIC",
     "-ffp-contract=off",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # matrix accumulators in ordinary registers: the attention scales and
-    # stores them, and moving each to and from the accumulation file costs more
-    # than the products (the compiler's own choice otherwise)
-    "-mllvm", "-amdgpu-mfma-vgpr-form=1",
     "-Wall",
     "-Winfinite-recursion",
     # host code: the hardware popcount (the free-page bitmap is merged and
     # counted word by word; without it every popcount is a dozen ALU ops)
     "-Xarch_host", "-mpopcnt",
 ]
+
+# Matrix accumulators in ordinary registers: the attention scales and stores them, and
+# moving each to and from the accumulation file costs more than the products (the
+# compiler's own choice otherwise).  Not where the sums alone fill that file.
+VGPR_SUMS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+OWN_SUMS = ("kernels_train_back.hip",)
+
+
+def flags(source: str) -> list:
+    return FLAGS + ([] if os.path.basename(source) in OWN_SUMS else VGPR_SUMS)
 
 
 def hipcc() -> str:
@@ -80,7 +86,7 @@ def build(verbose: bool = False) -> str:
     tmp = LIB_PATH + ".tmp"
     with tempfile.TemporaryDirectory() as d:
         objects = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
-        compiles = [[hipcc(), *FLAGS, "-I", INCLUDE, "-c", s, "-o", o] for s, o in zip(SOURCES, objects)]
+        compiles = [[hipcc(), *flags(s), "-I", INCLUDE, "-c", s, "-o", o] for s, o in zip(SOURCES, objects)]
         link = [hipcc(), "--offload-arch=gfx950", "-shared", "-Wl,--no-undefined", *objects, "-o", tmp]
         if verbose:
             print(" ".join(compiles[0]), flush=True)

@@ -36,14 +36,118 @@ __device__ void train_row(const TrainLaunch& a, int r, int q, int h, int lane) {
     a.lse[(static_cast<int64_t>(r) * a.n_pad + q) * a.heads + h] = l == 0.f ? -__builtin_inff() : (m + __log2f(l)) * kLn2;
 }
 
-// What the workspace says of blocks of 64 tokens (and for the backward pass delta), a
-// wave per block and unit.  Units: 0 the keys' death times; then the KV heads' values;
-// backward also their keys, then every head's dout (with delta) and its queries.
+constexpr int kScanThreads = 1024;
+constexpr int kScanWaves = kScanThreads / 64;
+
+// Keys chosen in order: each wave looks at 512 consecutive ones, `pick` says which go to
+// which place.
+struct Picked {
+  int count = 0;   // so far, the same in every thread
+};
+template <typename Is, typename Put>
+__device__ __forceinline__ void pick_in_order(int n, uint32_t (*totals)[kScanWaves], Picked& p, Is&& is, Put&& put) {
+  constexpr int E = 8;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  int at = 0;
+  for (int base = 0; base < n; base += kScanThreads * E, at ^= 1) {
+    uint64_t mine[E];
+    int death[E], sum = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int k = base + (wave * E + e) * 64 + lane;
+      mine[e] = __ballot(k < n && is(k, &death[e]));
+      sum += __popcll(mine[e]);
+    }
+    if (lane == 0) totals[at][wave] = sum;
+    __syncthreads();
+    int o = p.count;
+#pragma unroll
+    for (int x = 0; x < kScanWaves; ++x) {
+      if (x < wave) o += totals[at][x];
+      p.count += totals[at][x];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int k = base + (wave * E + e) * 64 + lane;
+      if (mine[e] >> lane & 1) put(o + __popcll(mine[e] & ((uint64_t{1} << lane) - 1)), k, death[e]);
+      o += __popcll(mine[e]);
+    }
+  }
+  __syncthreads();   // the totals may be used again
+}
+
+// Epoch e's list of keys and what its blocks hold; for the backward pass the keys that
+// die in the epoch in their places of the order (e = epochs: those that nobody sees).  A
+// workgroup each, which goes through all death times of the rollout (a few microseconds).
 template <bool BACKWARD>
-__global__ __launch_bounds__(256) void train_scan_kernel(TrainLaunch a) {
+__device__ void list_keys(const TrainLaunch& a, int r, int e, uint32_t (*totals)[kScanWaves]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t* const death = a.death + static_cast<int64_t>(r) * a.n_pad;
+  const int64_t from64 = static_cast<int64_t>(e) * a.epoch, end64 = from64 + a.epoch;
+  const int from = static_cast<int>(min(from64, static_cast<int64_t>(a.n_pad))), end = static_cast<int>(min(end64, static_cast<int64_t>(a.n_pad)));
+  if (e > 0 && e < a.epochs) {
+    const int64_t at = static_cast<int64_t>(r) * a.list_keys() + a.list_at(e);
+    KeyEntry* const list = a.list + at;
+    Picked p;
+    pick_in_order(from, totals, p,
+                  [&](int k, int* d) {
+                    *d = min(death[k], a.n_pad);
+                    return *d > from;
+                  },
+                  [&](int i, int k, int d) { list[i] = KeyEntry{k, d}; });
+    const int blocks = (p.count + kTrainBlock - 1) / kTrainBlock;
+    for (int i = p.count + threadIdx.x; i < blocks * kTrainBlock; i += kScanThreads) list[i] = KeyEntry{0, -1};
+    if (threadIdx.x == 0) a.list_count[static_cast<int64_t>(r) * a.epochs + e] = p.count;
+    __syncthreads();   // the list is written
+    for (int b = wave; b < blocks; b += kScanWaves) {
+      int first = list[b * kTrainBlock + lane].death, last = first;
+      for (int x = 32; x >= 1; x >>= 1) {
+        first = min(first, __shfl_xor(first, x));
+        last = max(last, __shfl_xor(last, x));
+      }
+      if (lane == 0) a.list_blocks[at / kTrainBlock + b] = KeyBlock{first, last};
+    }
+  }
+  if constexpr (BACKWARD) {
+    int32_t* const order = a.order + static_cast<int64_t>(r) * a.n_pad;
+    // those before: they die after this epoch (for the last place: all that are seen)
+    const int after = e == a.epochs ? 0 : end;
+    int before = 0;
+    for (int k = threadIdx.x; k < a.n_pad; k += kScanThreads) {
+      const int d = min(death[k], a.n_pad);
+      before += d > k && d > after;
+    }
+    for (int x = 32; x >= 1; x >>= 1) before += __shfl_xor(before, x);
+    if (lane == 0) totals[0][wave] = before;
+    __syncthreads();
+    Picked p;
+    for (int x = 0; x < kScanWaves; ++x) p.count += totals[0][x];
+    __syncthreads();
+    if (e == a.epochs && threadIdx.x == 0) a.seen_keys[r] = p.count;
+    pick_in_order(e == a.epochs ? a.n_pad : end, totals, p,
+                  [&](int k, int*) {
+                    const int d = min(death[k], a.n_pad);
+                    return e == a.epochs ? d <= k : d > k && d > from && d <= end;
+                  },
+                  [&](int i, int k, int) { order[i] = k; });
+  }
+}
+
+// What the workspace says of keys and of blocks of 64 tokens, and for the backward pass
+// delta.  Workgroups: first the epochs' lists; then a wave per block and unit: 0 the
+// keys' death times; the KV heads' values; backward also their keys, every head's dout
+// (with delta) and its queries.
+template <bool BACKWARD>
+__global__ __launch_bounds__(kScanThreads) void train_scan_kernel(TrainLaunch a) {
+  __shared__ uint32_t totals[2][kScanWaves];
   const int lane = threadIdx.x & 63;
+  const int lists = a.n * (a.epochs + BACKWARD);
+  if (static_cast<int>(blockIdx.x) < lists) {
+    list_keys<BACKWARD>(a, blockIdx.x % a.n, a.epochs + BACKWARD - 1 - blockIdx.x / a.n, totals);
+    return;
+  }
   const int units = 1 + (BACKWARD ? 2 * a.kv_heads + 2 * a.heads : a.kv_heads);
-  int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  int64_t id = static_cast<int64_t>(blockIdx.x - lists) * kScanWaves + (threadIdx.x >> 6);
   const int b = static_cast<int>(id % a.blocks);
   id /= a.blocks;
   const int r = static_cast<int>(id / units);
@@ -68,16 +172,16 @@ __global__ __launch_bounds__(256) void train_scan_kernel(TrainLaunch a) {
   Heads x, y{};
   uint32_t* odd;
   int width = a.dv, h;
-  bool sum = false;
+  bool sum = false, keys = true;
   if (unit < a.kv_heads) {
     x = a.v, h = unit, odd = a.odd_v + kv_at + static_cast<int64_t>(h) * a.blocks;
   } else if ((unit -= a.kv_heads) < a.kv_heads) {
     x = a.k, h = unit, odd = a.odd_k + kv_at + static_cast<int64_t>(h) * a.blocks, width = a.dk;
   } else if ((unit -= a.kv_heads) < a.heads) {
-    x = a.dout, y = a.out, h = unit, odd = a.odd_do + at_ + static_cast<int64_t>(h) * a.blocks, sum = true;
+    x = a.dout, y = a.out, h = unit, odd = a.odd_do + at_ + static_cast<int64_t>(h) * a.blocks, sum = true, keys = false;
   } else {
     unit -= a.heads;
-    x = a.q, h = unit, odd = a.odd_q + at_ + static_cast<int64_t>(h) * a.blocks, width = a.dk;
+    x = a.q, h = unit, odd = a.odd_q + at_ + static_cast<int64_t>(h) * a.blocks, width = a.dk, keys = false;
   }
   // 8, 16 or 32 lanes a row
   const int shift = width <= 64 ? 3 : width <= 128 ? 4 : 5, c = (lane & ((1 << shift) - 1)) * 8;
@@ -86,6 +190,7 @@ __global__ __launch_bounds__(256) void train_scan_kernel(TrainLaunch a) {
     const bool live = t < rows && c < width;
     chunk_t v{0u, 0u, 0u, 0u};
     if (live) v = *reinterpret_cast<const chunk_t*>(at(x, r, t0 + t, h) + c);
+    if (keys && live && a.death[static_cast<int64_t>(r) * a.n_pad + t0 + t] <= t0 + t) v = chunk_t{0u, 0u, 0u, 0u};   // nobody sees it
     bits |= exponents(v);
     if (BACKWARD && sum) {
       float d = dot8(load8(at(x, r, min(t0 + t, a.n_pad - 1), h) + c, live), load8(at(y, r, min(t0 + t, a.n_pad - 1), h) + c, live));
@@ -124,7 +229,6 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
   const int live_k = a.dk / 8, live_v = a.dv / 8;
   const uint16_t* const kp = at(a.k, r, 0, kvh);
   const uint16_t* const vp = at(a.v, r, 0, kvh);
-  const int32_t* const death = a.death + static_cast<int64_t>(r) * a.n_pad;
 
   bf16x8 q[KK];
   load_operand(q, at(a.q, r, min(mine, a.n_pad - 1), h), mine < a.n_pad, live_k, lane);
@@ -135,12 +239,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
     __syncthreads();
   }
-  auto load = [&](int block, int part, int stage) {
+  auto load = [&](KeyEntry key, int part, int stage) {
     const lds_ptr dst = lds + stage * STAGE;
-    const int k0 = block * kTrainBlock + part * BN;
-    KR::template load<BN, WAVES>(dst, kp, a.k.ts, k0, a.n_pad - 1, live_k, wave, lane);
-    VR::template load<BN, WAVES>(dst + BN * KR::BYTES, vp, a.v.ts, k0, a.n_pad - 1, live_v, wave, lane);
-    if (wave == 0) load_lds4(dst + BN * (KR::BYTES + VR::BYTES), death + min(k0 + lane, a.n_pad - 1));
+    const int row = KeyWalk::row_of(key, lane);
+    KR::template load<BN, WAVES>(dst, kp, a.k.ts, row, part * BN, live_k, wave, lane);
+    VR::template load<BN, WAVES>(dst + BN * KR::BYTES, vp, a.v.ts, row, part * BN, live_v, wave, lane);
+    if (wave == 0) reinterpret_cast<int*>(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES))[lane] = key.death;   // the whole block's
   };
 
   f32x16 o[DB];
@@ -150,23 +254,32 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   float m = -__builtin_inff(), l = 0.f;
 
-  KeyWalk walk{a.keys + static_cast<int64_t>(r) * a.blocks, a.odd_v + (static_cast<int64_t>(r) * a.kv_heads + kvh) * a.blocks,
-               q0, q1, q1 / kTrainBlock + 1};
-  bool all = false, next_all = false;
-  int block = walk.first(&all, lane), part = 0, stage = 0;
-  if (block >= 0) load(block, 0, 0);
+  // tiles of a block's keys: this one, the next one (on its way), and the block after
+  // that, whose keys are known a tile before they are asked for
+  KeyWalk walk(a, r, kvh, a.odd_v, q0, q1, lane);
+  bool all = false, next_all = false, then_all = false;
+  int block = walk.next(&all, lane), next = -1, part = 0, stage = 0;
+  KeyEntry key{}, next_key{};
+  if (block >= 0) {
+    key = walk.key(block, lane);
+    load(key, 0, 0);
+    next = walk.next(&next_all, lane);
+    if (next >= 0) next_key = walk.key(next, lane);
+  }
   while (block >= 0 && !walk.rows_only) {
-    int next = block, next_part = part + 1;
-    next_all = all;
-    if (PARTS == 1 || next_part == PARTS) {
-      next = walk.next(&next_all, lane);
-      next_part = 0;
-    }
+    const bool ends = part == PARTS - 1;   // the block's last tile
+    const int then = ends && next >= 0 ? walk.next(&then_all, lane) : -1;
     __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's part of the tile
     __syncthreads();                      // everyone's; and nobody reads the other stage any more
-    if (next >= 0) load(next, next_part, stage ^ 1);
+    KeyEntry then_key{};
+    if (!ends) {
+      load(key, part + 1, stage ^ 1);
+    } else if (next >= 0) {
+      load(next_key, 0, stage ^ 1);
+      if (then >= 0) then_key = walk.key(then, lane);
+    }
     const lds_ptr ks = lds + stage * STAGE, vs = ks + BN * KR::BYTES;
-    const int k0 = block * kTrainBlock + part * BN;
+    const int k0 = walk.first_key(block);
 
     f32x16 s[KB];
 #pragma unroll
@@ -187,7 +300,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
         const int* const d = reinterpret_cast<const int*>(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES));
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int k = b * 32 + product_row(i, lane);
+          const int k = part * BN + b * 32 + product_row(i, lane);
           if (k0 + k > mine || mine >= d[k]) s[b][i] = -__builtin_inff();
         }
       }
@@ -221,7 +334,13 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
         for (int d = 0; d < DB; ++d) o[d] = mfma(VR::columns(vs, b * 32 + x * 16, d, lane), p, o[d]);
       }
     }
-    block = next, part = next_part, all = next_all, stage ^= 1;
+    stage ^= 1;
+    if (!ends) {
+      ++part;
+    } else {
+      block = next, all = next_all, key = next_key, part = 0;
+      next = then, next_all = then_all, next_key = then_key;
+    }
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);   // loads on their way into LDS
   if (walk.rows_only) {
@@ -265,9 +384,10 @@ hipError_t launch_cap(const TrainLaunch& a, hipStream_t s) {
 
 hipError_t launch_train_scan(const TrainLaunch& a, bool backward, hipStream_t s) {
   const int64_t units = 1 + (backward ? 2 * a.kv_heads + 2 * a.heads : a.kv_heads);
-  const dim3 g(static_cast<unsigned>((a.n * units * a.blocks + 3) / 4));
-  if (backward) train_scan_kernel<true><<<g, dim3(256), 0, s>>>(a);
-  else train_scan_kernel<false><<<g, dim3(256), 0, s>>>(a);
+  const int64_t lists = int64_t{a.n} * (a.epochs + (backward ? 1 : 0));
+  const dim3 g(static_cast<unsigned>(lists + (a.n * units * a.blocks + kScanWaves - 1) / kScanWaves));
+  if (backward) train_scan_kernel<true><<<g, dim3(kScanThreads), 0, s>>>(a);
+  else train_scan_kernel<false><<<g, dim3(kScanThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -85,7 +85,6 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
   const int live_k = a.dk / 8, live_v = a.dv / 8;
   const uint16_t* const kp = at(a.k, r, 0, kvh);
   const uint16_t* const vp = at(a.v, r, 0, kvh);
-  const int32_t* const death = a.death + static_cast<int64_t>(r) * a.n_pad;
 
   bf16x8 q[KK], g[VK];
   load_operand(q, at(a.q, r, row, h), mine < a.n_pad, live_k, lane);
@@ -100,12 +99,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
     __syncthreads();
   }
-  auto load = [&](int block, int part, int stage) {
+  auto load = [&](KeyEntry key, int part, int stage) {
     const lds_ptr dst = lds + stage * STAGE;
-    const int k0 = block * kTrainBlock + part * BN;
-    KR::template load<BN, WAVES>(dst, kp, a.k.ts, k0, a.n_pad - 1, live_k, wave, lane);
-    VR::template load<BN, WAVES>(dst + BN * KR::BYTES, vp, a.v.ts, k0, a.n_pad - 1, live_v, wave, lane);
-    if (wave == 0) load_lds4(dst + BN * (KR::BYTES + VR::BYTES), death + min(k0 + lane, a.n_pad - 1));
+    const int row = KeyWalk::row_of(key, lane);
+    KR::template load<BN, WAVES>(dst, kp, a.k.ts, row, part * BN, live_k, wave, lane);
+    VR::template load<BN, WAVES>(dst + BN * KR::BYTES, vp, a.v.ts, row, part * BN, live_v, wave, lane);
+    if (wave == 0) reinterpret_cast<int*>(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES))[lane] = key.death;   // the whole block's
   };
   f32x16 o[DB];
 #pragma unroll
@@ -113,23 +112,32 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
 
-  KeyWalk walk{a.keys + static_cast<int64_t>(r) * a.blocks, a.odd_k + (static_cast<int64_t>(r) * a.kv_heads + kvh) * a.blocks,
-               q0, q1, q1 / kTrainBlock + 1};
-  bool all = false, next_all = false;
-  int block = walk.first(&all, lane), part = 0, stage = 0;
-  if (block >= 0) load(block, 0, 0);
+  // tiles of a block's keys: this one, the next one (on its way), and the block after
+  // that, whose keys are known a tile before they are asked for
+  KeyWalk walk(a, r, kvh, a.odd_k, q0, q1, lane);
+  bool all = false, next_all = false, then_all = false;
+  int block = walk.next(&all, lane), next = -1, part = 0, stage = 0;
+  KeyEntry key{}, next_key{};
+  if (block >= 0) {
+    key = walk.key(block, lane);
+    load(key, 0, 0);
+    next = walk.next(&next_all, lane);
+    if (next >= 0) next_key = walk.key(next, lane);
+  }
   while (block >= 0 && !walk.rows_only) {
-    int next = block, next_part = part + 1;
-    next_all = all;
-    if (PARTS == 1 || next_part == PARTS) {
-      next = walk.next(&next_all, lane);
-      next_part = 0;
-    }
+    const bool ends = part == PARTS - 1;   // the block's last tile
+    const int then = ends && next >= 0 ? walk.next(&then_all, lane) : -1;
     __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's part of the tile
     __syncthreads();                      // everyone's; and nobody reads the other stage any more
-    if (next >= 0) load(next, next_part, stage ^ 1);
+    KeyEntry then_key{};
+    if (!ends) {
+      load(key, part + 1, stage ^ 1);
+    } else if (next >= 0) {
+      load(next_key, 0, stage ^ 1);
+      if (then >= 0) then_key = walk.key(then, lane);
+    }
     const lds_ptr ks = lds + stage * STAGE, vs = ks + BN * KR::BYTES;
-    const int k0 = block * kTrainBlock + part * BN;
+    const int k0 = walk.first_key(block);
     const int* const dt = reinterpret_cast<const int*>(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES));
 #pragma unroll 1
     for (int b = 0; b < KB; ++b) {
@@ -147,7 +155,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
         float p = exp2_(__builtin_fmaf(s[i], c2, -ref));
         p *= (dp[i] - delta) * (a.scale * slope);
         if (!all) {
-          const int k = b * 32 + product_row(i, lane);
+          const int k = part * BN + b * 32 + product_row(i, lane);
           if (k0 + k > mine || mine >= dt[k]) p = 0.f;
         }
         s[i] = p;
@@ -159,7 +167,13 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
         for (int d = 0; d < DB; ++d) o[d] = mfma(KR::columns(ks, b * 32 + x * 16, d, lane), ds, o[d]);
       }
     }
-    block = next, part = next_part, all = next_all, stage ^= 1;
+    stage ^= 1;
+    if (!ends) {
+      ++part;
+    } else {
+      block = next, all = next_all, key = next_key, part = 0;
+      next = then, next_all = then_all, next_key = then_key;
+    }
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);   // loads on their way into LDS
   if (walk.rows_only) {
@@ -184,7 +198,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
 // them, BN at a time through LDS: S = Q K^T and dP = dO V^T with a lane per key, then
 // dV^T += dO^T P and dK^T += Q^T dS, dO^T and Q^T from the transposing LDS reads.
 template <int DK, int DV, int BN, int WAVES, bool CAP>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 128 ? 1 : 2))) void train_dkv_kernel(TrainLaunch a) {
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 64 ? 1 : 2))) void train_dkv_kernel(TrainLaunch a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   using QR = Rows<DK>;
   using GR = Rows<DV>;
@@ -193,41 +207,53 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pairs = a.n * a.kv_heads, pair = blockIdx.x % pairs;
   const int r = pair / a.kv_heads, kvh = pair % a.kv_heads;
-  const int k0 = blockIdx.x / pairs * 32 * WAVES, k1 = min(k0 + 32 * WAVES, a.n_pad) - 1;   // the first see the most queries
-  const int mine = k0 + wave * 32 + (lane & 31), row = min(mine, a.n_pad - 1);              // this lane's key
+  // places [p0, p0 + 32 * WAVES) of the keys' order: the first see the most queries
+  const int p0 = blockIdx.x / pairs * 32 * WAVES, place_ = p0 + wave * 32 + (lane & 31);
+  const int32_t* const order = a.order + static_cast<int64_t>(r) * a.n_pad;
+  const int32_t* const death = a.death + static_cast<int64_t>(r) * a.n_pad;
+  const int mine = order[min(place_, a.n_pad - 1)];              // this lane's key
+  const bool there = place_ < min(a.n_pad, a.seen_keys[r]);      // which somebody sees
   const lds_ptr lds = (lds_ptr)smem;
   const int live_k = a.dk / 8, live_v = a.dv / 8;
 
   bf16x8 k[KK], v[VK];
-  load_operand(k, at(a.k, r, row, kvh), mine < a.n_pad, live_k, lane);
-  load_operand(v, at(a.v, r, row, kvh), mine < a.n_pad, live_v, lane);
+  load_operand(k, at(a.k, r, mine, kvh), there, live_k, lane);
+  load_operand(v, at(a.v, r, mine, kvh), there, live_v, lane);
   const float c = fold_scale<CAP>(k, a.scale, a.cap);
   const float c2 = CAP ? a.cap * kLog2e : c;
-  int end = 0;   // this lane's key is seen by queries [mine, end)
-  if (mine < a.n_pad) end = min(a.death[static_cast<int64_t>(r) * a.n_pad + mine], a.n_pad);
-  // of all keys of the workgroup: the last query that sees one, and up to which all do
-  int last = 0, first = INT32_MAX;
-  for (int b = k0 / kTrainBlock; b <= k1 / kTrainBlock; ++b) {
-    const KeyBlock x = a.keys[static_cast<int64_t>(r) * a.blocks + b];
-    last = max(last, x.last);
-    first = min(first, x.first);
+  const int end = there ? min(death[mine], a.n_pad) : 0;   // this lane's key is seen by queries [mine, end)
+  // of all keys of the workgroup: the last query that sees one, up to which all do, and
+  // the first and last key
+  int last = 0, first = INT32_MAX, k0 = INT32_MAX, k1 = 0;
+#pragma unroll
+  for (int i = 0; i < WAVES / 2; ++i) {
+    const int p = p0 + i * 64 + lane;
+    const bool some = p < min(a.n_pad, a.seen_keys[r]);
+    const int key = order[min(p, a.n_pad - 1)], d = some ? min(death[key], a.n_pad) : 0;
+    last = max(last, d);
+    first = min(first, d);
+    if (some) k0 = min(k0, key), k1 = max(k1, key);
   }
-  if (k1 != k0 + 32 * WAVES - 1) first = 0;   // the last keys of a rollout: some lanes have none
+  for (int x = 32; x >= 1; x >>= 1) {
+    last = max(last, __shfl_xor(last, x));
+    first = min(first, __shfl_xor(first, x));
+    k0 = min(k0, __shfl_xor(k0, x));
+    k1 = max(k1, __shfl_xor(k1, x));
+  }
 
   if (live_k < QR::CH || live_v < GR::CH) {
     for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
     __syncthreads();
   }
   // step i: queries [t0 + i % tiles * BN ...) of head i / tiles
-  const int t0 = k0, tiles = last > t0 ? (last - t0 + BN - 1) / BN : 0, steps = tiles * a.group;
+  const int t0 = k0 - k0 % kTrainBlock, tiles = last > t0 ? (last - t0 + BN - 1) / BN : 0, steps = tiles * a.group;
   auto load = [&](int i, int stage) {
     const lds_ptr dst = lds + stage * STAGE;
-    const int h = kvh * a.group + i / tiles, q0 = t0 + i % tiles * BN;
-    QR::template load<BN, WAVES>(dst, at(a.q, r, 0, h), a.q.ts, q0, a.n_pad - 1, live_k, wave, lane);
-    GR::template load<BN, WAVES>(dst + BN * QR::BYTES, at(a.dout, r, 0, h), a.dout.ts, q0, a.n_pad - 1, live_v, wave, lane);
-    const int64_t q = min(q0 + lane, a.n_pad - 1);
-    if (wave == 0) load_lds4(dst + BN * (QR::BYTES + GR::BYTES), a.lse + (static_cast<int64_t>(r) * a.n_pad + q) * a.heads + h);
-    if (wave == 1) load_lds4(dst + BN * (QR::BYTES + GR::BYTES) + 256, a.delta + (static_cast<int64_t>(r) * a.heads + h) * a.n_pad + q);
+    const int h = kvh * a.group + i / tiles, q0 = t0 + i % tiles * BN, row = min(q0 + lane, a.n_pad - 1);
+    QR::template load<BN, WAVES>(dst, at(a.q, r, 0, h), a.q.ts, row, 0, live_k, wave, lane);
+    GR::template load<BN, WAVES>(dst + BN * QR::BYTES, at(a.dout, r, 0, h), a.dout.ts, row, 0, live_v, wave, lane);
+    if (wave == 0) load_lds4(dst + BN * (QR::BYTES + GR::BYTES), a.lse + (static_cast<int64_t>(r) * a.n_pad + row) * a.heads + h);
+    if (wave == 1) load_lds4(dst + BN * (QR::BYTES + GR::BYTES) + 256, a.delta + (static_cast<int64_t>(r) * a.heads + h) * a.n_pad + row);
   };
   // a tile of queries that sees the keys in part, with a value that is not finite
   bool rows_only = false;
@@ -239,7 +265,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
   }
   rows_only = __any(rows_only);
   if (rows_only) {
-    for (int i = k0 + wave; i <= k1; i += WAVES) train_dkv_row(a, r, i, kvh, lane);
+    for (int i = p0 + wave; i < min(p0 + 32 * WAVES, a.n_pad); i += WAVES) train_dkv_row(a, r, order[i], kvh, lane);
     return;
   }
 
@@ -291,7 +317,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
       }
     }
   }
-  if (mine >= a.n_pad) return;
+  if (place_ >= a.n_pad) return;
   auto store = [&](uint16_t* to, const f32x16& x, int d, int width) {
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {

@@ -70,8 +70,14 @@ int64_t lay_out(TrainLaunch* a, bool backward, char* at) {
   };
   const int64_t nb = int64_t{a->n} * a->blocks;
   a->keys = reinterpret_cast<KeyBlock*>(take(nb * static_cast<int64_t>(sizeof(KeyBlock))));
+  const int64_t listed = int64_t{a->n} * a->list_keys();
+  a->list = reinterpret_cast<KeyEntry*>(take(listed * static_cast<int64_t>(sizeof(KeyEntry))));
+  a->list_blocks = reinterpret_cast<KeyBlock*>(take(listed / kTrainBlock * static_cast<int64_t>(sizeof(KeyBlock))));
+  a->list_count = reinterpret_cast<int32_t*>(take(int64_t{a->n} * a->epochs * 4));
   a->odd_v = reinterpret_cast<uint32_t*>(take(nb * a->kv_heads * 4));
   if (backward) {
+    a->order = reinterpret_cast<int32_t*>(take(int64_t{a->n} * a->n_pad * 4));
+    a->seen_keys = reinterpret_cast<int32_t*>(take(int64_t{a->n} * 4));
     a->odd_k = reinterpret_cast<uint32_t*>(take(nb * a->kv_heads * 4));
     a->odd_q = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
     a->odd_do = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
@@ -88,6 +94,8 @@ TrainLaunch sizes(const kvs_attend_desc* d) {
   a.group = d->heads / d->kv_heads;
   a.n_pad = static_cast<int32_t>(d->n_pad);
   a.blocks = static_cast<int32_t>(ceil_div(d->n_pad, kTrainBlock));
+  a.epoch = static_cast<int32_t>(ceil_div(ceil_div(d->n_pad, kTrainEpochs), kTrainTile) * kTrainTile);
+  a.epochs = static_cast<int32_t>(ceil_div(d->n_pad, a.epoch));
   a.dk = d->key_dim;
   a.dv = d->value_dim;
   return a;

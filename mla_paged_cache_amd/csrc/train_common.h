@@ -76,10 +76,11 @@ struct Rows {
     if constexpr (CH % 16 == 0) return c ^ ((r & 3) << 2 | (r >> 2 & 3));
     else return c ^ ((r >> 1 & 1) << 2 | (r >> 2 & 3));
   }
-  // Rows [row0, row0 + N) of a head (x: its row 0, ts: values from row to row) into
-  // LDS, by WAVES waves; rows past `last` repeat it, chunks past `live` are left alone.
+  // N rows of a head (x: its row 0, ts: values from row to row) into LDS, by WAVES
+  // waves; lane r's `row` is the tile's row r (of the part from lane `from` on).  Chunks
+  // past `live` are left alone.
   template <int N, int WAVES>
-  static __device__ __forceinline__ void load(lds_ptr dst, const uint16_t* x, int64_t ts, int row0, int last, int live,
+  static __device__ __forceinline__ void load(lds_ptr dst, const uint16_t* x, int64_t ts, int row, int from, int live,
                                               int wave, int lane) {
     constexpr int LOADS = N * CH / 64;
     static_assert(LOADS % WAVES == 0, "as many for every wave");
@@ -87,7 +88,8 @@ struct Rows {
     for (int i = 0; i < LOADS / WAVES; ++i) {
       const int b = i * WAVES + wave;
       const int r = (b * 64 + lane) / CH, c = place(r, (b * 64 + lane) % CH);
-      if (c < live) load_lds<false>(dst + b * 1024, x + min(row0 + r, last) * ts + c * 8);
+      const int64_t at = __shfl(row, from + r);   // (every lane takes part)
+      if (c < live) load_lds<false>(dst + b * 1024, x + at * ts + c * 8);
     }
   }
   // Row r0 + (lane & 31), values 16 k + 8 (lane >> 5) on: an operand of S = X Y^T.
@@ -171,23 +173,49 @@ __device__ __forceinline__ void tanh_all(f32x16& s, float c) {
   }
 }
 
-// The blocks of keys that queries [q0, q1] see, 64 blocks looked at together: lane x
-// looks at block base + x.  Every wave of a workgroup goes through the same ones.
+// The blocks of keys that queries [q0, q1] of one epoch see: first those of the epoch's
+// list, then the epoch's own.  64 blocks are looked at together, lane x at block base + x;
+// every wave of a workgroup goes through the same ones.
 struct KeyWalk {
-  const KeyBlock* keys;          // of the rollout
-  const uint32_t* odd;           // of the rollout and KV head: blocks with values that are not finite
-  int q0, q1, blocks;            // blocks: those that begin at q1 or before
-  int base = 0;
-  uint64_t seen = 0, whole = 0;
-  bool rows_only = false;        // a block that is seen in part holds such a value
+  const KeyBlock* keys;          // the epoch's own blocks
+  const uint32_t* odd;           // which of them hold a value that is not finite
+  const KeyBlock* list_blocks;
+  const KeyEntry* list;
+  const int32_t* death;          // from the epoch's first key on
+  int q0, q1, k0;                // k0: the epoch's first key
+  int n_pad;
+  int listed, blocks;            // blocks of the list, and of the walk
+  bool odd_list;                 // some key before k0 holds such a value
+  int base;
+  uint64_t seen, whole;
+  bool rows_only;                // a block that is seen in part holds such a value
 
+  __device__ __forceinline__ KeyWalk(const TrainLaunch& a, int r, int kvh, const uint32_t* odd_blocks, int q0_, int q1_, int lane)
+      : q0(q0_), q1(q1_), n_pad(a.n_pad), odd_list(false), base(-64), seen(0), whole(0), rows_only(false) {
+    const int e = q0 / a.epoch;
+    k0 = e * a.epoch;
+    const int64_t own = static_cast<int64_t>(r) * a.blocks, first = k0 / kTrainBlock;
+    keys = a.keys + own + first;
+    odd = odd_blocks + (static_cast<int64_t>(r) * a.kv_heads + kvh) * a.blocks;
+    for (int b = lane; b < first; b += 64) odd_list |= odd[b] != 0;
+    odd_list = __any(odd_list);
+    odd += first;
+    death = a.death + static_cast<int64_t>(r) * a.n_pad + k0;
+    const int64_t at = static_cast<int64_t>(r) * a.list_keys() + a.list_at(e);
+    list = a.list + at;
+    list_blocks = a.list_blocks + at / kTrainBlock;
+    listed = e == 0 ? 0 : (a.list_count[static_cast<int64_t>(r) * a.epochs + e] + kTrainBlock - 1) / kTrainBlock;
+    blocks = listed + (q1 - k0) / kTrainBlock + 1;
+  }
   __device__ __forceinline__ void look(int lane) {
-    const int b = base + lane;
+    const int b = base + lane, own = b - listed;
     KeyBlock x{0, -1};
-    if (b < blocks) x = keys[b];
-    const bool some = x.last > q0, all = some && b * kTrainBlock + kTrainBlock - 1 <= q0 && x.first > q1;
+    if (b < listed) x = list_blocks[b];
+    else if (b < blocks) x = keys[own];
+    const bool some = x.last > q0;
+    const bool all = some && x.first > q1 && (own < 0 || k0 + own * kTrainBlock + kTrainBlock - 1 <= q0);
     bool bad = false;
-    if (some && !all) bad = odd[b] != 0;
+    if (some && !all) bad = own < 0 ? odd_list : odd[own] != 0;
     seen = __ballot(some);
     whole = __ballot(all);
     rows_only |= __any(bad);
@@ -204,10 +232,22 @@ struct KeyWalk {
     *all = whole >> x & 1;
     return base + x;
   }
-  __device__ __forceinline__ int first(bool* all, int lane) {
-    base = -64;
-    return next(all, lane);
+  // Key `lane` of block b and its death time (not above its number: nobody sees it).
+  __device__ __forceinline__ KeyEntry key(int b, int lane) const {
+    if (b < listed) return list[b * kTrainBlock + lane];
+    const int i = (b - listed) * kTrainBlock + lane;
+    return KeyEntry{k0 + i, k0 + i < n_pad ? death[i] : -1};
   }
+  // The row to read for it.  A key that nobody sees may hold anything: its place reads
+  // another key's row.
+  static __device__ __forceinline__ int row_of(KeyEntry x, int lane) {
+    const uint64_t some = __ballot(x.death > x.key);
+    const int other = __shfl(x.key, some ? __builtin_ctzll(some) : 0);
+    return some >> lane & 1 ? x.key : other;
+  }
+  // What the place of a block's key adds to its number for the comparison with a query:
+  // listed keys come before every query of the epoch.
+  __device__ __forceinline__ int first_key(int b) const { return b < listed ? -kTrainBlock : k0 + (b - listed) * kTrainBlock; }
 };
 
 }  // namespace

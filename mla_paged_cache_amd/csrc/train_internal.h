@@ -14,9 +14,14 @@ struct Heads {
   int64_t rs, ts, hs;
 };
 
-// Keys and queries are taken in blocks of this many tokens for what the workspace
-// says of them.
+// Keys and queries are taken in blocks of this many tokens.
 constexpr int kTrainBlock = 64;
+// Queries of one workgroup of the forward pass and of dq, keys of one of dk and dv.
+constexpr int kTrainTile = 128;
+// A rollout is cut into at most so many epochs of equal length, a multiple of
+// kTrainTile.  The keys that are still seen when an epoch begins are listed, so that its
+// queries go along those (and the epoch's own keys) instead of everything before them.
+constexpr int kTrainEpochs = 64;
 
 // Of a block of keys: the first and the last of its death times, each at most n_pad,
 // a key that nobody sees counted as -1.  Queries [q0, q1] see all of keys [k0, k1] if
@@ -24,6 +29,13 @@ constexpr int kTrainBlock = 64;
 struct KeyBlock {
   int32_t first;
   int32_t last;
+};
+
+// A key of an epoch's list, and its death time (at most n_pad); places behind the last
+// key up to a multiple of kTrainBlock hold key 0 and -1.
+struct KeyEntry {
+  int32_t key;
+  int32_t death;
 };
 
 struct TrainLaunch {
@@ -35,13 +47,23 @@ struct TrainLaunch {
   const int32_t* death;
   Heads q, k, v, out, dout, dq, dk_, dv_;
   float* lse;                    // [n][n_pad][heads]
+  int32_t epoch, epochs;         // length of an epoch, and how many there are
   // workspace
   KeyBlock* keys;                // [n][blocks]
-  uint32_t* odd_k;               // [n][kv_heads][blocks]: not 0 where a value of k is not finite; the same of v, q, dout
-  uint32_t* odd_v;
-  uint32_t* odd_q;               // [n][heads][blocks]
+  KeyEntry* list;                // [n][list_keys]: epoch e's at list_at(e), which holds up to e * epoch keys
+  KeyBlock* list_blocks;         // of the lists' blocks, in the same way
+  int32_t* list_count;           // [n][epochs] keys
+  int32_t* order;                // [n][n_pad]: backward, the keys by the epoch that they die in, the last first, and
+                                 // then by place; those that nobody sees behind them
+  int32_t* seen_keys;            // [n]: how many are seen
+  uint32_t* odd_k;               // [n][kv_heads][blocks]: whether a key that is seen holds a value that is not finite;
+  uint32_t* odd_v;               // the same of v
+  uint32_t* odd_q;               // [n][heads][blocks]: of q and dout, any query
   uint32_t* odd_do;
   float* delta;                  // [n][heads][n_pad]: sum of dout * out
+
+  __host__ __device__ int64_t list_at(int64_t e) const { return e * (e - 1) / 2 * epoch; }
+  __host__ __device__ int64_t list_keys() const { return list_at(epochs); }
 };
 
 hipError_t launch_train_scan(const TrainLaunch& a, bool backward, hipStream_t s);
