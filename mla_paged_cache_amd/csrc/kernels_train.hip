@@ -195,7 +195,12 @@ __global__ __launch_bounds__(kScanThreads) void train_scan_kernel(TrainLaunch a)
     if (BACKWARD && sum) {
       float d = dot8(load8(at(x, r, min(t0 + t, a.n_pad - 1), h) + c, live), load8(at(y, r, min(t0 + t, a.n_pad - 1), h) + c, live));
       for (int k = 1 << shift >> 1; k >= 1; k >>= 1) d += __shfl_xor(d, k);
-      if (c == 0 && t < rows) a.delta[(static_cast<int64_t>(r) * a.heads + h) * a.n_pad + t0 + t] = d;
+      if (c == 0 && t < rows) {
+        const int64_t i = (static_cast<int64_t>(r) * a.heads + h) * a.n_pad + t0 + t;
+        const float lse = a.lse[(static_cast<int64_t>(r) * a.n_pad + t0 + t) * a.heads + h];
+        a.delta[i] = d;
+        a.ref[i] = lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;   // no weight: every p is 0
+      }
     }
   }
   const bool any = __any((bits & kNotFinite) != 0);
@@ -213,7 +218,7 @@ __global__ __launch_bounds__(kScanThreads) void train_scan_kernel(TrainLaunch a)
 // by more than 8, so weights stay below 2^8 and most tiles scale nothing.
 template <int DK, int DV, int BN, int WAVES, bool CAP>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 192 ? 1 : 2))) void train_kernel(TrainLaunch a) {
-  extern __shared__ __attribute__((aligned(16))) char smem[];
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
   using KR = Rows<DK>;
   using VR = Rows<DV>;
   constexpr int STAGE = BN * (KR::BYTES + VR::BYTES) + kTrainBlock * 4;   // keys, values, death times
@@ -266,6 +271,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     next = walk.next(&next_all, lane);
     if (next >= 0) next_key = walk.key(next, lane);
   }
+  const int k_at = KR::straight_at(lane), v_at = VR::columns_at(lane);
   while (block >= 0 && !walk.rows_only) {
     const bool ends = part == PARTS - 1;   // the block's last tile
     const int then = ends && next >= 0 ? walk.next(&then_all, lane) : -1;
@@ -278,7 +284,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
       load(next_key, 0, stage ^ 1);
       if (then >= 0) then_key = walk.key(then, lane);
     }
-    const lds_ptr ks = lds + stage * STAGE, vs = ks + BN * KR::BYTES;
+    const uint32_t ks = tile_at(lds + stage * STAGE, k_at), vs = tile_at(lds + stage * STAGE + BN * KR::BYTES, v_at);
     const int k0 = walk.first_key(block);
 
     f32x16 s[KB];
@@ -287,7 +293,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
 #pragma unroll
-      for (int k = 0; k < KK; ++k) s[b] = mfma(KR::straight(ks, b * 32, k, lane), q[k], s[b]);
+      for (int k = 0; k < KK; ++k) s[b] = mfma(KR::straight(ks, b * 32, k), q[k], s[b]);
     }
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
@@ -297,12 +303,10 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
         for (int i = 0; i < 16; ++i) s[b][i] *= cap2;
       }
       if (!all) {
-        const int* const d = reinterpret_cast<const int*>(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES));
+        const uint32_t seen = seen_bits(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES), part * BN + b * 32, k0, mine, lane);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int k = part * BN + b * 32 + product_row(i, lane);
-          if (k0 + k > mine || mine >= d[k]) s[b][i] = -__builtin_inff();
-        }
+        for (int i = 0; i < 16; ++i)
+          if (!(seen >> i & 1)) s[b][i] = -__builtin_inff();
       }
     }
     float top = -__builtin_inff();
@@ -331,7 +335,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
       for (int x = 0; x < 2; ++x) {
         const bf16x8 p = operand(s[b], x);
 #pragma unroll
-        for (int d = 0; d < DB; ++d) o[d] = mfma(VR::columns(vs, b * 32 + x * 16, d, lane), p, o[d]);
+        for (int d = 0; d < DB; ++d) o[d] = mfma(VR::columns(vs, b * 32 + x * 16, d), p, o[d]);
       }
     }
     stage ^= 1;

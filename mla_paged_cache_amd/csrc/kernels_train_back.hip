@@ -7,6 +7,12 @@
 // of a key for dk and dv, so that each sum has one owner and one order.
 #include "train_common.h"
 
+#ifndef AH
+#define AH 3
+#endif
+#ifndef QW_
+#define QW_ 2
+#endif
 namespace ll {
 namespace {
 
@@ -70,7 +76,7 @@ __device__ void train_dkv_row(const TrainLaunch& a, int r, int k, int kvh, int l
 // registers, then dQ^T += K^T dS^T, K^T from the transposing LDS reads.
 template <int DK, int DV, int BN, int WAVES, bool CAP>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 192 ? 1 : 2))) void train_dq_kernel(TrainLaunch a) {
-  extern __shared__ __attribute__((aligned(16))) char smem[];
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
   using KR = Rows<DK>;
   using VR = Rows<DV>;
   constexpr int STAGE = BN * (KR::BYTES + VR::BYTES) + kTrainBlock * 4;   // keys, values, death times
@@ -91,9 +97,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
   load_operand(g, at(a.dout, r, row, h), mine < a.n_pad, live_v, lane);
   const float c = fold_scale<CAP>(q, a.scale, a.cap);
   const float c2 = CAP ? a.cap * kLog2e : c;
-  const float lse = a.lse[(static_cast<int64_t>(r) * a.n_pad + row) * a.heads + h];
-  const float ref = lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;   // no weight: every p is 0
-  const float delta = a.delta[(static_cast<int64_t>(r) * a.heads + h) * a.n_pad + row];
+  const int64_t at_row = (static_cast<int64_t>(r) * a.heads + h) * a.n_pad + row;
+  const float ref = a.ref[at_row], delta = a.delta[at_row];
 
   if (live_k < KR::CH || live_v < VR::CH) {
     for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
@@ -124,6 +129,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     next = walk.next(&next_all, lane);
     if (next >= 0) next_key = walk.key(next, lane);
   }
+  const int k_at = KR::straight_at(lane), v_at = VR::straight_at(lane), c_at = KR::columns_at(lane);
   while (block >= 0 && !walk.rows_only) {
     const bool ends = part == PARTS - 1;   // the block's last tile
     const int then = ends && next >= 0 ? walk.next(&then_all, lane) : -1;
@@ -136,36 +142,33 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
       load(next_key, 0, stage ^ 1);
       if (then >= 0) then_key = walk.key(then, lane);
     }
-    const lds_ptr ks = lds + stage * STAGE, vs = ks + BN * KR::BYTES;
+    const lds_ptr keys = lds + stage * STAGE;
+    const uint32_t ks = tile_at(keys, k_at), vs = tile_at(keys + BN * KR::BYTES, v_at), cs = tile_at(keys, c_at);
     const int k0 = walk.first_key(block);
-    const int* const dt = reinterpret_cast<const int*>(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES));
 #pragma unroll 1
     for (int b = 0; b < KB; ++b) {
       f32x16 s, dp;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KK; ++k) s = mfma(KR::straight(ks, b * 32, k, lane), q[k], s);
-#pragma unroll
-      for (int k = 0; k < VK; ++k) dp = mfma(VR::straight(vs, b * 32, k, lane), g[k], dp);
+      stream<KK, AH>([&](int k) { return KR::straight(ks, b * 32, k); }, [&](int k, bf16x8 x) { s = mfma(x, q[k], s); });
+      stream<VK, AH>([&](int k) { return VR::straight(vs, b * 32, k); }, [&](int k, bf16x8 x) { dp = mfma(x, g[k], dp); });
       if constexpr (CAP) tanh_all(s, c);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float slope = CAP ? 1.f - s[i] * s[i] : 1.f;
-        float p = exp2_(__builtin_fmaf(s[i], c2, -ref));
-        p *= (dp[i] - delta) * (a.scale * slope);
-        if (!all) {
-          const int k = part * BN + b * 32 + product_row(i, lane);
-          if (k0 + k > mine || mine >= dt[k]) p = 0.f;
-        }
-        s[i] = p;
+        const float p = exp2_(__builtin_fmaf(s[i], c2, -ref));
+        s[i] = p * (dp[i] - delta) * slope;
       }
+      if (!all) {
+        const uint32_t seen = seen_bits(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES), part * BN + b * 32, k0, mine, lane);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bf16x8 ds = operand(s, x);
-#pragma unroll
-        for (int d = 0; d < DB; ++d) o[d] = mfma(KR::columns(ks, b * 32 + x * 16, d, lane), ds, o[d]);
+        for (int i = 0; i < 16; ++i)
+          if (!(seen >> i & 1)) s[i] = 0.f;
       }
+      const bf16x8 ds[2] = {operand(s, 0), operand(s, 1)};
+      __builtin_amdgcn_sched_barrier(0);
+      stream<2 * DB, AH>([&](int x) { return KR::columns(cs, b * 32 + x / DB * 16, x % DB); },
+                         [&](int x, bf16x8 y) { o[x % DB] = mfma(y, ds[x / DB], o[x % DB]); });
     }
     stage ^= 1;
     if (!ends) {
@@ -187,52 +190,59 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const int col = d * 32 + product_row(i, lane);
-      f32x4 x{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
-      if (lse == -__builtin_inff()) x = f32x4{0.f, 0.f, 0.f, 0.f};   // no weight at all, whatever the keys hold
+      f32x4 x = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]} * a.scale;
+      if (ref == __builtin_inff()) x = f32x4{0.f, 0.f, 0.f, 0.f};   // no weight at all, whatever the keys hold
       if (col < a.dk) *reinterpret_cast<bf16x4*>(out + col) = __builtin_convertvector(x, bf16x4);
     }
 }
 
-// dk and dv: a workgroup takes 32 * WAVES keys of a KV head, a wave 32 of them in
-// registers, and goes along the queries that see some of them, of each head that shares
-// them, BN at a time through LDS: S = Q K^T and dP = dO V^T with a lane per key, then
-// dV^T += dO^T P and dK^T += Q^T dS, dO^T and Q^T from the transposing LDS reads.
-template <int DK, int DV, int BN, int WAVES, bool CAP>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 64 ? 1 : 2))) void train_dkv_kernel(TrainLaunch a) {
-  extern __shared__ __attribute__((aligned(16))) char smem[];
+// dk and dv: a workgroup takes kTrainTile keys of a KV head in the order that the scan
+// made, a wave 32 of them (K in registers, V in LDS or registers), and goes along the
+// queries that see some of them, of each head that shares them, 32 * QW at a time through
+// LDS, of which a wave takes 32: S = Q K^T and dP = dO V^T with a lane per key, then
+// dV^T += dO^T P and dK^T += Q^T dS, dO^T and Q^T from the transposing LDS reads.  In the
+// end the QW waves of the same keys add up.
+template <int DK, int DV, int QW, bool VLDS>
+struct KeyShape {
+  static constexpr int KW = kTrainTile / 32, WAVES = KW * QW, BN = 32 * QW;
+  static constexpr int STAGE = BN * (DK + DV) * 2 + 2 * BN * 4;   // queries, dout, lse and delta
+  static constexpr int VALUES = 2 * STAGE;                       // where V lies
+  static constexpr int SUMS = QW > 1 ? KW * 32 * (DK > DV ? DK : DV) * 4 : 0;
+  static constexpr int LDS = VALUES + (VLDS ? kTrainTile * DV * 2 : 0);
+  static_assert(QW <= 2 && SUMS <= LDS && VALUES % 256 == 0, "the second wave's sums fit where the tiles were");
+};
+template <int DK, int DV, int QW, bool VLDS, int OCC, bool CAP>
+__global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_per_eu(OCC))) void train_dkv_kernel(TrainLaunch a) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  using S = KeyShape<DK, DV, QW, VLDS>;
   using QR = Rows<DK>;
   using GR = Rows<DV>;
-  constexpr int STAGE = BN * (QR::BYTES + GR::BYTES) + 2 * 256;   // queries, dout, lse, delta
+  constexpr int WAVES = S::WAVES, BN = S::BN, STAGE = S::STAGE;
   constexpr int KK = DK / 16, VK = DV / 16, KD = DK / 32, VD = DV / 32;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = wave % S::KW, qw = wave / S::KW;
   const int pairs = a.n * a.kv_heads, pair = blockIdx.x % pairs;
   const int r = pair / a.kv_heads, kvh = pair % a.kv_heads;
-  // places [p0, p0 + 32 * WAVES) of the keys' order: the first see the most queries
-  const int p0 = blockIdx.x / pairs * 32 * WAVES, place_ = p0 + wave * 32 + (lane & 31);
+  // places [p0, p0 + kTrainTile) of the keys' order: the first see the most queries
+  const int p0 = blockIdx.x / pairs * kTrainTile, place_ = p0 + kw * 32 + (lane & 31);
   const int32_t* const order = a.order + static_cast<int64_t>(r) * a.n_pad;
   const int32_t* const death = a.death + static_cast<int64_t>(r) * a.n_pad;
   const int mine = order[min(place_, a.n_pad - 1)];              // this lane's key
-  const bool there = place_ < min(a.n_pad, a.seen_keys[r]);      // which somebody sees
+  const int some = min(a.n_pad, a.seen_keys[r]);                 // places of keys that somebody sees
+  const bool there = place_ < some;
   const lds_ptr lds = (lds_ptr)smem;
   const int live_k = a.dk / 8, live_v = a.dv / 8;
-
-  bf16x8 k[KK], v[VK];
-  load_operand(k, at(a.k, r, mine, kvh), there, live_k, lane);
-  load_operand(v, at(a.v, r, mine, kvh), there, live_v, lane);
-  const float c = fold_scale<CAP>(k, a.scale, a.cap);
-  const float c2 = CAP ? a.cap * kLog2e : c;
-  const int end = there ? min(death[mine], a.n_pad) : 0;   // this lane's key is seen by queries [mine, end)
   // of all keys of the workgroup: the last query that sees one, up to which all do, and
   // the first and last key
-  int last = 0, first = INT32_MAX, k0 = INT32_MAX, k1 = 0;
+  int last = 0, first = INT32_MAX, k0 = INT32_MAX, k1 = 0, rows[kTrainTile / 64];
 #pragma unroll
-  for (int i = 0; i < WAVES / 2; ++i) {
+  for (int i = 0; i < kTrainTile / 64; ++i) {
     const int p = p0 + i * 64 + lane;
-    const bool some = p < min(a.n_pad, a.seen_keys[r]);
-    const int key = order[min(p, a.n_pad - 1)], d = some ? min(death[key], a.n_pad) : 0;
+    const int key = order[min(p, a.n_pad - 1)], d = p < some ? min(death[key], a.n_pad) : 0;
+    rows[i] = key;
     last = max(last, d);
     first = min(first, d);
-    if (some) k0 = min(k0, key), k1 = max(k1, key);
+    if (p < some) k0 = min(k0, key), k1 = max(k1, key);
   }
   for (int x = 32; x >= 1; x >>= 1) {
     last = max(last, __shfl_xor(last, x));
@@ -240,34 +250,51 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     k0 = min(k0, __shfl_xor(k0, x));
     k1 = max(k1, __shfl_xor(k1, x));
   }
+  last = __builtin_amdgcn_readfirstlane(last);
+  first = __builtin_amdgcn_readfirstlane(first);
+  k0 = __builtin_amdgcn_readfirstlane(k0);
+  k1 = __builtin_amdgcn_readfirstlane(k1);
+  const int end = there ? min(death[mine], a.n_pad) : mine;   // this lane's key is seen by queries [mine, end)
 
-  if (live_k < QR::CH || live_v < GR::CH) {
-    for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
+  bf16x8 k[KK], v[VLDS ? 1 : VK];
+  load_operand(k, at(a.k, r, mine, kvh), there, live_k, lane);
+  if constexpr (!VLDS) load_operand(v, at(a.v, r, mine, kvh), there, live_v, lane);
+  const float c = fold_scale<CAP>(k, a.scale, a.cap);
+  const float c2 = CAP ? a.cap * kLog2e : c;
+  if (VLDS || live_k < QR::CH || live_v < GR::CH) {   // (V's places of keys that nobody sees stay 0)
+    for (int i = threadIdx.x; i < S::LDS / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
     __syncthreads();
   }
-  // step i: queries [t0 + i % tiles * BN ...) of head i / tiles
-  const int t0 = k0 - k0 % kTrainBlock, tiles = last > t0 ? (last - t0 + BN - 1) / BN : 0, steps = tiles * a.group;
-  auto load = [&](int i, int stage) {
-    const lds_ptr dst = lds + stage * STAGE;
-    const int h = kvh * a.group + i / tiles, q0 = t0 + i % tiles * BN, row = min(q0 + lane, a.n_pad - 1);
-    QR::template load<BN, WAVES>(dst, at(a.q, r, 0, h), a.q.ts, row, 0, live_k, wave, lane);
-    GR::template load<BN, WAVES>(dst + BN * QR::BYTES, at(a.dout, r, 0, h), a.dout.ts, row, 0, live_v, wave, lane);
-    if (wave == 0) load_lds4(dst + BN * (QR::BYTES + GR::BYTES), a.lse + (static_cast<int64_t>(r) * a.n_pad + row) * a.heads + h);
-    if (wave == 1) load_lds4(dst + BN * (QR::BYTES + GR::BYTES) + 256, a.delta + (static_cast<int64_t>(r) * a.heads + h) * a.n_pad + row);
-  };
+  if constexpr (VLDS) {
+#pragma unroll
+    for (int i = 0; i < kTrainTile / 64; ++i)
+      GR::template load<64, WAVES>(lds + S::VALUES + i * 64 * GR::BYTES, at(a.v, r, 0, kvh), a.v.ts, rows[i], 0, live_v, wave,
+                                   lane, some - p0 - i * 64);
+  }
   // a tile of queries that sees the keys in part, with a value that is not finite
+  const int t0 = k0 - k0 % kTrainBlock, blocks = last > t0 ? (last - t0 + kTrainBlock - 1) / kTrainBlock : 0;
   bool rows_only = false;
-  for (int x = lane; x < a.group * ((last - t0 + kTrainBlock - 1) / kTrainBlock); x += 64) {
-    const int nb = (last - t0 + kTrainBlock - 1) / kTrainBlock, b = t0 / kTrainBlock + x % nb;
-    const int64_t o = (static_cast<int64_t>(r) * a.heads + kvh * a.group + x / nb) * a.blocks + b;
+  for (int x = lane; x < a.group * blocks; x += 64) {
+    const int b = t0 / kTrainBlock + x % blocks;
+    const int64_t o = (static_cast<int64_t>(r) * a.heads + kvh * a.group + x / blocks) * a.blocks + b;
     const bool all = b * kTrainBlock >= k1 && b * kTrainBlock + kTrainBlock - 1 < first;
     if (!all && (a.odd_q[o] | a.odd_do[o])) rows_only = true;
   }
-  rows_only = __any(rows_only);
-  if (rows_only) {
-    for (int i = p0 + wave; i < min(p0 + 32 * WAVES, a.n_pad); i += WAVES) train_dkv_row(a, r, order[i], kvh, lane);
+  if (__any(rows_only)) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // loads on their way into LDS
+    for (int i = p0 + wave; i < min(p0 + kTrainTile, a.n_pad); i += WAVES) train_dkv_row(a, r, order[i], kvh, lane);
     return;
   }
+  // step i: queries [t0 + i % tiles * BN ...) of head i / tiles
+  const int tiles = blocks * kTrainBlock / BN, steps = tiles * a.group;
+  auto load = [&](int i, int stage) {
+    const lds_ptr dst = lds + stage * STAGE;
+    const int h = kvh * a.group + i / tiles, row = min(t0 + i % tiles * BN + lane, a.n_pad - 1);
+    QR::template load<BN, WAVES>(dst, at(a.q, r, 0, h), a.q.ts, row, 0, live_k, wave, lane);
+    GR::template load<BN, WAVES>(dst + BN * QR::BYTES, at(a.dout, r, 0, h), a.dout.ts, row, 0, live_v, wave, lane);
+    const int64_t q = (static_cast<int64_t>(r) * a.heads + h) * a.n_pad + row;
+    if (wave < 2 && lane < BN) load_lds4(dst + BN * (QR::BYTES + GR::BYTES) + wave * BN * 4, (wave == 0 ? a.ref : a.delta) + q);
+  };
 
   f32x16 gk[KD], gv[VD];
 #pragma unroll
@@ -278,77 +305,116 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     for (int d = 0; d < VD; ++d) gv[d][i] = 0.f;
   }
   if (steps > 0) load(0, 0);
+  const int q_at = QR::straight_at(lane), g_at = GR::straight_at(lane), qc_at = QR::columns_at(lane), gc_at = GR::columns_at(lane);
   for (int i = 0; i < steps; ++i) {
     const int stage = i & 1, q0 = t0 + i % tiles * BN;
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
     if (i + 1 < steps) load(i + 1, stage ^ 1);
-    const lds_ptr qs = lds + stage * STAGE, gs = qs + BN * QR::BYTES;
-    const float* const ls = reinterpret_cast<const float*>(smem + stage * STAGE + BN * (QR::BYTES + GR::BYTES));
+    const lds_ptr qs = lds + stage * STAGE + qw * 32 * QR::BYTES, gs = lds + stage * STAGE + BN * QR::BYTES + qw * 32 * GR::BYTES;
+    const uint32_t qa = tile_at(qs, q_at), ga = tile_at(gs, g_at), qc = tile_at(qs, qc_at), gc = tile_at(gs, gc_at);
+    const uint32_t va = VLDS ? tile_at(lds + S::VALUES + kw * 32 * GR::BYTES, g_at) : 0u;
+    const f32x4* const ls = reinterpret_cast<const f32x4*>(smem + stage * STAGE + BN * (QR::BYTES + GR::BYTES)) + qw * 8;
     const bool all = q0 >= k1 && q0 + BN - 1 < first;
-#pragma unroll 1
-    for (int b = 0; b < BN / 32; ++b) {
-      f32x16 s, dp;
+    f32x16 s, dp;
 #pragma unroll
-      for (int x = 0; x < 16; ++x) s[x] = dp[x] = 0.f;
+    for (int x = 0; x < 16; ++x) s[x] = dp[x] = 0.f;
+    stream<KK, AH>([&](int x) { return QR::straight(qa, 0, x); }, [&](int x, bf16x8 y) { s = mfma(y, k[x], s); });
+    if constexpr (VLDS) {
+      bf16x8 z[2];
+      stream<2 * VK, 4>([&](int x) { return x & 1 ? GR::straight(va, 0, x / 2) : GR::straight(ga, 0, x / 2); },
+                        [&](int x, bf16x8 y) {
+                          z[x & 1] = y;
+                          if (x & 1) dp = mfma(z[0], z[1], dp);
+                        });
+    } else {
+      stream<VK, AH>([&](int x) { return GR::straight(ga, 0, x); }, [&](int x, bf16x8 y) { dp = mfma(y, v[x], dp); });
+    }
+    if constexpr (CAP) tanh_all(s, c);
 #pragma unroll
-      for (int x = 0; x < KK; ++x) s = mfma(QR::straight(qs, b * 32, x, lane), k[x], s);
+    for (int x = 0; x < 16; x += 4) {
+      const f32x4 ref = ls[product_row(x, lane) / 4], delta = ls[BN / 4 + product_row(x, lane) / 4];
 #pragma unroll
-      for (int x = 0; x < VK; ++x) dp = mfma(GR::straight(gs, b * 32, x, lane), v[x], dp);
-      if constexpr (CAP) tanh_all(s, c);
-#pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const int t = b * 32 + product_row(x, lane);
-        const float lse = ls[t], ref = lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;
-        const float slope = CAP ? 1.f - s[x] * s[x] : 1.f;
-        float p = exp2_(__builtin_fmaf(s[x], c2, -ref));
-        float ds = p * (dp[x] - ls[64 + t]) * (a.scale * slope);
-        if (!all && (q0 + t < mine || q0 + t >= end)) p = ds = 0.f;
-        s[x] = p;
-        dp[x] = ds;
-      }
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const bf16x8 p = operand(s, y), ds = operand(dp, y);
-#pragma unroll
-        for (int d = 0; d < VD; ++d) gv[d] = mfma(GR::columns(gs, b * 32 + y * 16, d, lane), p, gv[d]);
-#pragma unroll
-        for (int d = 0; d < KD; ++d) gk[d] = mfma(QR::columns(qs, b * 32 + y * 16, d, lane), ds, gk[d]);
+      for (int y = 0; y < 4; ++y) {
+        const float slope = CAP ? 1.f - s[x + y] * s[x + y] : 1.f;
+        const float p = exp2_(__builtin_fmaf(s[x + y], c2, -ref[y]));
+        dp[x + y] = p * (dp[x + y] - delta[y]) * slope;
+        s[x + y] = p;
       }
     }
+    if (!all) {
+      uint32_t from = mine - q0 - qw * 32, n = end - mine;   // seen: queries [from, from + n) of the wave's 32
+      asm volatile("" : "+v"(from), "+v"(n));                // (a branch around it, not a selection)
+#pragma unroll
+      for (int x = 0; x < 16; ++x)
+        if (product_row(x, lane) - from >= n) s[x] = dp[x] = 0.f;
+    }
+    const bf16x8 p[2] = {operand(s, 0), operand(s, 1)}, ds[2] = {operand(dp, 0), operand(dp, 1)};
+    __builtin_amdgcn_sched_barrier(0);
+    stream<2 * (VD + KD), AH>(
+        [&](int x) {
+          return x < 2 * VD ? GR::columns(gc, x / VD * 16, x % VD)
+                            : QR::columns(qc, (x - 2 * VD) / KD * 16, (x - 2 * VD) % KD);
+        },
+        [&](int x, bf16x8 y) {
+          if (x < 2 * VD) gv[x % VD] = mfma(y, p[x / VD], gv[x % VD]);
+          else gk[(x - 2 * VD) % KD] = mfma(y, ds[(x - 2 * VD) / KD], gk[(x - 2 * VD) % KD]);
+        });
   }
-  if (place_ >= a.n_pad) return;
-  auto store = [&](uint16_t* to, const f32x16& x, int d, int width) {
+  if constexpr (QW > 1) {
+    // the other waves' sums through LDS, 16 bytes a lane at a time
+    f32x4* const sums = reinterpret_cast<f32x4*>(smem) + kw * 32 * (DK > DV ? DK : DV) / 4;
+    auto join = [&](auto& g) {
+      constexpr int N = sizeof(g) / sizeof(f32x16);
+      __syncthreads();
+      if (qw == 1)
+#pragma unroll
+        for (int d = 0; d < N; ++d)
+#pragma unroll
+          for (int x = 0; x < 16; x += 4) sums[(d * 4 + x / 4) * 64 + lane] = f32x4{g[d][x], g[d][x + 1], g[d][x + 2], g[d][x + 3]};
+      __syncthreads();
+      if (qw == 0)
+#pragma unroll
+        for (int d = 0; d < N; ++d)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) g[d][x] += sums[(d * 4 + x / 4) * 64 + lane][x & 3];
+    };
+    join(gk);
+    join(gv);
+  }
+  if (place_ >= a.n_pad || qw > 0) return;
+  auto store = [&](uint16_t* to, const f32x16& x, int d, int width, float by) {
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const int col = d * 32 + product_row(i, lane);
       const f32x4 y{x[i], x[i + 1], x[i + 2], x[i + 3]};
-      if (col < width) *reinterpret_cast<bf16x4*>(to + col) = __builtin_convertvector(y, bf16x4);
+      if (col < width) *reinterpret_cast<bf16x4*>(to + col) = __builtin_convertvector(y * by, bf16x4);
     }
   };
 #pragma unroll
-  for (int d = 0; d < KD; ++d) store(place(a.dk_, r, mine, kvh), gk[d], d, a.dk);
+  for (int d = 0; d < KD; ++d) store(place(a.dk_, r, mine, kvh), gk[d], d, a.dk, a.scale);
 #pragma unroll
-  for (int d = 0; d < VD; ++d) store(place(a.dv_, r, mine, kvh), gv[d], d, a.dv);
+  for (int d = 0; d < VD; ++d) store(place(a.dv_, r, mine, kvh), gv[d], d, a.dv, 1.f);
 }
 
-template <int DK, int DV, int BN, int WAVES, bool CAP>
+template <int DK, int DV, int BN, int QW, bool VLDS, int OCC, bool CAP>
 hipError_t launch_shape(const TrainLaunch& a, hipStream_t s) {
-  constexpr int q_lds = 2 * (BN * (DK + DV) * 2 + kTrainBlock * 4), k_lds = 2 * (BN * (DK + DV) * 2 + 512);
-  hipError_t e = allow_lds<train_dq_kernel<DK, DV, BN, WAVES, CAP>>(q_lds);
-  if (e == hipSuccess) e = allow_lds<train_dkv_kernel<DK, DV, BN, WAVES, CAP>>(k_lds);
+  using K = KeyShape<DK, DV, QW, VLDS>;
+  constexpr int waves = kTrainTile / 32, lds = 2 * (BN * (DK + DV) * 2 + kTrainBlock * 4);
+  hipError_t e = allow_lds<train_dq_kernel<DK, DV, BN, waves, CAP>>(lds);
+  if (e == hipSuccess) e = allow_lds<train_dkv_kernel<DK, DV, QW, VLDS, OCC, CAP>>(K::LDS);
   if (e != hipSuccess) return e;
-  const int64_t tiles = (a.n_pad + 32 * WAVES - 1) / (32 * WAVES);
-  train_dkv_kernel<DK, DV, BN, WAVES, CAP><<<dim3(static_cast<unsigned>(a.n * a.kv_heads * tiles)), dim3(64 * WAVES), k_lds, s>>>(a);
+  const int64_t tiles = (a.n_pad + kTrainTile - 1) / kTrainTile;
+  train_dkv_kernel<DK, DV, QW, VLDS, OCC, CAP><<<dim3(static_cast<unsigned>(a.n * a.kv_heads * tiles)), dim3(64 * K::WAVES), K::LDS, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  train_dq_kernel<DK, DV, BN, WAVES, CAP><<<dim3(static_cast<unsigned>(a.n * a.heads * tiles)), dim3(64 * WAVES), q_lds, s>>>(a);
+  train_dq_kernel<DK, DV, BN, waves, CAP><<<dim3(static_cast<unsigned>(a.n * a.heads * tiles)), dim3(64 * waves), lds, s>>>(a);
   return hipGetLastError();
 }
 
-template <int DK, int DV, int BN, int WAVES>
+template <int DK, int DV, int BN, int QW, bool VLDS, int OCC>
 hipError_t launch_cap(const TrainLaunch& a, hipStream_t s) {
-  return a.cap == 0.f ? launch_shape<DK, DV, BN, WAVES, false>(a, s) : launch_shape<DK, DV, BN, WAVES, true>(a, s);
+  return a.cap == 0.f ? launch_shape<DK, DV, BN, QW, VLDS, OCC, false>(a, s) : launch_shape<DK, DV, BN, QW, VLDS, OCC, true>(a, s);
 }
 
 }  // namespace
@@ -356,10 +422,10 @@ hipError_t launch_cap(const TrainLaunch& a, hipStream_t s) {
 hipError_t launch_train_back(const TrainLaunch& a, hipStream_t s) {
   hipError_t e = launch_train_scan(a, true, s);
   if (e != hipSuccess) return e;
-  if (a.dk <= 64 && a.dv <= 64) return launch_cap<64, 64, 64, 4>(a, s);
-  if (a.dk <= 128 && a.dv <= 128) return launch_cap<128, 128, 64, 4>(a, s);
-  if (a.dk <= 192 && a.dv <= 128) return launch_cap<192, 128, 32, 4>(a, s);
-  return launch_cap<256, 256, 32, 4>(a, s);
+  if (a.dk <= 64 && a.dv <= 64) return launch_cap<64, 64, 64, 2, false, 2>(a, s);
+  if (a.dk <= 128 && a.dv <= 128) return launch_cap<128, 128, 64, QW_, true, 2>(a, s);
+  if (a.dk <= 192 && a.dv <= 128) return launch_cap<192, 128, 32, 1, true, 1>(a, s);
+  return launch_cap<256, 256, 32, 1, true, 1>(a, s);
 }
 
 }  // namespace ll

@@ -82,6 +82,7 @@ int64_t lay_out(TrainLaunch* a, bool backward, char* at) {
     a->odd_q = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
     a->odd_do = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
     a->delta = reinterpret_cast<float*>(take(int64_t{a->n} * a->heads * a->n_pad * 4));
+    a->ref = reinterpret_cast<float*>(take(int64_t{a->n} * a->heads * a->n_pad * 4));
   }
   return size;
 }

@@ -78,10 +78,10 @@ struct Rows {
   }
   // N rows of a head (x: its row 0, ts: values from row to row) into LDS, by WAVES
   // waves; lane r's `row` is the tile's row r (of the part from lane `from` on).  Chunks
-  // past `live` are left alone.
+  // past `live` and rows from `rows` on are left alone.
   template <int N, int WAVES>
   static __device__ __forceinline__ void load(lds_ptr dst, const uint16_t* x, int64_t ts, int row, int from, int live,
-                                              int wave, int lane) {
+                                              int wave, int lane, int rows = N) {
     constexpr int LOADS = N * CH / 64;
     static_assert(LOADS % WAVES == 0, "as many for every wave");
 #pragma unroll
@@ -89,27 +89,63 @@ struct Rows {
       const int b = i * WAVES + wave;
       const int r = (b * 64 + lane) / CH, c = place(r, (b * 64 + lane) % CH);
       const int64_t at = __shfl(row, from + r);   // (every lane takes part)
-      if (c < live) load_lds<false>(dst + b * 1024, x + at * ts + c * 8);
+      if (c < live && r < rows) load_lds<false>(dst + b * 1024, x + at * ts + c * 8);
     }
   }
+  // A lane's byte offsets in a tile, to which the tile's address in LDS (a multiple of 256)
+  // is added; a step in k or d is then an exclusive or of the swizzled bits and a constant
+  // above them, a step of 16 rows a constant.
+  static constexpr int LOW = CH % 16 == 0 ? 16 : 8;   // chunks that the swizzle permutes
+  static __device__ __forceinline__ int straight_at(int lane) {
+    const int r = lane & 31;
+    return r * BYTES + (place(r, lane >> 5) << 4);
+  }
+  static __device__ __forceinline__ int columns_at(int lane) {
+    const int li = lane & 15, r = (lane >> 5) * 4 + (li >> 2);
+    return r * BYTES + (place(r, (lane >> 4 & 1) * 2 + (li >> 1 & 1)) << 4) + (li & 1) * 8;
+  }
   // Row r0 + (lane & 31), values 16 k + 8 (lane >> 5) on: an operand of S = X Y^T.
-  static __device__ __forceinline__ bf16x8 straight(lds_ptr x, int r0, int k, int lane) {
-    const int r = r0 + (lane & 31);
-    return lds_chunk(x + r * BYTES + (place(r, 2 * k + (lane >> 5)) << 4));
+  static __device__ __forceinline__ bf16x8 straight(uint32_t at, int r0, int k) {
+    return lds_chunk(reinterpret_cast<lds_ptr>(at ^ (2 * k % LOW) << 4) + r0 * BYTES + 2 * k / LOW * LOW * 16);
   }
   // Column 32 d + (lane & 31) of the rows that a lane of the 32x32 products holds:
   // r0 + 4 (lane >> 5) + {0 .. 3, 8 .. 11}.
-  static __device__ __forceinline__ bf16x8 columns(lds_ptr x, int r0, int d, int lane) {
-    const int li = lane & 15, c = d * 4 + (lane >> 4 & 1) * 2 + (li >> 1 & 1);
-    const int r = r0 + (lane >> 5) * 4 + (li >> 2), q = r + 8;
-    const s16x4 y0 = lds_columns(x + r * BYTES + (place(r, c) << 4) + (li & 1) * 8);
-    const s16x4 y1 = lds_columns(x + q * BYTES + (place(q, c) << 4) + (li & 1) * 8);
+  static __device__ __forceinline__ bf16x8 columns(uint32_t at, int r0, int d) {
+    const uint32_t c = (4 * d % LOW) << 4, o = r0 * BYTES + 4 * d / LOW * LOW * 16;
+    const s16x4 y0 = lds_columns(reinterpret_cast<lds_ptr>(at ^ c) + o);
+    const s16x4 y1 = lds_columns(reinterpret_cast<lds_ptr>(at ^ c ^ 32) + o + 8 * BYTES);
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 };
 
+// A lane's offset in the tile at x.  What follows from it is worked out where it is used,
+// in one instruction, rather than kept in registers.
+__device__ __forceinline__ uint32_t tile_at(lds_ptr x, int at) {
+  uint32_t y = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x)) + at;
+  asm volatile("" : "+v"(y));
+  return y;
+}
+
 // Row of a 32x32 product's value i in a lane.
 __device__ __forceinline__ int product_row(int i, int lane) { return (i >> 2) * 8 + (lane >> 5) * 4 + (i & 3); }
+
+// Whether the query of this lane sees the keys of a product's values, as bits: key i has
+// number first + product_row(i) and its death time in LDS (16-byte words of four).  Only
+// for blocks that are seen in part: a branch around it, not a selection.
+__device__ __forceinline__ uint32_t seen_bits(const char* deaths, int part, int first, int query, int lane) {
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const int k = part + product_row(i, lane);
+    const i32x4 d = *reinterpret_cast<const i32x4*>(deaths + k * 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (first + k + e <= query && query < d[e]) bits |= 1u << (i + e);
+  }
+  asm volatile("" : "+v"(bits));
+  return bits;
+}
 
 // Values 8 x .. 8 x + 7 of a product as the operand of the next one.
 __device__ __forceinline__ bf16x8 operand(const f32x16& p, int x) {
@@ -122,6 +158,22 @@ __device__ __forceinline__ bf16x8 operand(const f32x16& p, int x) {
 
 __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// N products whose operands are read a few steps ahead; the fences keep the compiler
+// from reading everything at once into registers that it lacks.
+template <int N, int AHEAD, typename Read, typename Use>
+__device__ __forceinline__ void stream(Read&& read, Use&& use) {
+  constexpr int A = AHEAD < N ? AHEAD : N;
+  bf16x8 x[A + 1];
+#pragma unroll
+  for (int i = 0; i < A; ++i) x[i] = read(i);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i + A < N) x[(i + A) % (A + 1)] = read(i + A);
+    use(i, x[i % (A + 1)]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 // A row (of q, k, v or dout) as a lane's operand: KK steps of 16 values, this lane's 8

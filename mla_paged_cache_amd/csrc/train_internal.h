@@ -61,6 +61,7 @@ struct TrainLaunch {
   uint32_t* odd_q;               // [n][heads][blocks]: of q and dout, any query
   uint32_t* odd_do;
   float* delta;                  // [n][heads][n_pad]: sum of dout * out
+  float* ref;                    // [n][heads][n_pad]: lse in base 2; infinity where there is no weight
 
   __host__ __device__ int64_t list_at(int64_t e) const { return e * (e - 1) / 2 * epoch; }
   __host__ __device__ int64_t list_keys() const { return list_at(epochs); }
