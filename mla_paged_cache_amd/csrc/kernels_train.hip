@@ -398,10 +398,12 @@ hipError_t launch_train_scan(const TrainLaunch& a, bool backward, hipStream_t s)
 hipError_t launch_train(const TrainLaunch& a, hipStream_t s) {
   hipError_t e = launch_train_scan(a, false, s);
   if (e != hipSuccess) return e;
-  if (a.dk <= 64 && a.dv <= 64) return launch_cap<64, 64, 64, 4>(a, s);
-  if (a.dk <= 128 && a.dv <= 128) return launch_cap<128, 128, 64, 4>(a, s);
-  if (a.dk <= 192 && a.dv <= 128) return launch_cap<192, 128, 32, 4>(a, s);
-  return launch_cap<256, 256, 32, 4>(a, s);
+  switch (head_shape(a.dk, a.dv).dk) {
+    case 64: return launch_cap<64, 64, 64, 4>(a, s);
+    case 128: return launch_cap<128, 128, 64, 4>(a, s);
+    case 192: return launch_cap<192, 128, 32, 4>(a, s);
+    default: return launch_cap<256, 256, 32, 4>(a, s);
+  }
 }
 
 }  // namespace ll

@@ -7,14 +7,10 @@
 // of a key for dk and dv, so that each sum has one owner and one order.
 #include "train_common.h"
 
-#ifndef AH
-#define AH 3
-#endif
-#ifndef QW_
-#define QW_ 2
-#endif
 namespace ll {
 namespace {
+
+constexpr int AH = 3;   // steps that a product's operands are read ahead (5: 2% slower)
 
 // One pair that is seen: the weight p and the gradient ds of its product.
 struct Pair {
@@ -74,12 +70,14 @@ __device__ void train_dkv_row(const TrainLaunch& a, int r, int k, int kvh, int l
 // dq: a workgroup takes 32 * WAVES queries of a head and goes along the keys that they
 // see, as the forward kernel does: S^T = K Q^T and dP^T = V dO^T with the queries in
 // registers, then dQ^T += K^T dS^T, K^T from the transposing LDS reads.
-template <int DK, int DV, int BN, int WAVES, bool CAP>
+// GLDS: dO lies in LDS, where the registers hold no more.
+template <int DK, int DV, int BN, int WAVES, bool GLDS, bool CAP>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 192 ? 1 : 2))) void train_dq_kernel(TrainLaunch a) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   using KR = Rows<DK>;
   using VR = Rows<DV>;
   constexpr int STAGE = BN * (KR::BYTES + VR::BYTES) + kTrainBlock * 4;   // keys, values, death times
+  constexpr int DOUT = 2 * STAGE;   // where dO lies
   constexpr int KB = BN / 32, KK = DK / 16, VK = DV / 16, DB = DK / 32, PARTS = kTrainBlock / BN;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pairs = a.n * a.kv_heads, pair = blockIdx.x % pairs, rest = blockIdx.x / pairs;
@@ -92,17 +90,24 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
   const uint16_t* const kp = at(a.k, r, 0, kvh);
   const uint16_t* const vp = at(a.v, r, 0, kvh);
 
-  bf16x8 q[KK], g[VK];
+  bf16x8 q[KK], g[GLDS ? 1 : VK];
   load_operand(q, at(a.q, r, row, h), mine < a.n_pad, live_k, lane);
-  load_operand(g, at(a.dout, r, row, h), mine < a.n_pad, live_v, lane);
+  if constexpr (!GLDS) load_operand(g, at(a.dout, r, row, h), mine < a.n_pad, live_v, lane);
   const float c = fold_scale<CAP>(q, a.scale, a.cap);
   const float c2 = CAP ? a.cap * kLog2e : c;
   const int64_t at_row = (static_cast<int64_t>(r) * a.heads + h) * a.n_pad + row;
   const float ref = a.ref[at_row], delta = a.delta[at_row];
 
   if (live_k < KR::CH || live_v < VR::CH) {
-    for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
+    for (int i = threadIdx.x; i < DOUT / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
+    if (GLDS) for (int i = threadIdx.x; i < 32 * WAVES * VR::BYTES / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem + DOUT)[i] = chunk_t{0u, 0u, 0u, 0u};
     __syncthreads();
+  }
+  if constexpr (GLDS) {   // (a wave reads its own rows: queries that are not there repeat the last one)
+#pragma unroll
+    for (int i = 0; i < WAVES / 2; ++i)
+      VR::template load<64, WAVES>(lds + DOUT + i * 64 * VR::BYTES, at(a.dout, r, 0, h), a.dout.ts,
+                                   min(q0 + i * 64 + lane, a.n_pad - 1), 0, live_v, wave, lane);
   }
   auto load = [&](KeyEntry key, int part, int stage) {
     const lds_ptr dst = lds + stage * STAGE;
@@ -144,6 +149,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     }
     const lds_ptr keys = lds + stage * STAGE;
     const uint32_t ks = tile_at(keys, k_at), vs = tile_at(keys + BN * KR::BYTES, v_at), cs = tile_at(keys, c_at);
+    const uint32_t gs = GLDS ? tile_at(lds + DOUT + wave * 32 * VR::BYTES, v_at) : 0u;
     const int k0 = walk.first_key(block);
 #pragma unroll 1
     for (int b = 0; b < KB; ++b) {
@@ -151,7 +157,16 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.f;
       stream<KK, AH>([&](int k) { return KR::straight(ks, b * 32, k); }, [&](int k, bf16x8 x) { s = mfma(x, q[k], s); });
-      stream<VK, AH>([&](int k) { return VR::straight(vs, b * 32, k); }, [&](int k, bf16x8 x) { dp = mfma(x, g[k], dp); });
+      if constexpr (GLDS) {
+        bf16x8 z[2];
+        stream<2 * VK, 4>([&](int x) { return x & 1 ? VR::straight(gs, 0, x / 2) : VR::straight(vs, b * 32, x / 2); },
+                          [&](int x, bf16x8 y) {
+                            z[x & 1] = y;
+                            if (x & 1) dp = mfma(z[0], z[1], dp);
+                          });
+      } else {
+        stream<VK, AH>([&](int k) { return VR::straight(vs, b * 32, k); }, [&](int k, bf16x8 x) { dp = mfma(x, g[k], dp); });
+      }
       if constexpr (CAP) tanh_all(s, c);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -223,8 +238,11 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
   const int kw = wave % S::KW, qw = wave / S::KW;
   const int pairs = a.n * a.kv_heads, pair = blockIdx.x % pairs;
   const int r = pair / a.kv_heads, kvh = pair % a.kv_heads;
+  // The longest tiles first.  A tile's later shares may be short or empty; which of them
+  // comes first changes from tile to tile, since workgroups go to the chip's parts in turn.
+  const int tile = blockIdx.x / pairs / a.shares, share = (blockIdx.x / pairs + tile) % a.shares;
   // places [p0, p0 + kTrainTile) of the keys' order: the first see the most queries
-  const int p0 = blockIdx.x / pairs * kTrainTile, place_ = p0 + kw * 32 + (lane & 31);
+  const int p0 = tile * kTrainTile, place_ = p0 + kw * 32 + (lane & 31);
   const int32_t* const order = a.order + static_cast<int64_t>(r) * a.n_pad;
   const int32_t* const death = a.death + static_cast<int64_t>(r) * a.n_pad;
   const int mine = order[min(place_, a.n_pad - 1)];              // this lane's key
@@ -254,6 +272,10 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
   first = __builtin_amdgcn_readfirstlane(first);
   k0 = __builtin_amdgcn_readfirstlane(k0);
   k1 = __builtin_amdgcn_readfirstlane(k1);
+  const int64_t slot = static_cast<int64_t>(pair) * ((a.n_pad + kTrainTile - 1) / kTrainTile) + tile;
+  const int t0 = k0 - k0 % kTrainBlock, blocks = last > t0 ? (last - t0 + kTrainBlock - 1) / kTrainBlock : 0;
+  const int cuts = max(1, (blocks * a.group + a.chunk - 1) / a.chunk);
+  if (share >= cuts) return;
   const int end = there ? min(death[mine], a.n_pad) : mine;   // this lane's key is seen by queries [mine, end)
 
   bf16x8 k[KK], v[VLDS ? 1 : VK];
@@ -261,7 +283,7 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
   if constexpr (!VLDS) load_operand(v, at(a.v, r, mine, kvh), there, live_v, lane);
   const float c = fold_scale<CAP>(k, a.scale, a.cap);
   const float c2 = CAP ? a.cap * kLog2e : c;
-  if (VLDS || live_k < QR::CH || live_v < GR::CH) {   // (V's places of keys that nobody sees stay 0)
+  if ((VLDS && p0 + kTrainTile > some) || live_k < QR::CH || live_v < GR::CH) {   // (V's places of keys that nobody sees stay 0)
     for (int i = threadIdx.x; i < S::LDS / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
     __syncthreads();
   }
@@ -272,7 +294,6 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
                                    lane, some - p0 - i * 64);
   }
   // a tile of queries that sees the keys in part, with a value that is not finite
-  const int t0 = k0 - k0 % kTrainBlock, blocks = last > t0 ? (last - t0 + kTrainBlock - 1) / kTrainBlock : 0;
   bool rows_only = false;
   for (int x = lane; x < a.group * blocks; x += 64) {
     const int b = t0 / kTrainBlock + x % blocks;
@@ -280,13 +301,18 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
     const bool all = b * kTrainBlock >= k1 && b * kTrainBlock + kTrainBlock - 1 < first;
     if (!all && (a.odd_q[o] | a.odd_do[o])) rows_only = true;
   }
-  if (__any(rows_only)) {
+  rows_only = __any(rows_only);
+  if (share == 0 && threadIdx.x == 0) a.used[slot] = rows_only ? 1 : cuts;
+  if (rows_only) {
     __builtin_amdgcn_s_waitcnt(0x0F70);   // loads on their way into LDS
+    if (share > 0) return;
     for (int i = p0 + wave; i < min(p0 + kTrainTile, a.n_pad); i += WAVES) train_dkv_row(a, r, order[i], kvh, lane);
     return;
   }
-  // step i: queries [t0 + i % tiles * BN ...) of head i / tiles
-  const int tiles = blocks * kTrainBlock / BN, steps = tiles * a.group;
+  // step i: queries [t0 + i % tiles * BN ...) of head i / tiles; this share's are
+  // [begin, steps)
+  const int per = kTrainBlock / BN, tiles = blocks * per, begin = share * a.chunk * per;
+  const int steps = min(begin + a.chunk * per, tiles * a.group);
   auto load = [&](int i, int stage) {
     const lds_ptr dst = lds + stage * STAGE;
     const int h = kvh * a.group + i / tiles, row = min(t0 + i % tiles * BN + lane, a.n_pad - 1);
@@ -304,10 +330,10 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
 #pragma unroll
     for (int d = 0; d < VD; ++d) gv[d][i] = 0.f;
   }
-  if (steps > 0) load(0, 0);
+  if (begin < steps) load(begin, 0);
   const int q_at = QR::straight_at(lane), g_at = GR::straight_at(lane), qc_at = QR::columns_at(lane), gc_at = GR::columns_at(lane);
-  for (int i = 0; i < steps; ++i) {
-    const int stage = i & 1, q0 = t0 + i % tiles * BN;
+  for (int i = begin; i < steps; ++i) {
+    const int stage = (i - begin) & 1, q0 = t0 + i % tiles * BN;
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
     if (i + 1 < steps) load(i + 1, stage ^ 1);
@@ -382,7 +408,21 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
     join(gk);
     join(gv);
   }
-  if (place_ >= a.n_pad || qw > 0) return;
+  if (qw > 0) return;
+  if (cuts > 1) {
+    // 16 bytes a lane at a time, which train_join_kernel adds up
+    f32x4* const parts = reinterpret_cast<f32x4*>(a.parts) + (slot * a.shares + share) * (kTrainTile * (DK + DV) / 4);
+    auto put = [&](f32x4* to, const f32x16& x) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) __builtin_nontemporal_store(f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]}, to + i / 4 * 64 + lane);
+    };
+#pragma unroll
+    for (int d = 0; d < KD; ++d) put(parts + (kw * KD + d) * 256, gk[d]);
+#pragma unroll
+    for (int d = 0; d < VD; ++d) put(parts + kTrainTile * DK / 4 + (kw * VD + d) * 256, gv[d]);
+    return;
+  }
+  if (place_ >= a.n_pad) return;
   auto store = [&](uint16_t* to, const f32x16& x, int d, int width, float by) {
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
@@ -397,18 +437,50 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
   for (int d = 0; d < VD; ++d) store(place(a.dv_, r, mine, kvh), gv[d], d, a.dv, 1.f);
 }
 
+// The shares of a tile of keys added up in order, 4 values of a key per thread.
+template <int DK, int DV>
+__global__ __launch_bounds__(256) void train_join_kernel(TrainLaunch a) {
+  constexpr int N = kTrainTile * (DK + DV) / 4, BLOCKS = N / 256;
+  const int64_t slot = blockIdx.x / BLOCKS;
+  const int cuts = a.used[slot];
+  if (cuts <= 1) return;
+  const int tiles = (a.n_pad + kTrainTile - 1) / kTrainTile, pair = static_cast<int>(slot / tiles);
+  const int r = pair / a.kv_heads, kvh = pair % a.kv_heads;
+  int i = blockIdx.x % BLOCKS * 256 + threadIdx.x;
+  const f32x4* const p = reinterpret_cast<const f32x4*>(a.parts) + slot * a.shares * N + i;
+  f32x4 sum = p[0];
+  for (int c = 1; c < cuts; ++c) sum += p[static_cast<int64_t>(c) * N];
+  const bool keys = i < kTrainTile * DK / 4;
+  if (!keys) i -= kTrainTile * DK / 4;
+  const int lane = i & 63, part = i >> 6, width = (keys ? DK : DV) / 8;   // parts of a wave's 32 keys
+  const int at = static_cast<int>(slot % tiles) * kTrainTile + part / width * 32 + (lane & 31);
+  const int col = part % width * 8 + (lane >> 5) * 4;
+  if (at >= a.n_pad || col >= (keys ? a.dk : a.dv)) return;
+  const int key = a.order[static_cast<int64_t>(r) * a.n_pad + at];
+  if (keys) sum *= a.scale;
+  *reinterpret_cast<bf16x4*>(place(keys ? a.dk_ : a.dv_, r, key, kvh) + col) = __builtin_convertvector(sum, bf16x4);
+}
+
 template <int DK, int DV, int BN, int QW, bool VLDS, int OCC, bool CAP>
 hipError_t launch_shape(const TrainLaunch& a, hipStream_t s) {
   using K = KeyShape<DK, DV, QW, VLDS>;
-  constexpr int waves = kTrainTile / 32, lds = 2 * (BN * (DK + DV) * 2 + kTrainBlock * 4);
-  hipError_t e = allow_lds<train_dq_kernel<DK, DV, BN, waves, CAP>>(lds);
+  constexpr bool GLDS = DK == 192;
+  constexpr int waves = kTrainTile / 32, lds = 2 * (BN * (DK + DV) * 2 + kTrainBlock * 4) + (GLDS ? kTrainTile * DV * 2 : 0);
+  hipError_t e = allow_lds<train_dq_kernel<DK, DV, BN, waves, GLDS, CAP>>(lds);
   if (e == hipSuccess) e = allow_lds<train_dkv_kernel<DK, DV, QW, VLDS, OCC, CAP>>(K::LDS);
   if (e != hipSuccess) return e;
   const int64_t tiles = (a.n_pad + kTrainTile - 1) / kTrainTile;
-  train_dkv_kernel<DK, DV, QW, VLDS, OCC, CAP><<<dim3(static_cast<unsigned>(a.n * a.kv_heads * tiles)), dim3(64 * K::WAVES), K::LDS, s>>>(a);
+  train_dkv_kernel<DK, DV, QW, VLDS, OCC, CAP>
+      <<<dim3(static_cast<unsigned>(a.n * a.kv_heads * tiles * a.shares)), dim3(64 * K::WAVES), K::LDS, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  train_dq_kernel<DK, DV, BN, waves, CAP><<<dim3(static_cast<unsigned>(a.n * a.heads * tiles)), dim3(64 * waves), lds, s>>>(a);
+  if (a.shares > 1) {
+    constexpr int blocks = kTrainTile * (DK + DV) / 4 / 256;
+    train_join_kernel<DK, DV><<<dim3(static_cast<unsigned>(a.n * a.kv_heads * tiles * blocks)), dim3(256), 0, s>>>(a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  train_dq_kernel<DK, DV, BN, waves, GLDS, CAP><<<dim3(static_cast<unsigned>(a.n * a.heads * tiles)), dim3(64 * waves), lds, s>>>(a);
   return hipGetLastError();
 }
 
@@ -422,10 +494,12 @@ hipError_t launch_cap(const TrainLaunch& a, hipStream_t s) {
 hipError_t launch_train_back(const TrainLaunch& a, hipStream_t s) {
   hipError_t e = launch_train_scan(a, true, s);
   if (e != hipSuccess) return e;
-  if (a.dk <= 64 && a.dv <= 64) return launch_cap<64, 64, 64, 2, false, 2>(a, s);
-  if (a.dk <= 128 && a.dv <= 128) return launch_cap<128, 128, 64, QW_, true, 2>(a, s);
-  if (a.dk <= 192 && a.dv <= 128) return launch_cap<192, 128, 32, 1, true, 1>(a, s);
-  return launch_cap<256, 256, 32, 1, true, 1>(a, s);
+  switch (head_shape(a.dk, a.dv).dk) {
+    case 64: return launch_cap<64, 64, 64, 2, false, 2>(a, s);
+    case 128: return launch_cap<128, 128, 64, 2, true, 2>(a, s);
+    case 192: return launch_cap<192, 128, 32, 1, true, 1>(a, s);
+    default: return launch_cap<256, 256, 32, 1, true, 1>(a, s);
+  }
 }
 
 }  // namespace ll

@@ -2,6 +2,7 @@
 // the layout of the workspace and the launches of its kernels.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/leyline_train.h"
@@ -15,6 +16,11 @@ using namespace ll;
 namespace {
 
 constexpr int64_t kMaxStride = int64_t{1} << 40;
+// Tiles of keys from which on none is cut (with 512 of them, half the chip's work each
+// round: 2 x 4096 tokens of 8 KV heads cut by evictions 908 us whole, 867 with every tile
+// in two; 4001 tokens of an MLA model, uncut, 714 and 765; 0.8 of a tile is between), and
+// blocks of queries that a share has at least.
+constexpr int64_t kTrainUnits = 640, kTrainChunk = 6;
 
 ll_status check_sizes(const kvs_attend_desc* d) {
   if (d->n < 0) return fail(LL_EINVAL, "n must not be negative");
@@ -83,6 +89,10 @@ int64_t lay_out(TrainLaunch* a, bool backward, char* at) {
     a->odd_do = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
     a->delta = reinterpret_cast<float*>(take(int64_t{a->n} * a->heads * a->n_pad * 4));
     a->ref = reinterpret_cast<float*>(take(int64_t{a->n} * a->heads * a->n_pad * 4));
+    const int64_t units = int64_t{a->n} * a->kv_heads * ceil_div(a->n_pad, kTrainTile);
+    const HeadShape w = head_shape(a->dk, a->dv);
+    a->used = reinterpret_cast<int32_t*>(take(units * 4));
+    a->parts = reinterpret_cast<float*>(take(a->shares > 1 ? units * a->shares * kTrainTile * (w.dk + w.dv) * 4 : 0));
   }
   return size;
 }
@@ -99,6 +109,12 @@ TrainLaunch sizes(const kvs_attend_desc* d) {
   a.epochs = static_cast<int32_t>(ceil_div(d->n_pad, a.epoch));
   a.dk = d->key_dim;
   a.dv = d->value_dim;
+  // A tile of keys that many queries see takes long: with few tiles the longest are cut,
+  // so that they take no longer than the rest together.
+  const int64_t units = std::max<int64_t>(1, int64_t{a.n} * a.kv_heads * ceil_div(a.n_pad, kTrainTile));
+  const int64_t most = int64_t{a.group} * a.blocks;   // blocks of queries that a tile of keys goes along
+  a.chunk = static_cast<int32_t>(std::clamp(ceil_div(most * units, kTrainUnits), std::min(most, kTrainChunk), most));
+  a.shares = static_cast<int32_t>(ceil_div(most, a.chunk));
   return a;
 }
 

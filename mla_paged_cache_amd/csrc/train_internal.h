@@ -31,6 +31,17 @@ struct KeyBlock {
   int32_t last;
 };
 
+// The widths of the kernels' tiles that hold heads of dk and dv values.
+struct HeadShape {
+  int32_t dk, dv;
+};
+inline HeadShape head_shape(int32_t dk, int32_t dv) {
+  if (dk <= 64 && dv <= 64) return HeadShape{64, 64};
+  if (dk <= 128 && dv <= 128) return HeadShape{128, 128};
+  if (dk <= 192 && dv <= 128) return HeadShape{192, 128};
+  return HeadShape{256, 256};
+}
+
 // A key of an epoch's list, and its death time (at most n_pad); places behind the last
 // key up to a multiple of kTrainBlock hold key 0 and -1.
 struct KeyEntry {
@@ -48,6 +59,8 @@ struct TrainLaunch {
   Heads q, k, v, out, dout, dq, dk_, dv_;
   float* lse;                    // [n][n_pad][heads]
   int32_t epoch, epochs;         // length of an epoch, and how many there are
+  int32_t shares, chunk;         // backward: workgroups that a tile of keys may be cut over, each of which takes
+                                 // `chunk` blocks of queries
   // workspace
   KeyBlock* keys;                // [n][blocks]
   KeyEntry* list;                // [n][list_keys]: epoch e's at list_at(e), which holds up to e * epoch keys
@@ -62,6 +75,9 @@ struct TrainLaunch {
   uint32_t* odd_do;
   float* delta;                  // [n][heads][n_pad]: sum of dout * out
   float* ref;                    // [n][heads][n_pad]: lse in base 2; infinity where there is no weight
+
+  int32_t* used;                 // [n * kv_heads * tiles]: shares that a tile of keys was cut into
+  float* parts;                  // [n * kv_heads * tiles][shares]: their sums
 
   __host__ __device__ int64_t list_at(int64_t e) const { return e * (e - 1) / 2 * epoch; }
   __host__ __device__ int64_t list_keys() const { return list_at(epochs); }
