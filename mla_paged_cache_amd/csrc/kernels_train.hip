@@ -112,18 +112,34 @@ __device__ void list_keys(const TrainLaunch& a, int r, int e, uint32_t (*totals)
     int32_t* const order = a.order + static_cast<int64_t>(r) * a.n_pad;
     // those before: they die after this epoch (for the last place: all that are seen)
     const int after = e == a.epochs ? 0 : end;
+    __shared__ int64_t pairs[kScanWaves];
     int before = 0;
+    int64_t sees = 0;
     for (int k = threadIdx.x; k < a.n_pad; k += kScanThreads) {
       const int d = min(death[k], a.n_pad);
       before += d > k && d > after;
+      sees += max(d - k, 0);
     }
-    for (int x = 32; x >= 1; x >>= 1) before += __shfl_xor(before, x);
-    if (lane == 0) totals[0][wave] = before;
+    for (int x = 32; x >= 1; x >>= 1) {
+      before += __shfl_xor(before, x);
+      sees += __shfl_xor(sees, x);
+    }
+    if (lane == 0) {
+      totals[0][wave] = before;
+      pairs[wave] = sees;
+    }
     __syncthreads();
     Picked p;
-    for (int x = 0; x < kScanWaves; ++x) p.count += totals[0][x];
+    sees = 0;
+    for (int x = 0; x < kScanWaves; ++x) {
+      p.count += totals[0][x];
+      sees += pairs[x];
+    }
     __syncthreads();
-    if (e == a.epochs && threadIdx.x == 0) a.seen_keys[r] = p.count;
+    if (e == a.epochs && threadIdx.x == 0) {
+      a.seen_keys[r] = p.count;
+      a.work[r] = sees;
+    }
     pick_in_order(e == a.epochs ? a.n_pad : end, totals, p,
                   [&](int k, int*) {
                     const int d = min(death[k], a.n_pad);

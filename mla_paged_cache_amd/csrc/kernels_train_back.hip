@@ -226,6 +226,26 @@ struct KeyShape {
   static constexpr int LDS = VALUES + (VLDS ? kTrainTile * DV * 2 : 0);
   static_assert(QW <= 2 && SUMS <= LDS && VALUES % 256 == 0, "the second wave's sums fit where the tiles were");
 };
+
+// Blocks of 64 queries that a share of a tile of keys takes.  A tile whose keys all live
+// on goes along all queries of every head that shares them; where that is more than a
+// compute unit's part of the whole work and a quarter, tiles are cut into shares of 0.6 of
+// that part.  (2 x 4096 tokens, 8 KV heads, cut by evictions so that the longest tile is a
+// third more than the part: whole 908 us, with shares 867.  4001 tokens of an MLA model,
+// uncut, the longest as long as the part: whole 560, cut in two 605.)
+constexpr int kUnits = 256, kShareBlocks = 6;   // compute units; blocks of a share at least
+__device__ __forceinline__ int share_blocks(const TrainLaunch& a, int lane) {
+  const int most = a.blocks * a.group;
+  if (a.shares == 1) return most;
+  int64_t pairs = 0;
+  for (int r = lane; r < a.n; r += 64) pairs += a.work[r];
+  for (int x = 32; x >= 1; x >>= 1) pairs += __shfl_xor(pairs, x);
+  const float part = static_cast<float>(pairs) * a.heads / (kTrainTile * kTrainBlock * kUnits);
+  if (most <= part * 1.25f) return most;
+  const int chunk = max(max(static_cast<int>(part * 0.6f) + 1, kShareBlocks), (most + a.shares - 1) / a.shares);
+  return __builtin_amdgcn_readfirstlane(min(chunk, most));
+}
+
 template <int DK, int DV, int QW, bool VLDS, int OCC, bool CAP>
 __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_per_eu(OCC))) void train_dkv_kernel(TrainLaunch a) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -238,9 +258,12 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
   const int kw = wave % S::KW, qw = wave / S::KW;
   const int pairs = a.n * a.kv_heads, pair = blockIdx.x % pairs;
   const int r = pair / a.kv_heads, kvh = pair % a.kv_heads;
+  // (workgroups that a call does not need end before they look at anything else)
+  const int chunk = share_blocks(a, lane);
   // The longest tiles first.  A tile's later shares may be short or empty; which of them
   // comes first changes from tile to tile, since workgroups go to the chip's parts in turn.
   const int tile = blockIdx.x / pairs / a.shares, share = (blockIdx.x / pairs + tile) % a.shares;
+  if (share * chunk >= a.blocks * a.group) return;
   // places [p0, p0 + kTrainTile) of the keys' order: the first see the most queries
   const int p0 = tile * kTrainTile, place_ = p0 + kw * 32 + (lane & 31);
   const int32_t* const order = a.order + static_cast<int64_t>(r) * a.n_pad;
@@ -274,7 +297,7 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
   k1 = __builtin_amdgcn_readfirstlane(k1);
   const int64_t slot = static_cast<int64_t>(pair) * ((a.n_pad + kTrainTile - 1) / kTrainTile) + tile;
   const int t0 = k0 - k0 % kTrainBlock, blocks = last > t0 ? (last - t0 + kTrainBlock - 1) / kTrainBlock : 0;
-  const int cuts = max(1, (blocks * a.group + a.chunk - 1) / a.chunk);
+  const int cuts = max(1, (blocks * a.group + chunk - 1) / chunk);
   if (share >= cuts) return;
   const int end = there ? min(death[mine], a.n_pad) : mine;   // this lane's key is seen by queries [mine, end)
 
@@ -311,8 +334,8 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
   }
   // step i: queries [t0 + i % tiles * BN ...) of head i / tiles; this share's are
   // [begin, steps)
-  const int per = kTrainBlock / BN, tiles = blocks * per, begin = share * a.chunk * per;
-  const int steps = min(begin + a.chunk * per, tiles * a.group);
+  const int per = kTrainBlock / BN, tiles = blocks * per, begin = share * chunk * per;
+  const int steps = min(begin + chunk * per, tiles * a.group);
   auto load = [&](int i, int stage) {
     const lds_ptr dst = lds + stage * STAGE;
     const int h = kvh * a.group + i / tiles, row = min(t0 + i % tiles * BN + lane, a.n_pad - 1);

@@ -16,11 +16,9 @@ using namespace ll;
 namespace {
 
 constexpr int64_t kMaxStride = int64_t{1} << 40;
-// Tiles of keys from which on none is cut (with 512 of them, half the chip's work each
-// round: 2 x 4096 tokens of 8 KV heads cut by evictions 908 us whole, 867 with every tile
-// in two; 4001 tokens of an MLA model, uncut, 714 and 765; 0.8 of a tile is between), and
-// blocks of queries that a share has at least.
-constexpr int64_t kTrainUnits = 640, kTrainChunk = 6;
+// Shares of tiles of keys that the workspace has room for, where they may be cut at all,
+// and shares of one tile at most.
+constexpr int64_t kTrainParts = 2048, kTrainShares = 16;
 
 ll_status check_sizes(const kvs_attend_desc* d) {
   if (d->n < 0) return fail(LL_EINVAL, "n must not be negative");
@@ -84,6 +82,7 @@ int64_t lay_out(TrainLaunch* a, bool backward, char* at) {
   if (backward) {
     a->order = reinterpret_cast<int32_t*>(take(int64_t{a->n} * a->n_pad * 4));
     a->seen_keys = reinterpret_cast<int32_t*>(take(int64_t{a->n} * 4));
+    a->work = reinterpret_cast<int64_t*>(take(int64_t{a->n} * 8));
     a->odd_k = reinterpret_cast<uint32_t*>(take(nb * a->kv_heads * 4));
     a->odd_q = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
     a->odd_do = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
@@ -109,12 +108,10 @@ TrainLaunch sizes(const kvs_attend_desc* d) {
   a.epochs = static_cast<int32_t>(ceil_div(d->n_pad, a.epoch));
   a.dk = d->key_dim;
   a.dv = d->value_dim;
-  // A tile of keys that many queries see takes long: with few tiles the longest are cut,
-  // so that they take no longer than the rest together.
+  // A tile of keys that many queries see takes long: with few tiles the longest may be
+  // cut (see share_blocks), as far as there is room for the shares' sums.
   const int64_t units = std::max<int64_t>(1, int64_t{a.n} * a.kv_heads * ceil_div(a.n_pad, kTrainTile));
-  const int64_t most = int64_t{a.group} * a.blocks;   // blocks of queries that a tile of keys goes along
-  a.chunk = static_cast<int32_t>(std::clamp(ceil_div(most * units, kTrainUnits), std::min(most, kTrainChunk), most));
-  a.shares = static_cast<int32_t>(ceil_div(most, a.chunk));
+  a.shares = static_cast<int32_t>(std::clamp<int64_t>(kTrainParts / units, 1, kTrainShares));
   return a;
 }
 

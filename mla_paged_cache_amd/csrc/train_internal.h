@@ -59,8 +59,7 @@ struct TrainLaunch {
   Heads q, k, v, out, dout, dq, dk_, dv_;
   float* lse;                    // [n][n_pad][heads]
   int32_t epoch, epochs;         // length of an epoch, and how many there are
-  int32_t shares, chunk;         // backward: workgroups that a tile of keys may be cut over, each of which takes
-                                 // `chunk` blocks of queries
+  int32_t shares;                // backward: workgroups that a tile of keys may be cut over
   // workspace
   KeyBlock* keys;                // [n][blocks]
   KeyEntry* list;                // [n][list_keys]: epoch e's at list_at(e), which holds up to e * epoch keys
@@ -69,6 +68,7 @@ struct TrainLaunch {
   int32_t* order;                // [n][n_pad]: backward, the keys by the epoch that they die in, the last first, and
                                  // then by place; those that nobody sees behind them
   int32_t* seen_keys;            // [n]: how many are seen
+  int64_t* work;                 // [n]: pairs of a query and a key that it sees
   uint32_t* odd_k;               // [n][kv_heads][blocks]: whether a key that is seen holds a value that is not finite;
   uint32_t* odd_v;               // the same of v
   uint32_t* odd_q;               // [n][heads][blocks]: of q and dout, any query
