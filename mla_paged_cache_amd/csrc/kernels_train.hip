@@ -254,7 +254,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
   bf16x8 q[KK];
   load_operand(q, at(a.q, r, min(mine, a.n_pad - 1), h), mine < a.n_pad, live_k, lane);
   const float c = fold_scale<CAP>(q, a.scale, a.cap);
-  const float c2 = CAP ? 1.f : c, cap2 = a.cap * kLog2e;
+  const float c2 = CAP ? 1.f : c;
+  const Tanh capped(c, a.cap * kLog2e);
 
   if (live_k < KR::CH || live_v < VR::CH) {
     for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
@@ -313,11 +314,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     }
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
-      if constexpr (CAP) {
-        tanh_all(s[b], c);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] *= cap2;
-      }
+      if constexpr (CAP) tanh_all(s[b], capped);
       if (!all) {
         const uint32_t seen = seen_bits(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES), part * BN + b * 32, k0, mine, lane);
 #pragma unroll

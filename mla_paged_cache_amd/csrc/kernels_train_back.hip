@@ -95,6 +95,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
   if constexpr (!GLDS) load_operand(g, at(a.dout, r, row, h), mine < a.n_pad, live_v, lane);
   const float c = fold_scale<CAP>(q, a.scale, a.cap);
   const float c2 = CAP ? a.cap * kLog2e : c;
+  const Tanh capped(c, 1.f);
   const int64_t at_row = (static_cast<int64_t>(r) * a.heads + h) * a.n_pad + row;
   const float ref = a.ref[at_row], delta = a.delta[at_row];
 
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
       } else {
         stream<VK, AH>([&](int k) { return VR::straight(vs, b * 32, k); }, [&](int k, bf16x8 x) { dp = mfma(x, g[k], dp); });
       }
-      if constexpr (CAP) tanh_all(s, c);
+      if constexpr (CAP) tanh_all(s, capped);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float slope = CAP ? 1.f - s[i] * s[i] : 1.f;
@@ -306,6 +307,7 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
   if constexpr (!VLDS) load_operand(v, at(a.v, r, mine, kvh), there, live_v, lane);
   const float c = fold_scale<CAP>(k, a.scale, a.cap);
   const float c2 = CAP ? a.cap * kLog2e : c;
+  const Tanh capped(c, 1.f);
   if ((VLDS && p0 + kTrainTile > some) || live_k < QR::CH || live_v < GR::CH) {   // (V's places of keys that nobody sees stay 0)
     for (int i = threadIdx.x; i < S::LDS / 16; i += 64 * WAVES) reinterpret_cast<chunk_t*>(smem)[i] = chunk_t{0u, 0u, 0u, 0u};
     __syncthreads();
@@ -379,7 +381,7 @@ __global__ __launch_bounds__(2 * kTrainTile * QW) __attribute__((amdgpu_waves_pe
     } else {
       stream<VK, AH>([&](int x) { return GR::straight(ga, 0, x); }, [&](int x, bf16x8 y) { dp = mfma(y, v[x], dp); });
     }
-    if constexpr (CAP) tanh_all(s, c);
+    if constexpr (CAP) tanh_all(s, capped);
 #pragma unroll
     for (int x = 0; x < 16; x += 4) {
       const f32x4 ref = ls[product_row(x, lane) / 4], delta = ls[BN / 4 + product_row(x, lane) / 4];

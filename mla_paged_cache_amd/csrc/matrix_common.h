@@ -212,20 +212,44 @@ __device__ __forceinline__ void stream(Read&& read, Use&& use) {
   }
 }
 
-// tanh of each product times c: all of a wave's in the short form where that holds.
-__device__ __forceinline__ void tanh_all(f32x16& s, float c) {
+// by * tanh(c * s) of products s, without a multiplication by c or by: the polynomial's
+// coefficients hold them, for c of a size where its powers do.
+struct Tanh {
+  float k[5];                    // s * sum k_i (s^2)^i
+  float most;                    // |s| up to which that holds (-1: c is outside [2^-12, 2^12])
+  float c, by;
+  __device__ __forceinline__ Tanh(float c_, float by_) : c(c_), by(by_) {
+    const float w = c * c;
+    const float b[5] = {0.99999999f, -0.33333072f, 0.13324829f, -0.052989241f, 0.017141319f};
+    float x = c * by;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      k[i] = b[i] * x;
+      x *= w;
+    }
+    most = fabsf(c) >= 0x1p-12f && fabsf(c) <= 0x1p12f ? 0.5f / fabsf(c) : -1.f;
+  }
+  __device__ __forceinline__ float slope(float s) const {   // of the chord from 0
+    const float w = s * s;
+    float p = __builtin_fmaf(k[4], w, k[3]);
+    p = __builtin_fmaf(p, w, k[2]);
+    p = __builtin_fmaf(p, w, k[1]);
+    return __builtin_fmaf(p, w, k[0]);
+  }
+  __device__ __forceinline__ float small(float s) const { return slope(s) * s; }
+};
+// All of a wave's products in the short form where that holds (a NaN takes either: both
+// give NaN).
+__device__ __forceinline__ void tanh_all(f32x16& s, const Tanh& f) {
   float most = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    s[i] *= c;
-    most = fmaxf(most, fabsf(s[i]));
-  }
-  if (__any(most > 0.5f)) {
+  for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(s[i]));
+  if (__any(most > f.most)) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = tanh_any(s[i]);
+    for (int i = 0; i < 16; ++i) s[i] = f.by * tanh_any(s[i] * f.c);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = tanh_small(s[i]);
+    for (int i = 0; i < 16; ++i) s[i] = f.small(s[i]);
   }
 }
 

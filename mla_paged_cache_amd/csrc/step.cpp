@@ -203,6 +203,7 @@ ll_status ll_step_create(ll_pool* p, const ll_step_desc* d, ll_step** out) try {
   s->d_theta = reinterpret_cast<double*>(s->d_buf + o_theta);
   s->d_part_o = reinterpret_cast<float*>(s->d_buf + o_po);
   s->d_part_ml = reinterpret_cast<float*>(s->d_buf + o_ml);
+  s->part_values = static_cast<int64_t>(part_rows) * s->value_dim;
   const ll::StepCounts none{};
   hipError_t e = hipMemcpy(s->d_theta, p->theta.data(), pairs * sizeof(double), hipMemcpyHostToDevice);
   for (const Plan& x : s->plans)

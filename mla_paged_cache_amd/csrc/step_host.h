@@ -43,6 +43,7 @@ struct ll_step {
   double* d_theta = nullptr;
   float* d_part_o = nullptr;
   float* d_part_ml = nullptr;
+  int64_t part_values = 0;       // room in d_part_o
   // the step begun last
   bool begun = false;
   std::vector<int32_t> seqs;

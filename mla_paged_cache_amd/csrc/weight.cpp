@@ -86,6 +86,8 @@ ll_status ll_step_weigh(ll_step* s, const ll_weigh_desc* d, void* stream) try {
   a.lse = d->lse;
   a.weights = d->weights;
   a.weight_stride = d->weight_stride;
+  a.parts = s->d_part_o;
+  a.part_values = s->part_values;
   if ((rc = start(s, st, capturing))) return rc;
   hipError_t e = ll::launch_weigh(a, p->gqa, st);
   if (e != hipSuccess) return ll::pool_device_fail(p, e, "weigh_kernel launch");

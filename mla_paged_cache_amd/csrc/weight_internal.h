@@ -35,6 +35,9 @@ struct WeighLaunch {
   const float* lse;              // [tokens][heads]
   float* weights;                // [page-table rows][stride]
   int64_t weight_stride;
+  int32_t shares;                // workgroups that a tile of rows is cut over, set by the launch
+  float* parts;                  // [shares][n_seqs][max_rows]: their sums, which a second kernel adds up
+  int64_t part_values;           // room there
 };
 
 // One sequence's selection.
