@@ -3,10 +3,12 @@
 // to the earlier row, as keep bytes; their weights moved together.
 //
 // One workgroup takes one sequence.  The weight that the last kept row has is found
-// digit by digit, eight bits at a time from the top, by counting the rows of each
+// digit by digit, eleven bits at a time from the top, by counting the rows of each
 // digit among those that match so far; a last pass then keeps what is above it and,
-// in row order, as many equal ones as there is room for.
-#include "device_common.h"
+// in row order, as many equal ones as there is room for.  Up to kKeepRows rows the
+// weights are read once and stay in LDS; what is left is the passes' barriers and LDS
+// (ONE_NEW us for 4097 rows, BATCH_KEEP for 96 sequences of up to 32768 rows).
+#include "matrix_common.h"
 #include "weight_internal.h"
 
 namespace ll {
@@ -14,7 +16,9 @@ namespace {
 
 constexpr int kKeepThreads = 1024;
 constexpr int kKeepWaves = kKeepThreads / 64;
-constexpr int kKeepRows = 8;                             // rows a thread takes at a time
+constexpr int kKeepBits = 11, kKeepBins = 1 << kKeepBits;
+constexpr int kKeepCopies = 2;   // of the counts, against waves waiting for one another
+constexpr int kKeepRows = 35 * kKeepThreads;   // whose weights fit LDS beside the counts
 
 // Order of the weights as unsigned numbers: NaN above infinity, -0 as 0.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -23,6 +27,8 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
+// RESIDENT: the weights lie in LDS.
+template <bool RESIDENT>
 __global__ __launch_bounds__(kKeepThreads) void keep_kernel(KeepLaunch a) {
   const KeepSeq q = a.seqs[blockIdx.x];
   const int n = static_cast<int>(q.rows), tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -34,64 +40,100 @@ __global__ __launch_bounds__(kKeepThreads) void keep_kernel(KeepLaunch a) {
   const int hi = max(lo, n - static_cast<int>(min(a.recent, q.rows)));
   const int need = min(static_cast<int>(q.budget) - lo - (n - hi), hi - lo);   // of them to keep, >= 0
 
-  __shared__ uint32_t bins[kKeepWaves][256];
-  __shared__ uint32_t found[2];
-  __shared__ uint32_t totals[2][kKeepWaves][2];
+  __shared__ uint32_t bins[kKeepCopies][kKeepBins];
+  __shared__ uint32_t found[2], sums[kKeepWaves];
+  __shared__ int totals[2][kKeepWaves][2];
+  extern __shared__ float held[];
+  if (RESIDENT) {   // all on their way at once
+    for (int i = wave * 64; i < n; i += kKeepThreads)
+      if (i + lane < n) load_lds4((lds_ptr)held + i * 4, w + i + lane);
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // (a thread's own ones, before a barrier)
+  }
+  auto weight = [&](int i) { return RESIDENT ? held[i] : w[i]; };
+
   uint32_t edge = 0, mask = 0;   // the digits found so far
   int left = need;               // rows to keep among those that match them
-  for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-    for (int i = tid; i < kKeepWaves * 256; i += kKeepThreads) (&bins[0][0])[i] = 0;
+  // (whoever keeps every row to choose from, or none, needs no edge)
+  for (int shift = 32 - kKeepBits; need > 0 && need < hi - lo; shift = max(0, shift - kKeepBits)) {
+    for (int i = tid; i < kKeepCopies * kKeepBins / 4; i += kKeepThreads) reinterpret_cast<chunk_t*>(bins)[i] = chunk_t{0u, 0u, 0u, 0u};
     __syncthreads();
-    for (int i = lo + tid; i < hi; i += kKeepThreads) {
-      const uint32_t k = order_of(w[i]);
-      if ((k & mask) == edge) atomicAdd(&bins[wave][k >> shift & 255], 1u);
+#pragma unroll 8
+    for (int i = tid; i < hi; i += kKeepThreads) {
+      const uint32_t k = order_of(weight(i));
+      if (i >= lo && (k & mask) == edge) atomicAdd(&bins[wave % kKeepCopies][k >> shift & (kKeepBins - 1)], 1u);
     }
     __syncthreads();
-    uint32_t sum = 0;
-    if (tid < 256)
-      for (int x = 0; x < kKeepWaves; ++x) sum += bins[x][tid];
-    __syncthreads();
-    if (tid < 256) bins[0][tid] = sum;
-    __syncthreads();
-    if (tid < 256) {
-      uint32_t above = 0;
-      for (int x = tid + 1; x < 256; ++x) above += bins[0][x];
-      if (above < static_cast<uint32_t>(left) && above + sum >= static_cast<uint32_t>(left)) {
-        found[0] = tid;
-        found[1] = left - above;
-      }
-    }
-    __syncthreads();
-    edge |= found[0] << shift;
-    mask |= 255u << shift;
-    left = static_cast<int>(found[1]);
-    __syncthreads();
-  }
-
-  // rows above the edge, and the first `left` that equal it
-  int over = 0, ties = 0;        // of the chunks before this one
-  int at = 0;
-  for (int base = 0; base < n; base += kKeepThreads * kKeepRows, at ^= 1) {
-    float v[kKeepRows];
-    uint64_t is_over[kKeepRows], is_tie[kKeepRows];
-    int my_over = 0, my_ties = 0;   // the wave's
+    // two digits a thread; how many rows lie above them
+    uint32_t one = 0, two = 0;
 #pragma unroll
-    for (int e = 0; e < kKeepRows; ++e) {
-      const int i = base + (wave * kKeepRows + e) * 64 + lane;
-      v[e] = i < n ? w[i] : 0.f;
-      const uint32_t k = order_of(v[e]);
-      const bool inner = i >= lo && i < hi;
-      is_over[e] = __ballot(i < n && (!inner || (need > 0 && k > edge)));
-      is_tie[e] = __ballot(inner && need > 0 && k == edge);
-      my_over += __popcll(is_over[e]);
-      my_ties += __popcll(is_tie[e]);
+    for (int c = 0; c < kKeepCopies; ++c) {
+      one += bins[c][2 * tid];
+      two += bins[c][2 * tid + 1];
     }
+    uint32_t up = one + two;   // of this lane and those after it
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t x = __shfl_down(up, d);
+      if (lane + d < 64) up += x;
+    }
+    if (lane == 0) sums[wave] = up;
+    __syncthreads();
+    uint32_t above = up - one - two;
+    for (int x = wave + 1; x < kKeepWaves; ++x) above += sums[x];
+    const uint32_t room = static_cast<uint32_t>(left);
+    if (above < room && above + two >= room) {
+      found[0] = 2 * tid + 1;
+      found[1] = room - above;
+    } else if (above + two < room && above + two + one >= room) {
+      found[0] = 2 * tid;
+      found[1] = room - above - two;
+    }
+    __syncthreads();
+    edge |= found[0] << shift;     // (the last digit covers bits that an earlier one has found: they are the same)
+    mask |= (kKeepBins - 1u) << shift;
+    left = static_cast<int>(found[1]);
+    if (shift == 0) break;
+  }
+  const bool every = need > 0 && need == hi - lo;
+
+  // Rows above the edge, and the first `left` that equal it: of 64 rows at a time as bits.
+  // As numbers: above is whatever is not at or below the edge, NaN with it; where the edge
+  // is NaN nothing is above, and NaN equals it.
+  const bool odd = edge == 0xFFFFFFFFu;
+  const float limit = __uint_as_float(edge & 0x80000000u ? edge ^ 0x80000000u : ~edge);
+  const bool some = need > 0 && !every;
+  auto look = [&](int i0, float x, uint64_t* overs, uint64_t* tied) {   // rows i0 + lane
+    uint64_t o = __ballot(!(x <= limit)), t = __ballot(x == limit);
+    if (odd) t = o & __ballot(x != x), o = 0;
+    if (!some) t = 0, o = every ? ~uint64_t{0} : 0;
+    if (i0 < lo || i0 + 64 > hi) {   // rows that are kept whatever they hold, and places behind the last row
+      const uint64_t inner = __ballot(i0 + lane >= lo && i0 + lane < hi), there = __ballot(i0 + lane < n);
+      o = ((o & inner) | ~inner) & there;
+      t &= inner;
+    }
+    *overs = o;
+    *tied = t;
+  };
+  const uint64_t before = (uint64_t{1} << lane) - 1;
+  int over = 0, ties = 0;   // of all waves so far
+  int o = 0, t = 0;         // of this wave's rows so far, and those before them
+  auto put = [&](int i0, float x) {
+    uint64_t overs, tied;
+    look(i0, x, &overs, &tied);
+    const int i = i0 + lane, rank = t + __popcll(tied & before);
+    const bool mine = (overs >> lane & 1) || ((tied >> lane & 1) && rank < left);
+    if (i < n) keep[i] = mine;
+    if (mine && out) out[o + __popcll(overs & before) + min(rank, left)] = x;
+    o += __popcll(overs);
+    t += __popcll(tied);
+  };
+  auto share = [&](int my_over, int my_ties, int at) {   // where this wave's rows begin
     if (lane == 0) {
       totals[at][wave][0] = my_over;
       totals[at][wave][1] = my_ties;
     }
     __syncthreads();   // (also: every weight of the chunk is read before any is written)
-    int o = over, t = ties;
+    o = over, t = ties;
     for (int x = 0; x < kKeepWaves; ++x) {
       if (x < wave) {
         o += totals[at][x][0];
@@ -100,16 +142,46 @@ __global__ __launch_bounds__(kKeepThreads) void keep_kernel(KeepLaunch a) {
       over += totals[at][x][0];
       ties += totals[at][x][1];
     }
-    const uint64_t before = (uint64_t{1} << lane) - 1;
+  };
+  if constexpr (RESIDENT) {
+    // each wave takes one run of rows
+    const int run = ((n + kKeepWaves - 1) / kKeepWaves + 63) / 64 * 64, first = wave * run, last = min(first + run, n);
+    int my_over = 0, my_ties = 0;
+    __syncthreads();   // all weights are in LDS
+    auto read = [&](int i0) { return held[min(i0 + lane, n - 1)]; };
+#pragma unroll 4
+    for (int i = first; i < last; i += 64) {
+      uint64_t overs, tied;
+      look(i, read(i), &overs, &tied);
+      my_over += __popcll(overs);
+      my_ties += __popcll(tied);
+    }
+    share(my_over, my_ties, 0);
+#pragma unroll 4
+    for (int i = first; i < last; i += 64) put(i, read(i));
+  } else {
+    // chunks of rows in registers, of which each wave has a run: weights that move within
+    // their buffer only reach rows that have been read
+    constexpr int E = 8;
+    int at = 0;
+    for (int base = 0; base < n; base += kKeepThreads * E, at ^= 1) {
+      float v[E];
+      int my_over = 0, my_ties = 0;
 #pragma unroll
-    for (int e = 0; e < kKeepRows; ++e) {
-      const int i = base + (wave * kKeepRows + e) * 64 + lane;
-      const int rank = t + __popcll(is_tie[e] & before);
-      const bool mine = (is_over[e] >> lane & 1) || ((is_tie[e] >> lane & 1) && rank < left);
-      if (i < n) keep[i] = mine;
-      if (mine && out) out[o + __popcll(is_over[e] & before) + min(rank, left)] = v[e];
-      o += __popcll(is_over[e]);
-      t += __popcll(is_tie[e]);
+      for (int e = 0; e < E; ++e) {
+        const int i = base + (wave * E + e) * 64 + lane;
+        v[e] = i < n ? w[i] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        uint64_t overs, tied;
+        look(base + (wave * E + e) * 64, v[e], &overs, &tied);
+        my_over += __popcll(overs);
+        my_ties += __popcll(tied);
+      }
+      share(my_over, my_ties, at);
+#pragma unroll
+      for (int e = 0; e < E; ++e) put(base + (wave * E + e) * 64, v[e]);
     }
   }
   if (out) {
@@ -120,8 +192,16 @@ __global__ __launch_bounds__(kKeepThreads) void keep_kernel(KeepLaunch a) {
 
 }  // namespace
 
+// The longest sequence of a launch comes first.
 hipError_t launch_keep(const KeepLaunch& a, int n, hipStream_t s) {
-  keep_kernel<<<dim3(static_cast<unsigned>(n)), dim3(kKeepThreads), 0, s>>>(a);
+  const dim3 g(static_cast<unsigned>(n)), b(kKeepThreads);
+  const int64_t rows = a.seqs[0].rows;
+  if (rows <= kKeepRows) {
+    if (const hipError_t e = allow_lds<keep_kernel<true>>(kKeepRows * 4); e != hipSuccess) return e;
+    keep_kernel<true><<<g, b, static_cast<size_t>(rows) * 4, s>>>(a);
+  } else {
+    keep_kernel<false><<<g, b, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
