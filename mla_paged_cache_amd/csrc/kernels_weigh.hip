@@ -75,7 +75,7 @@ __global__ __launch_bounds__(64 * kWeighWaves) __attribute__((amdgpu_waves_per_e
     // A head's keys come from memory in whole rows (256 bytes of 4 rows an instruction, 128
     // of 8 at a row's end) and change lanes through LDS, 128 values of each row at a time;
     // a lane's operands straight from memory, 32 bytes of 32 rows an instruction, took 384
-    // us instead of BATCH_NEW (64 tokens over up to 16384 rows of 8 heads of 128).  MLA rows
+    // us instead of 289 (64 tokens over up to 16384 rows of 8 heads of 128).  MLA rows
     // are their own operands' length, and the way through LDS costs more than it gives
     // (64 tokens over up to 32768 rows: 606 us, 360 without).
     bf16x8 k[KB][KK], next[KB][KK];
@@ -133,11 +133,8 @@ __global__ __launch_bounds__(64 * kWeighWaves) __attribute__((amdgpu_waves_per_e
         }
       }
     };
-    const int first = static_cast<int>(unit / a.shares % a.kv_heads);
-    auto head_of = [&](int i) { return (i / per + first) % a.kv_heads; };
-    // Step i: query rows [r0 + i % per * 32 ...) of a KV head, the first of which differs from
-    // workgroup to workgroup: the same head's keys all lie in a few of the memory's channels
-    // (64 tokens over up to 16384 rows of 8 heads: HEADS_NEW us so, 371 all from head 0).  Lane x of a half wave
+    auto head_of = [&](int i) { return i / per; };
+    // Step i: query rows [r0 + i % per * 32 ...) of KV head i / per.  Lane x of a half wave
     // knows row x, token `tok` and head `head` of the KV head's group; rows past the last one
     // repeat it and are seen by nothing.
     float ref = 0.f;
