@@ -57,7 +57,8 @@ typedef struct {
 
 /* Bytes of workspace that kvs_attend (backward = 0) or kvs_attend_backward (1) needs
  * for this n, n_pad, heads, kv_heads, key_dim and value_dim (the rest of desc is not
- * read).  Errors: LL_EINVAL. */
+ * read): for a longer n_pad never less.  Errors: LL_EINVAL, LL_EUNSUPPORTED (as
+ * kvs_attend). */
 ll_status kvs_attend_workspace(const kvs_attend_desc* desc, int32_t backward, int64_t* bytes);
 
 /* out[q][h] = sum_k p_k v_k and lse[q][h] = log sum_k exp s_k over the keys that
@@ -72,7 +73,8 @@ ll_status kvs_attend(kvs_ctx* ctx, const kvs_attend_desc* desc, void* stream);
 /* The gradients of kvs_attend: with dout the gradient of out (lse has none),
  *   delta = sum_d dout out,  ds = p (dout . v - delta) scale (1 - tanh^2),
  *   dv = sum_q p dout,  dk = sum_q ds q,  dq = sum_k ds k,
- * dk and dv summed over the heads that share a KV head.  out and lse are those that
+ * dk and dv summed over the heads that share a KV head.  delta is what sum_k p dout . v
+ * gives (the same but for the rounding of out, which only a first guess is taken from).  out and lse are those that
  * kvs_attend gave for the same inputs.  dq, dk and dv are written whole (zeros where
  * nothing is seen) and may not overlap anything else.  Errors: as kvs_attend. */
 typedef struct {

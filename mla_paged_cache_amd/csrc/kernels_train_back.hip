@@ -5,10 +5,21 @@
 // dk and dv summed over the heads that share a KV head.  Weights are worked out again
 // from lse; one kernel goes along the keys of a query for dq, another along the queries
 // of a key for dk and dv, so that each sum has one owner and one order.
+//
+// The out that comes is rounded to bf16, and delta from it is off by as much; where few
+// keys hold a query's weight, dout . v - delta cancels, and that error is what is left.
+// Since the weights sum to 1, sum_k p (dout . v - delta) is what delta lacks: the dq
+// kernel adds that sum, and dk and dv are worked out with the delta that it corrected;
+// where it matters for dq, a workgroup goes along its keys a second time.  ds and p are
+// rounded to bf16 for the products after them, half a step (2^-8) of each.
 #include "train_common.h"
 
 namespace ll {
 namespace {
+
+// Of the 2-norm of dq, what may be missing for delta's sake: less than the rounding of ds
+// makes it differ by (0.0017).
+constexpr float kLacks = 0.001f;
 
 constexpr int AH = 3;   // steps that a product's operands are read ahead (5: 2% slower)
 
@@ -31,16 +42,25 @@ __device__ void train_dq_row(const TrainLaunch& a, int r, int q, int h, int lane
   const int32_t* const death = a.death + static_cast<int64_t>(r) * a.n_pad;
   const Vals x = load8(at(a.q, r, q, h) + lane * 8, lk), g = load8(at(a.dout, r, q, h) + lane * 8, lv);
   const float lse = a.lse[(static_cast<int64_t>(r) * a.n_pad + q) * a.heads + h];
-  const float delta = a.delta[(static_cast<int64_t>(r) * a.heads + h) * a.n_pad + q];
+  float* const at_delta = a.delta + (static_cast<int64_t>(r) * a.heads + h) * a.n_pad + q;
+  float delta = *at_delta, lacks = 0.f;
   Vals o{};
   if (lse != -__builtin_inff())
-    for (int k = 0; k <= q; ++k) {
-      if (death[k] <= q) continue;
-      const Vals y = load8(at(a.k, r, k, kvh) + lane * 8, lk);
-      const float s = wave_sum(dot8(x, y));
-      const float dp = wave_sum(dot8(g, load8(at(a.v, r, k, kvh) + lane * 8, lv)));
-      add8(o, pair_of(a, s, dp, lse, delta).ds, y);
+    for (int pass = 0; pass < 2; ++pass) {   // the sum of p (dp - delta), then of ds k
+      for (int k = 0; k <= q; ++k) {
+        if (death[k] <= q) continue;
+        const Vals y = load8(at(a.k, r, k, kvh) + lane * 8, lk);
+        const float s = wave_sum(dot8(x, y));
+        const float dp = wave_sum(dot8(g, load8(at(a.v, r, k, kvh) + lane * 8, lv)));
+        const Pair w = pair_of(a, s, dp, lse, delta);
+        if (pass == 0)
+          lacks += w.p * (dp - delta);
+        else
+          add8(o, w.ds, y);
+      }
+      if (pass == 0) delta += lacks;
     }
+  if (lane == 0) *at_delta = delta;
   if (lk) store8(place(a.dq, r, q, h) + lane * 8, o, 1.f);
 }
 
@@ -71,9 +91,16 @@ __device__ void train_dkv_row(const TrainLaunch& a, int r, int k, int kvh, int l
 // see, as the forward kernel does: S^T = K Q^T and dP^T = V dO^T with the queries in
 // registers, then dQ^T += K^T dS^T, K^T from the transposing LDS reads.
 // GLDS: dO lies in LDS, where the registers hold no more.
-template <int DK, int DV, int BN, int WAVES, bool GLDS, bool CAP>
+// FIRST: delta is from the rounded out, and is corrected; not FIRST: it is correct, and
+// those workgroups go again that need to.  (In one kernel, registers for the loop around
+// the loop are missing.)  The sums cost 12 us of 270 where they are lacks alone, 110 with
+// both squares over every block, 50 over every second one (4001 tokens of an MLA model,
+// capped); going again, 20 there and 16 where documents of 100 tokens are packed.
+template <int DK, int DV, int BN, int WAVES, bool GLDS, bool CAP, bool FIRST>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 192 ? 1 : 2))) void train_dq_kernel(TrainLaunch a) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int unit = blockIdx.x;
+  if (!FIRST && !a.again[unit]) return;
   using KR = Rows<DK>;
   using VR = Rows<DV>;
   constexpr int STAGE = BN * (KR::BYTES + VR::BYTES) + kTrainBlock * 4;   // keys, values, death times
@@ -118,6 +145,9 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     if (wave == 0) reinterpret_cast<int*>(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES))[lane] = key.death;   // the whole block's
   };
   f32x16 o[DB];
+  // sums of p (dp - delta), and of p's squares and its own over the blocks that are seen in
+  // part and every second one of the others
+  float lacks = 0.f, p2 = 0.f, t2 = 0.f;
 #pragma unroll
   for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -169,17 +199,25 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
         stream<VK, AH>([&](int k) { return VR::straight(vs, b * 32, k); }, [&](int k, bf16x8 x) { dp = mfma(x, g[k], dp); });
       }
       if constexpr (CAP) tanh_all(s, capped);
+      auto pairs = [&](auto plain, uint32_t seen) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float slope = CAP ? 1.f - s[i] * s[i] : 1.f;
-        const float p = exp2_(__builtin_fmaf(s[i], c2, -ref));
-        s[i] = p * (dp[i] - delta) * slope;
-      }
-      if (!all) {
-        const uint32_t seen = seen_bits(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES), part * BN + b * 32, k0, mine, lane);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!(seen >> i & 1)) s[i] = 0.f;
+        for (int i = 0; i < 16; ++i) {
+          float p = exp2_(__builtin_fmaf(s[i], c2, -ref)), t = p * (dp[i] - delta);
+          if (!plain && !(seen >> i & 1)) p = t = 0.f;
+          if (FIRST) lacks += t;
+          if (FIRST && !plain) {
+            p2 = __builtin_fmaf(p, p, p2);
+            t2 = __builtin_fmaf(t, t, t2);
+          }
+          s[i] = CAP ? t * (1.f - s[i] * s[i]) : t;
+        }
+      };
+      if (all && (!FIRST || (block & 1))) {
+        pairs(std::true_type{}, 0u);
+      } else {
+        uint32_t seen = ~0u;
+        if (!all) seen = seen_bits(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES), part * BN + b * 32, k0, mine, lane);
+        pairs(std::false_type{}, seen);
       }
       const bf16x8 ds[2] = {operand(s, 0), operand(s, 1)};
       __builtin_amdgcn_sched_barrier(0);
@@ -197,7 +235,32 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
   __builtin_amdgcn_s_waitcnt(0x0F70);   // loads on their way into LDS
   if (walk.rows_only) {
     for (int i = q0 + wave; i <= q1; i += WAVES) train_dq_row(a, r, i, h, lane);
+    if (threadIdx.x == 0) a.again[unit] = 0;
     return;
+  }
+  if constexpr (FIRST) {
+    // What delta lacks, times sum_k p k, is missing from dq = sum_k ds k: of the workgroup's
+    // rows, and keys that know nothing of each other, lacks^2 sum p^2 of sum t^2.
+    lacks += __shfl_xor(lacks, 32);
+    p2 += __shfl_xor(p2, 32);
+    t2 += __shfl_xor(t2, 32);
+    const bool weighs = mine < a.n_pad && ref < __builtin_inff();
+    if (weighs && lane < 32) a.delta[at_row] = delta + lacks;
+    float missing = weighs ? lacks * lacks * p2 : 0.f, of = weighs ? t2 : 0.f;
+    for (int x = 16; x >= 1; x >>= 1) {
+      missing += __shfl_xor(missing, x);
+      of += __shfl_xor(of, x);
+    }
+    __syncthreads();   // nobody reads the tiles any more
+    float* const sums = reinterpret_cast<float*>(smem);
+    if (lane == 0) sums[2 * wave] = missing, sums[2 * wave + 1] = of;
+    __syncthreads();
+    missing = of = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) missing += sums[2 * w], of += sums[2 * w + 1];
+    const bool again = missing > kLacks * kLacks * of;
+    if (threadIdx.x == 0) a.again[unit] = again;
+    if (again) return;
   }
   if (mine >= a.n_pad) return;
   uint16_t* const out = place(a.dq, r, mine, h);
@@ -491,10 +554,15 @@ hipError_t launch_shape(const TrainLaunch& a, hipStream_t s) {
   using K = KeyShape<DK, DV, QW, VLDS>;
   constexpr bool GLDS = DK == 192;
   constexpr int waves = kTrainTile / 32, lds = 2 * (BN * (DK + DV) * 2 + kTrainBlock * 4) + (GLDS ? kTrainTile * DV * 2 : 0);
-  hipError_t e = allow_lds<train_dq_kernel<DK, DV, BN, waves, GLDS, CAP>>(lds);
+  hipError_t e = allow_lds<train_dq_kernel<DK, DV, BN, waves, GLDS, CAP, true>>(lds);
+  if (e == hipSuccess) e = allow_lds<train_dq_kernel<DK, DV, BN, waves, GLDS, CAP, false>>(lds);
   if (e == hipSuccess) e = allow_lds<train_dkv_kernel<DK, DV, QW, VLDS, OCC, CAP>>(K::LDS);
   if (e != hipSuccess) return e;
   const int64_t tiles = (a.n_pad + kTrainTile - 1) / kTrainTile;
+  const dim3 queries(static_cast<unsigned>(a.n * a.heads * tiles));
+  train_dq_kernel<DK, DV, BN, waves, GLDS, CAP, true><<<queries, dim3(64 * waves), lds, s>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
   train_dkv_kernel<DK, DV, QW, VLDS, OCC, CAP>
       <<<dim3(static_cast<unsigned>(a.n * a.kv_heads * tiles * a.shares)), dim3(64 * K::WAVES), K::LDS, s>>>(a);
   e = hipGetLastError();
@@ -505,7 +573,7 @@ hipError_t launch_shape(const TrainLaunch& a, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  train_dq_kernel<DK, DV, BN, waves, GLDS, CAP><<<dim3(static_cast<unsigned>(a.n * a.heads * tiles)), dim3(64 * waves), lds, s>>>(a);
+  train_dq_kernel<DK, DV, BN, waves, GLDS, CAP, false><<<queries, dim3(64 * waves), lds, s>>>(a);
   return hipGetLastError();
 }
 

@@ -27,6 +27,9 @@ ll_status check_sizes(const kvs_attend_desc* d) {
     return fail(LL_EINVAL, "heads must be a positive multiple of kv_heads");
   if (d->key_dim < 8 || d->key_dim > 256 || d->key_dim % 8 || d->value_dim < 8 || d->value_dim > 256 || d->value_dim % 8)
     return fail(LL_EINVAL, "key_dim and value_dim must be multiples of 8 in [8, 256]");
+  const int64_t rows = int64_t{d->n} * d->heads, blocks = ceil_div(d->n_pad, kTrainBlock), most = int64_t{1} << 23;
+  if (rows >= most || rows * blocks >= most)
+    return fail(LL_EUNSUPPORTED, "n * heads * ceil(n_pad / 64) must stay below 2^23");
   return LL_OK;
 }
 
@@ -87,11 +90,13 @@ int64_t lay_out(TrainLaunch* a, bool backward, char* at) {
     a->odd_q = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
     a->odd_do = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
     a->delta = reinterpret_cast<float*>(take(int64_t{a->n} * a->heads * a->n_pad * 4));
+    a->again = reinterpret_cast<int32_t*>(take(int64_t{a->n} * a->heads * ceil_div(a->n_pad, kTrainTile) * 4));
     a->ref = reinterpret_cast<float*>(take(int64_t{a->n} * a->heads * a->n_pad * 4));
     const int64_t units = int64_t{a->n} * a->kv_heads * ceil_div(a->n_pad, kTrainTile);
     const HeadShape w = head_shape(a->dk, a->dv);
     a->used = reinterpret_cast<int32_t*>(take(units * 4));
-    a->parts = reinterpret_cast<float*>(take(a->shares > 1 ? units * a->shares * kTrainTile * (w.dk + w.dv) * 4 : 0));
+    // (as much room for the longest n_pad as for any shorter one, though long ones are not cut)
+    a->parts = reinterpret_cast<float*>(take(std::min(units * kTrainShares, kTrainParts) * kTrainTile * (w.dk + w.dv) * 4));
   }
   return size;
 }
@@ -120,8 +125,6 @@ ll_status fill(const kvs_attend_desc* d, bool backward, TrainLaunch* a) {
   if (rc) return rc;
   if ((rc = check_scale(d->scale, d->cap))) return rc;
   *a = sizes(d);
-  if (int64_t{a->n} * a->heads * a->blocks >= (int64_t{1} << 23))
-    return fail(LL_EUNSUPPORTED, "n * heads * ceil(n_pad / 64) must stay below 2^23");
   if (d->n == 0) return LL_OK;
   if (!d->death || (reinterpret_cast<uintptr_t>(d->death) & 3)) return fail(LL_EINVAL, "death is NULL or not 4-byte aligned");
   if ((rc = check_heads(d->q, d, d->heads, d->key_dim, false, "q"))) return rc;
