@@ -16,9 +16,7 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 struct Vals {
   float v[8];
 };
-__device__ __forceinline__ Vals load8(const uint16_t* p, bool live) {
-  chunk_t c{0u, 0u, 0u, 0u};
-  if (live) c = *reinterpret_cast<const chunk_t*>(p);
+__device__ __forceinline__ Vals vals_of(chunk_t c) {
   Vals r;
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
@@ -27,6 +25,11 @@ __device__ __forceinline__ Vals load8(const uint16_t* p, bool live) {
     r.v[2 * i + 1] = bf16_hi(w[i]);
   }
   return r;
+}
+__device__ __forceinline__ Vals load8(const uint16_t* p, bool live) {
+  chunk_t c{0u, 0u, 0u, 0u};
+  if (live) c = *reinterpret_cast<const chunk_t*>(p);
+  return vals_of(c);
 }
 __device__ __forceinline__ float dot8(const Vals& x, const Vals& y) {
   float s = 0.f;
