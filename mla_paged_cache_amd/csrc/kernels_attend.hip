@@ -6,7 +6,9 @@
 // One pass over the rows keeps m, l and the unscaled sum of v, in float32; when m
 // grows, l and the sum are scaled down.  Scores are kept in base 2 (times
 // log2 e), so that each exponential is one instruction.  With a cap,
-//   s_j = cap * tanh(scale * q . k_j / cap).
+//   s_j = cap * tanh(scale * q . k_j / cap),
+// a polynomial where a wave's scores lie below half the cap (2 x up to 1024 tokens over
+// 8192 rows, 4 KV heads, 8 of 256: 223 us without a cap, 240 with one).
 #include <atomic>
 #include <type_traits>
 

@@ -95,6 +95,9 @@ __device__ void train_dkv_row(const TrainLaunch& a, int r, int k, int kvh, int l
 // see, as the forward kernel does: S^T = K Q^T and dP^T = V dO^T with the queries in
 // registers, then dQ^T += K^T dS^T, K^T from the transposing LDS reads.
 // GLDS: dO lies in LDS, where the registers hold no more.
+// Bound by its registers: two waves a SIMD, matrix units 39% busy (2 x 4096 tokens, 8 KV
+// heads, 32 of 128, cut every 1024: 340 us; 4001 tokens of 16 heads of 192 / 128, capped:
+// 265 us, 30%).
 // FIRST: delta is from the rounded out, and is corrected; not FIRST: it is correct, and
 // those workgroups go again that need to.  (In one kernel, registers for the loop around
 // the loop are missing.)  The sums cost 12 us of 270 where they are lacks alone, 110 with
@@ -286,6 +289,9 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
 // LDS, of which a wave takes 32: S = Q K^T and dP = dO V^T with a lane per key, then
 // dV^T += dO^T P and dK^T += Q^T dS, dO^T and Q^T from the transposing LDS reads.  In the
 // end the QW waves of the same keys add up.
+// Matrix units 44% busy where two waves share a SIMD (2 x 4096 tokens, 8 KV heads, 32 of
+// 128, cut every 1024: 570 us), 25% where registers hold one, whose exponentials nothing
+// covers (4001 tokens of 16 heads of 192 / 128, capped: 350 us).
 template <int DK, int DV, int QW, bool VLDS>
 struct KeyShape {
   static constexpr int KW = kTrainTile / 32, WAVES = KW * QW, BN = 32 * QW;
