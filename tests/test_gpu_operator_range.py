@@ -214,3 +214,58 @@ def test_pages_past_32_bits(gqa):
         pool.close()
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,T,H,G,dk,dv,cap", [(2, 150, 1, 1, 136, 192, 0.0), (1, 140, 2, 2, 8, 256, 0.0), (1, 133, 1, 2, 256, 8, 20.0),
+                                               (1, 200, 1, 3, 200, 64, 0.0), (400, 5, 1, 1, 64, 64, 0.0), (1, 70, 1, 64, 64, 64, 0.0),
+                                               (1, 1000, 1, 1, 72, 40, 10.0)])
+def test_odd_widths_and_counts(n, T, H, G, dk, dv, cap):
+    L = need_gpu()
+    g = np.random.default_rng(n + T + dk)
+    kvs = L.KvsMask(0)
+    q, k, v, dout = randn(g, n, T, H * G, dk), randn(g, n, T, H, dk), randn(g, n, T, H, dv), randn(g, n, T, H * G, dv)
+    death = torch.from_numpy(deaths("cut", n, T, g).astype(np.int32)).cuda()
+    out, lse = kvs.attend(q, k, v, death, cap=cap)
+    got = kvs.attend_backward(dout, q, k, v, out, lse, death, cap=cap)
+    for name, a, b in zip(("dq", "dk", "dv"), got, exact(q, k, v, dout, death, dk ** -0.5, cap)):
+        assert off(a, b) <= GRAD, (name, off(a, b))
+    kvs.close()
+
+
+def test_no_rollouts():
+    L = need_gpu()
+    kvs = L.KvsMask(0)
+    q, k, v = (torch.empty((0, 9, h, 64), dtype=torch.bfloat16, device="cuda", requires_grad=True) for h in (4, 2, 2))
+    death = torch.empty((0, 9), dtype=torch.int32, device="cuda")
+    out = kvs.attention(q, k, v, death)
+    out.sum().backward()
+    assert out.shape == (0, 9, 4, 64) and q.grad.shape == q.shape and v.grad.shape == v.shape
+    with pytest.raises((ValueError, L.LeylineError)):
+        kvs.attend(q[:, :0], k[:, :0], v[:, :0], death[:, :0])
+    with pytest.raises((ValueError, L.LeylineError)):
+        kvs.attend(q, k, v, death.long())
+    kvs.close()
+
+
+def test_weights_in_wider_rows_and_a_budget_of_nothing():
+    """A selection over weights whose rows lie apart in a wider tensor; a budget of no rows
+    keeps none, one past the rows keeps all, and other sequences' weights stay."""
+    L = need_gpu()
+    table = torch.full((3, 20), -1, dtype=torch.int32, device="cuda")
+    pool = L.Pool(torch.zeros((1, 64, 16, 576), dtype=torch.bfloat16, device="cuda"), table)
+    lens = [0, 100, 300]
+    seqs = [pool.seq_alloc(n) for n in lens]
+    wide = torch.rand((3, 1000), device="cuda")
+    before = wide.clone()
+    keep, offsets = pool.keep_heaviest(seqs[1:], [0, 400], wide, kept_weights=wide)
+    torch.cuda.synchronize()
+    assert not keep[:100].any() and keep[100:400].all() and list(offsets) == [0, 100]
+    before[seqs[1], :100] = 0   # (zeros up to the old length)
+    assert torch.equal(wide, before)
+    keep, _ = pool.keep_heaviest([seqs[2]], [7], wide, sinks=2, recent=2, kept_weights=wide)
+    torch.cuda.synchronize()
+    kept = torch.nonzero(keep[:300]).flatten()
+    assert len(kept) == 7 and kept[:2].tolist() == [0, 1] and kept[-2:].tolist() == [298, 299]
+    assert torch.equal(wide[seqs[2], :7], before[seqs[2]][kept]) and torch.equal(wide[seqs[1]], before[seqs[1]])
+    assert torch.equal(wide[:, 300:], before[:, 300:])
+    pool.close()
