@@ -26,13 +26,13 @@ constexpr int weigh_keys(int d) { return kWeighRows * (d < 128 ? d : 128) * 2; }
 // workgroup's waves share: S = Q K^T with a lane per cached row, so that the sum over
 // query rows and heads stays in one register of the lane and one owner.  Single tokens
 // are bound by reading the keys (the next head's are asked for before this one's are
-// multiplied): 64 tokens over up to 16384 rows of 8 heads of 128 287 us, 4.7 TB/s.  Chunks
+// multiplied): 64 tokens over up to 16384 rows of 8 heads of 128 265 us, 5.1 TB/s.  Chunks
 // are bound by the vector instructions of scores to weights, 27 for each matrix instruction
 // with a cap: 3 x up to 1501 tokens over 8191 rows, 32 heads of 128, 482 us (matrix units
 // 21% busy); without a cap and MLA, whose rows are longer, 657 TFLOP/s.  Larger grids take
 // several tiles a workgroup.
 template <bool MLA, int DP, int KB, bool CAP>
-__global__ __launch_bounds__(64 * kWeighWaves) __attribute__((amdgpu_waves_per_eu(2))) void weigh_kernel(WeighLaunch a) {
+__global__ __launch_bounds__(64 * kWeighWaves) __attribute__((amdgpu_waves_per_eu(!MLA && KB == 1 && DP <= 128 ? 3 : 2))) void weigh_kernel(WeighLaunch a) {
   constexpr int D = MLA ? kRowElems : DP, KK = D / 16, KEYS = 32 * KB * kWeighWaves;
   using R = Rows<D>;
   constexpr int LOADS = kWeighRows * R::CH / 64 / kWeighWaves;
@@ -79,9 +79,11 @@ __global__ __launch_bounds__(64 * kWeighWaves) __attribute__((amdgpu_waves_per_e
     // A head's keys come from memory in whole rows (256 bytes of 4 rows an instruction, 128
     // of 8 at a row's end) and change lanes through LDS, 128 values of each row at a time;
     // a lane's operands straight from memory, 32 bytes of 32 rows an instruction, took 384
-    // us instead of 289 (64 tokens over up to 16384 rows of 8 heads of 128).  MLA rows
+    // us instead of 289 (64 tokens over up to 16384 rows of 8 heads of 128).  They are read
+    // once and go past the caches: 265 instead of 278 us there.  MLA rows
     // are their own operands' length, and the way through LDS costs more than it gives
-    // (64 tokens over up to 32768 rows: 606 us, 360 without).
+    // (64 tokens over up to 32768 rows: 606 us, 360 without); past the caches, where each
+    // line is asked for four times, 634.
     bf16x8 k[KB][KK], next[KB][KK];
     constexpr int WIDE = D / 128;
     auto fetch = [&](int kvh) {
@@ -105,7 +107,7 @@ __global__ __launch_bounds__(64 * kWeighWaves) __attribute__((amdgpu_waves_per_e
           const int c = i < WIDE * 8 ? i / 8 * 16 + (lane & 15) : WIDE * 16 + (lane & 7);
           const bool in = MLA || c < live;   // (a place without a value reads the row's first one, and counts as 0)
           const uint64_t of = static_cast<uint64_t>(static_cast<uint32_t>(__shfl(static_cast<int>(row[b]), r))) * width;
-          chunk_t v = *reinterpret_cast<const chunk_t*>(base + of + (in ? c * 8 : 0));
+          chunk_t v = __builtin_nontemporal_load(reinterpret_cast<const chunk_t*>(base + of + (in ? c * 8 : 0)));
           if (!in || nothing) v = chunk_t{0u, 0u, 0u, 0u};
           next[b][i] = __builtin_bit_cast(bf16x8, v);
         }
@@ -293,11 +295,13 @@ hipError_t launch_shape(const WeighLaunch& a, hipStream_t s) {
   return a.cap == 0.f ? launch_cap<MLA, DP, KB, false>(a, s) : launch_cap<MLA, DP, KB, true>(a, s);
 }
 
-// Two blocks of cached rows a wave halve the reads of LDS per product, where the rows
-// (or the shares of many query rows) still fill the chip.
+// Two blocks of cached rows a wave halve the reads of LDS per product, which chunks gain
+// from; of single tokens, three waves of one block a SIMD ask for more at once (64 tokens
+// over up to 16384 rows, through the caches: 278 us, 287 with two blocks; heads of 64 179
+// and 195).
 template <int DP>
 hipError_t launch_dim(const WeighLaunch& a, hipStream_t s) {
-  if (a.max_rows * a.n_seqs >= 512 * 64 * kWeighWaves || a.most >= 16 * kWeighRows) return launch_shape<false, DP, 2>(a, s);
+  if (a.most >= 16 * kWeighRows) return launch_shape<false, DP, 2>(a, s);
   return launch_shape<false, DP, 1>(a, s);
 }
 
