@@ -20,8 +20,8 @@ namespace {
 // Of the 2-norm of a workgroup's dq, what may be missing for delta's sake: less than the
 // rounding of ds makes it differ by (0.0017).  Along many keys it is a few rows whose
 // weight is on few of them that come near, in few of the workgroups, and going again takes
-// as long for one as for all (4001 tokens of an MLA model, four inputs: 630 to 790 us at
-// 0.001, 625 to 670 at 0.0015; documents of 20 tokens miss 0.0012 everywhere).
+// as long for one as for all (4001 tokens of an MLA model, by the inputs: 630 to 790 us at
+// 0.001, 625 to 715 at 0.0015; documents of 20 tokens miss 0.0012 everywhere).
 constexpr float kLacks = 0.001f, kLacksLong = 0.0015f;
 constexpr int kLong = 16;   // blocks of 64 keys
 
@@ -102,7 +102,7 @@ __device__ void train_dkv_row(const TrainLaunch& a, int r, int k, int kvh, int l
 // those workgroups go again that need to.  (In one kernel, registers for the loop around
 // the loop are missing.)  The sums cost 12 us of 270 where they are lacks alone, 110 with
 // both squares over every block, 50 over every second one (4001 tokens of an MLA model,
-// capped); going again, 30 to 70 there and 14 where documents of 100 tokens are packed.
+// capped); going again, 30 to 110 there and 16 where documents of 100 tokens are packed.
 template <int DK, int DV, int BN, int WAVES, bool GLDS, bool CAP, bool FIRST>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 192 ? 1 : 2))) void train_dq_kernel(TrainLaunch a) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];

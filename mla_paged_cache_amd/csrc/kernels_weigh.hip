@@ -26,7 +26,7 @@ constexpr int weigh_keys(int d) { return kWeighRows * (d < 128 ? d : 128) * 2; }
 // workgroup's waves share: S = Q K^T with a lane per cached row, so that the sum over
 // query rows and heads stays in one register of the lane and one owner.  Single tokens
 // are bound by reading the keys (the next head's are asked for before this one's are
-// multiplied): 64 tokens over up to 16384 rows of 8 heads of 128 265 us, 5.1 TB/s.  Chunks
+// multiplied): 64 tokens over up to 16384 rows of 8 heads of 128 256 us, 5.25 TB/s.  Chunks
 // are bound by the vector instructions of scores to weights, 27 for each matrix instruction
 // with a cap: 3 x up to 1501 tokens over 8191 rows, 32 heads of 128, 482 us (matrix units
 // 21% busy); without a cap and MLA, whose rows are longer, 657 TFLOP/s.  Larger grids take
@@ -80,8 +80,7 @@ __global__ __launch_bounds__(64 * kWeighWaves) __attribute__((amdgpu_waves_per_e
     // of 8 at a row's end) and change lanes through LDS, 128 values of each row at a time;
     // a lane's operands straight from memory, 32 bytes of 32 rows an instruction, took 384
     // us instead of 289 (64 tokens over up to 16384 rows of 8 heads of 128).  They are read
-    // once and go past the caches: 265 instead of 278 us there.  MLA rows
-    // are their own operands' length, and the way through LDS costs more than it gives
+    // once and go past the caches: 256 instead of 278 us there.  MLA rows are their own operands' length, and the way through LDS costs more than it gives
     // (64 tokens over up to 32768 rows: 606 us, 360 without); past the caches, where each
     // line is asked for four times, 634.
     bf16x8 k[KB][KK], next[KB][KK];
