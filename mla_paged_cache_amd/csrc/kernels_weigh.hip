@@ -80,9 +80,10 @@ __global__ __launch_bounds__(64 * kWeighWaves) __attribute__((amdgpu_waves_per_e
     // of 8 at a row's end) and change lanes through LDS, 128 values of each row at a time;
     // a lane's operands straight from memory, 32 bytes of 32 rows an instruction, took 384
     // us instead of 289 (64 tokens over up to 16384 rows of 8 heads of 128).  They are read
-    // once and go past the caches: 256 instead of 278 us there.  MLA rows are their own operands' length, and the way through LDS costs more than it gives
-    // (64 tokens over up to 32768 rows: 606 us, 360 without); past the caches, where each
-    // line is asked for four times, 634.
+    // once and go past the caches: 256 instead of 278 us there.  MLA rows are their own
+    // operands' length, and the way through LDS costs more than it gives (64 tokens over up
+    // to 32768 rows: 606 us, 360 without); past the caches, where each line is asked for
+    // four times, 634.
     bf16x8 k[KB][KK], next[KB][KK];
     constexpr int WIDE = D / 128;
     auto fetch = [&](int kvh) {
