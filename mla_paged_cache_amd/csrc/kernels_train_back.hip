@@ -8,22 +8,26 @@
 //
 // The out that comes is rounded to bf16, and delta from it is off by as much; where few
 // keys hold a query's weight, dout . v - delta cancels, and that error is what is left.
-// Since the weights sum to 1, sum_k p (dout . v - delta) is what delta lacks: the dq
-// kernel adds that sum, and dk and dv are worked out with the delta that it corrected;
-// where it matters for dq, a workgroup goes along its keys a second time.  ds and p are
-// rounded to bf16 for the products after them, half a step (2^-8) of each.
+// Since the weights sum to 1, sum_k p (dout . v - delta) is what delta lacks: the dq kernel
+// adds that sum, and dk and dv are worked out with the delta that it corrected.  dq itself
+// takes the query's weighted mean key, sum_k p k, off its keys: sum_k ds k is the same for
+// the ds of the formula, whose sum is 0, and neither an error of delta nor what ds is
+// rounded by then counts with what the keys share, or with the one key that holds the
+// weight.  ds and p are rounded to bf16 for the products after them, half a step (2^-8) of
+// each.
 #include "train_common.h"
 
 namespace ll {
 namespace {
 
-// Of the 2-norm of a workgroup's dq, what may be missing for delta's sake: less than the
-// rounding of ds makes it differ by (0.0017).  Along many keys it is a few rows whose
-// weight is on few of them that come near, in few of the workgroups, and going again takes
-// as long for one as for all (4001 tokens of an MLA model, by the inputs: 630 to 790 us at
-// 0.001, 625 to 715 at 0.0015; documents of 20 tokens miss 0.0012 everywhere).
-constexpr float kLacks = 0.001f, kLacksLong = 0.0015f;
-constexpr int kLong = 16;   // blocks of 64 keys
+// x's values and c.
+__device__ __forceinline__ float sum8(bf16x8 x, float c) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 ones = {static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)};
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) c = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{x[i], x[i + 1]}, ones, c, false);
+  return c;
+}
 
 constexpr int AH = 3;   // steps that a product's operands are read ahead (5: 2% slower)
 
@@ -93,27 +97,30 @@ __device__ void train_dkv_row(const TrainLaunch& a, int r, int k, int kvh, int l
 //
 // dq: a workgroup takes 32 * WAVES queries of a head and goes along the keys that they
 // see, as the forward kernel does: S^T = K Q^T and dP^T = V dO^T with the queries in
-// registers, then dQ^T += K^T dS^T, K^T from the transposing LDS reads.
-// GLDS: dO lies in LDS, where the registers hold no more.
-// Bound by its registers: two waves a SIMD, matrix units 39% busy (2 x 4096 tokens, 8 KV
-// heads, 32 of 128, cut every 1024: 340 us; 4001 tokens of 16 heads of 192 / 128, capped:
-// 265 us, 30%).
-// FIRST: delta is from the rounded out, and is corrected; not FIRST: it is correct, and
-// those workgroups go again that need to.  (In one kernel, registers for the loop around
-// the loop are missing.)  The sums cost 12 us of 270 where they are lacks alone, 110 with
-// both squares over every block, 50 over every second one (4001 tokens of an MLA model,
-// capped); going again, 30 to 110 there and 16 where documents of 100 tokens are packed.
-template <int DK, int DV, int BN, int WAVES, bool GLDS, bool CAP, bool FIRST>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 192 ? 1 : 2))) void train_dq_kernel(TrainLaunch a) {
+// registers, then dQ^T += K^T dS^T and the weighted mean key's K^T W^T, K^T from the
+// transposing LDS reads, once for both.
+// GLDS: dO lies in LDS, where the registers of two waves a SIMD hold no more (keys are
+// then taken 32 at a time, so that two workgroups fit).
+// Bound by its registers: two waves a SIMD, one where heads are wider than 128 (2 x 4096
+// tokens, 8 KV heads, 32 of 128, cut every 1024: 430 us; 4001 tokens of 16 heads of 192 /
+// 128, capped: 304 us).  One wave a SIMD for heads of 128, 64 keys at a time: 8% slower.
+// With w = p (under a cap p times its slope), rounded to w~, and ds from delta and rounded
+// to ds~, what delta lacks is L = sum p (dp - delta), and
+//   dq = sum ds~ k - (sum ds~ - sum ds + L sum w) / sum w~ * sum w~ k;
+// without a cap sum ds is L and sum w is 1.  The rounded sums are those of the products'
+// own operands, so that a key with nearly all weight drops out whatever it was rounded by.
+// (Going along the keys again with the corrected delta instead leaves the rounding of ds
+// times what the keys share: 0.005 of dq where each key value's mean is 3 standard
+// deviations.)
+template <int DK, int DV, int BN, int WAVES, bool GLDS, bool CAP>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 128 ? 1 : 2))) void train_dq_kernel(TrainLaunch a) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  const int unit = blockIdx.x;
-  if (!FIRST && !a.again[unit]) return;
   using KR = Rows<DK>;
   using VR = Rows<DV>;
   constexpr int STAGE = BN * (KR::BYTES + VR::BYTES) + kTrainBlock * 4;   // keys, values, death times
   constexpr int DOUT = 2 * STAGE;   // where dO lies
   constexpr int KB = BN / 32, KK = DK / 16, VK = DV / 16, DB = DK / 32, PARTS = kTrainBlock / BN;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & (WAVES - 1);
   const int pairs = a.n * a.kv_heads, pair = blockIdx.x % pairs, rest = blockIdx.x / pairs;
   const int r = pair / a.kv_heads, kvh = pair % a.kv_heads, h = kvh * a.group + rest % a.group;
   const int tiles = (a.n_pad + 32 * WAVES - 1) / (32 * WAVES), tile = tiles - 1 - rest / a.group;
@@ -151,14 +158,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
     VR::template load<BN, WAVES>(dst + BN * KR::BYTES, vp, a.v.ts, row, part * BN, live_v, wave, lane);
     if (wave == 0) reinterpret_cast<int*>(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES))[lane] = key.death;   // the whole block's
   };
-  f32x16 o[DB];
-  // sums of p (dp - delta), and of p's squares and its own over the blocks that are seen in
-  // part and every second one of the others
-  float lacks = 0.f, p2 = 0.f, t2 = 0.f;
+  f32x16 o[DB], mean[DB];   // sums of ds~ k and of w~ k
+  float lacks = 0.f, ds_sum = 0.f, w_sum = 0.f, ds_rounded = 0.f, w_rounded = 0.f;
 #pragma unroll
   for (int d = 0; d < DB; ++d)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+    for (int i = 0; i < 16; ++i) o[d][i] = mean[d][i] = 0.f;
 
   // tiles of a block's keys: this one, the next one (on its way), and the block after
   // that, whose keys are known a tile before they are asked for
@@ -195,6 +200,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.f;
       stream<KK, AH>([&](int k) { return KR::straight(ks, b * 32, k); }, [&](int k, bf16x8 x) { s = mfma(x, q[k], s); });
+      if constexpr (CAP) tanh_all(s, capped);
       if constexpr (GLDS) {
         bf16x8 z[2];
         stream<2 * VK, 4>([&](int x) { return x & 1 ? VR::straight(gs, 0, x / 2) : VR::straight(vs, b * 32, x / 2); },
@@ -205,31 +211,35 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
       } else {
         stream<VK, AH>([&](int k) { return VR::straight(vs, b * 32, k); }, [&](int k, bf16x8 x) { dp = mfma(x, g[k], dp); });
       }
-      if constexpr (CAP) tanh_all(s, capped);
-      auto pairs = [&](auto plain, uint32_t seen) {
+      if (!all) {   // no weight and no ds for what is not seen (a tanh of -1 has no slope)
+        const uint32_t seen = seen_bits(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES), part * BN + b * 32, k0, mine, lane);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float p = exp2_(__builtin_fmaf(s[i], c2, -ref)), t = p * (dp[i] - delta);
-          if (!plain && !(seen >> i & 1)) p = t = 0.f;
-          if (FIRST) lacks += t;
-          if (FIRST && !plain) {
-            p2 = __builtin_fmaf(p, p, p2);
-            t2 = __builtin_fmaf(t, t, t2);
-          }
-          s[i] = CAP ? t * (1.f - s[i] * s[i]) : t;
-        }
-      };
-      if (all && (!FIRST || (block & 1))) {
-        pairs(std::true_type{}, 0u);
-      } else {
-        uint32_t seen = ~0u;
-        if (!all) seen = seen_bits(smem + stage * STAGE + BN * (KR::BYTES + VR::BYTES), part * BN + b * 32, k0, mine, lane);
-        pairs(std::false_type{}, seen);
+        for (int i = 0; i < 16; ++i)
+          if (!(seen >> i & 1)) s[i] = CAP ? -1.f : -__builtin_inff(), dp[i] = delta;
       }
-      const bf16x8 ds[2] = {operand(s, 0), operand(s, 1)};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float p = exp2_(__builtin_fmaf(s[i], c2, -ref)), t = p * (dp[i] - delta);
+        lacks += t;
+        if constexpr (CAP) {
+          const float slope = __builtin_fmaf(-s[i], s[i], 1.f);
+          w_sum += p *= slope;
+          ds_sum += t *= slope;
+        }
+        s[i] = p, dp[i] = t;
+      }
+      // (sums here and now: the compiler otherwise leaves them to the loop's end, and keeps what they add until then)
+      asm volatile("" : "+v"(lacks), "+v"(w_sum), "+v"(ds_sum));
+      const bf16x8 ds[2] = {operand(dp, 0), operand(dp, 1)}, w[2] = {operand(s, 0), operand(s, 1)};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) ds_rounded = sum8(ds[x], ds_rounded), w_rounded = sum8(w[x], w_rounded);
+      asm volatile("" : "+v"(ds_rounded), "+v"(w_rounded));
       __builtin_amdgcn_sched_barrier(0);
       stream<2 * DB, AH>([&](int x) { return KR::columns(cs, b * 32 + x / DB * 16, x % DB); },
-                         [&](int x, bf16x8 y) { o[x % DB] = mfma(y, ds[x / DB], o[x % DB]); });
+                         [&](int x, bf16x8 y) {
+                           o[x % DB] = mfma(y, ds[x / DB], o[x % DB]);
+                           mean[x % DB] = mfma(y, w[x / DB], mean[x % DB]);
+                         });
     }
     stage ^= 1;
     if (!ends) {
@@ -242,34 +252,13 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
   __builtin_amdgcn_s_waitcnt(0x0F70);   // loads on their way into LDS
   if (walk.rows_only) {
     for (int i = q0 + wave; i <= q1; i += WAVES) train_dq_row(a, r, i, h, lane);
-    if (threadIdx.x == 0) a.again[unit] = 0;
     return;
   }
-  if constexpr (FIRST) {
-    // What delta lacks, times sum_k p k, is missing from dq = sum_k ds k: of the workgroup's
-    // rows, and keys that know nothing of each other, lacks^2 sum p^2 of sum t^2.
-    lacks += __shfl_xor(lacks, 32);
-    p2 += __shfl_xor(p2, 32);
-    t2 += __shfl_xor(t2, 32);
-    const bool weighs = mine < a.n_pad && ref < __builtin_inff();
-    if (weighs && lane < 32) a.delta[at_row] = delta + lacks;
-    float missing = weighs ? lacks * lacks * p2 : 0.f, of = weighs ? t2 : 0.f;
-    for (int x = 16; x >= 1; x >>= 1) {
-      missing += __shfl_xor(missing, x);
-      of += __shfl_xor(of, x);
-    }
-    __syncthreads();   // nobody reads the tiles any more
-    float* const sums = reinterpret_cast<float*>(smem);
-    if (lane == 0) sums[2 * wave] = missing, sums[2 * wave + 1] = of;
-    __syncthreads();
-    missing = of = 0.f;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) missing += sums[2 * w], of += sums[2 * w + 1];
-    const float most = walk.blocks > kLong ? kLacksLong : kLacks;
-    const bool again = missing > most * most * of;
-    if (threadIdx.x == 0) a.again[unit] = again;
-    if (again) return;
-  }
+  auto both = [](float x) { return x + __shfl_xor(x, 32); };
+  lacks = both(lacks), ds_rounded = both(ds_rounded), w_rounded = both(w_rounded);
+  if constexpr (CAP) ds_rounded += lacks * both(w_sum) - both(ds_sum);
+  const float by = w_rounded > 0.f ? ds_rounded / w_rounded : 0.f;   // (0: no key's weight is left)
+  if (lane < 32 && mine < a.n_pad && ref < __builtin_inff()) a.delta[at_row] = delta + lacks;
   if (mine >= a.n_pad) return;
   uint16_t* const out = place(a.dq, r, mine, h);
 #pragma unroll
@@ -277,7 +266,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const int col = d * 32 + product_row(i, lane);
-      f32x4 x = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]} * a.scale;
+      f32x4 x = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+      x = (x - f32x4{mean[d][i], mean[d][i + 1], mean[d][i + 2], mean[d][i + 3]} * by) * a.scale;
       if (ref == __builtin_inff()) x = f32x4{0.f, 0.f, 0.f, 0.f};   // no weight at all, whatever the keys hold
       if (col < a.dk) *reinterpret_cast<bf16x4*>(out + col) = __builtin_convertvector(x, bf16x4);
     }
@@ -563,15 +553,14 @@ __global__ __launch_bounds__(256) void train_join_kernel(TrainLaunch a) {
 template <int DK, int DV, int BN, int QW, bool VLDS, int OCC, bool CAP>
 hipError_t launch_shape(const TrainLaunch& a, hipStream_t s) {
   using K = KeyShape<DK, DV, QW, VLDS>;
-  constexpr bool GLDS = DK == 192;
+  constexpr bool GLDS = DK == 128;
   constexpr int waves = kTrainTile / 32, lds = 2 * (BN * (DK + DV) * 2 + kTrainBlock * 4) + (GLDS ? kTrainTile * DV * 2 : 0);
-  hipError_t e = allow_lds<train_dq_kernel<DK, DV, BN, waves, GLDS, CAP, true>>(lds);
-  if (e == hipSuccess) e = allow_lds<train_dq_kernel<DK, DV, BN, waves, GLDS, CAP, false>>(lds);
+  hipError_t e = allow_lds<train_dq_kernel<DK, DV, BN, waves, GLDS, CAP>>(lds);
   if (e == hipSuccess) e = allow_lds<train_dkv_kernel<DK, DV, QW, VLDS, OCC, CAP>>(K::LDS);
   if (e != hipSuccess) return e;
   const int64_t tiles = (a.n_pad + kTrainTile - 1) / kTrainTile;
   const dim3 queries(static_cast<unsigned>(a.n * a.heads * tiles));
-  train_dq_kernel<DK, DV, BN, waves, GLDS, CAP, true><<<queries, dim3(64 * waves), lds, s>>>(a);
+  train_dq_kernel<DK, DV, BN, waves, GLDS, CAP><<<queries, dim3(64 * waves), lds, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   train_dkv_kernel<DK, DV, QW, VLDS, OCC, CAP>
@@ -582,10 +571,8 @@ hipError_t launch_shape(const TrainLaunch& a, hipStream_t s) {
     constexpr int blocks = kTrainTile * (DK + DV) / 4 / 256;
     train_join_kernel<DK, DV><<<dim3(static_cast<unsigned>(a.n * a.kv_heads * tiles * blocks)), dim3(256), 0, s>>>(a);
     e = hipGetLastError();
-    if (e != hipSuccess) return e;
   }
-  train_dq_kernel<DK, DV, BN, waves, GLDS, CAP, false><<<queries, dim3(64 * waves), lds, s>>>(a);
-  return hipGetLastError();
+  return e;
 }
 
 template <int DK, int DV, int BN, int QW, bool VLDS, int OCC>
@@ -600,8 +587,8 @@ hipError_t launch_train_back(const TrainLaunch& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   switch (head_shape(a.dk, a.dv).dk) {
     case 64: return launch_cap<64, 64, 64, 2, false, 2>(a, s);
-    case 128: return launch_cap<128, 128, 64, 2, true, 2>(a, s);
-    case 192: return launch_cap<192, 128, 32, 1, true, 1>(a, s);
+    case 128: return launch_cap<128, 128, 32, 2, true, 2>(a, s);
+    case 192: return launch_cap<192, 128, 64, 1, true, 1>(a, s);
     default: return launch_cap<256, 256, 32, 1, true, 1>(a, s);
   }
 }

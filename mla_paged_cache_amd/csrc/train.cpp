@@ -90,7 +90,6 @@ int64_t lay_out(TrainLaunch* a, bool backward, char* at) {
     a->odd_q = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
     a->odd_do = reinterpret_cast<uint32_t*>(take(nb * a->heads * 4));
     a->delta = reinterpret_cast<float*>(take(int64_t{a->n} * a->heads * a->n_pad * 4));
-    a->again = reinterpret_cast<int32_t*>(take(int64_t{a->n} * a->heads * ceil_div(a->n_pad, kTrainTile) * 4));
     a->ref = reinterpret_cast<float*>(take(int64_t{a->n} * a->heads * a->n_pad * 4));
     const int64_t units = int64_t{a->n} * a->kv_heads * ceil_div(a->n_pad, kTrainTile);
     const HeadShape w = head_shape(a->dk, a->dv);

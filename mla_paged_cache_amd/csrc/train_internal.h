@@ -73,8 +73,7 @@ struct TrainLaunch {
   uint32_t* odd_v;               // the same of v
   uint32_t* odd_q;               // [n][heads][blocks]: of q and dout, any query
   uint32_t* odd_do;
-  float* delta;                  // [n][heads][n_pad]: sum of dout * out; corrected by the first kernel of dq
-  int32_t* again;                // [n * heads * tiles]: whether dq of a tile of queries needs the corrected one
+  float* delta;                  // [n][heads][n_pad]: sum of dout * out; corrected by the kernel of dq
   float* ref;                    // [n][heads][n_pad]: lse in base 2; infinity where there is no weight
 
   int32_t* used;                 // [n * kv_heads * tiles]: shares that a tile of keys was cut into
