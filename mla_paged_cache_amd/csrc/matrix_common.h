@@ -219,19 +219,22 @@ __device__ __forceinline__ void stream(Read&& read, Use&& use) {
 // coefficients hold them, for c of a size where its powers do.
 struct Tanh {
   float k[5];                    // s * sum k_i (s^2)^i
-  float most;                    // |s| up to which that holds (-1: c is outside [2^-12, 2^12])
+  float most;                    // |s| up to which that holds (-1: c is outside [2^-12, 2^12], or by above 2^120 / c^9)
   float c, by;
   static __device__ __forceinline__ float uniform(float x) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x))); }
   __device__ __forceinline__ Tanh(float c_, float by_) : c(uniform(c_)), by(uniform(by_)) {
     const float w = c * c;
     const float b[5] = {0.99999999f, -0.33333072f, 0.13324829f, -0.052989241f, 0.017141319f};
-    float x = c * by;
+    float x = c * by, last = x;
 #pragma unroll
     for (int i = 0; i < 5; ++i) {
       k[i] = uniform(b[i] * x);
+      last = x;
       x *= w;
     }
-    most = uniform(fabsf(c) >= 0x1p-12f && fabsf(c) <= 0x1p12f ? 0.5f / fabsf(c) : -1.f);
+    // (an infinite coefficient times a score of 0 would be NaN; one that vanishes belongs to
+    // scores below 2^-12, which it moves by 2^-26)
+    most = uniform(fabsf(c) >= 0x1p-12f && fabsf(c) <= 0x1p12f && fabsf(last) <= 0x1p120f ? 0.5f / fabsf(c) : -1.f);
   }
   __device__ __forceinline__ float slope(float s) const {   // of the chord from 0
     const float w = s * s;
