@@ -4,6 +4,8 @@
 //   out = sum_k softmax(s)_k v_k,  lse = log sum_k exp s_k,
 // in one pass over the keys that keeps the running maximum, sum and weighted values in
 // float32.  Scores are kept in base 2.
+#include <algorithm>
+
 #include "train_common.h"
 
 namespace ll {
@@ -152,18 +154,18 @@ __device__ void list_keys(const TrainLaunch& a, int r, int e, uint32_t (*totals)
 // What the workspace says of keys and of blocks of 64 tokens, and for the backward pass
 // delta.  Workgroups: first the epochs' lists; then a wave per block and unit: 0 the
 // keys' death times; the KV heads' values; backward also their keys, every head's dout
-// (with delta) and its queries.
+// (with delta) and its queries.  This dispatch begins with workgroup `first_group`.
 template <bool BACKWARD>
-__global__ __launch_bounds__(kScanThreads) void train_scan_kernel(TrainLaunch a) {
+__global__ __launch_bounds__(kScanThreads) void train_scan_kernel(TrainLaunch a, int first_group) {
   __shared__ uint32_t totals[2][kScanWaves];
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, group = first_group + static_cast<int>(blockIdx.x);
   const int lists = a.n * (a.epochs + BACKWARD);
-  if (static_cast<int>(blockIdx.x) < lists) {
-    list_keys<BACKWARD>(a, blockIdx.x % a.n, a.epochs + BACKWARD - 1 - blockIdx.x / a.n, totals);
+  if (group < lists) {
+    list_keys<BACKWARD>(a, group % a.n, a.epochs + BACKWARD - 1 - group / a.n, totals);
     return;
   }
   const int units = 1 + (BACKWARD ? 2 * a.kv_heads + 2 * a.heads : a.kv_heads);
-  int64_t id = static_cast<int64_t>(blockIdx.x - lists) * kScanWaves + (threadIdx.x >> 6);
+  int64_t id = static_cast<int64_t>(group - lists) * kScanWaves + (threadIdx.x >> 6);
   const int b = static_cast<int>(id % a.blocks);
   id /= a.blocks;
   const int r = static_cast<int>(id / units);
@@ -420,13 +422,20 @@ hipError_t launch_cap(const TrainLaunch& a, hipStream_t s) {
 
 }  // namespace
 
+// As many dispatches as it takes: many short rollouts have more work-items than the 2^32 - 1
+// that one holds.
 hipError_t launch_train_scan(const TrainLaunch& a, bool backward, hipStream_t s) {
+  constexpr int64_t most = 0xFFFFFFFFll / kScanThreads;
   const int64_t units = 1 + (backward ? 2 * a.kv_heads + 2 * a.heads : a.kv_heads);
   const int64_t lists = int64_t{a.n} * (a.epochs + (backward ? 1 : 0));
-  const dim3 g(static_cast<unsigned>(lists + (a.n * units * a.blocks + kScanWaves - 1) / kScanWaves));
-  if (backward) train_scan_kernel<true><<<g, dim3(kScanThreads), 0, s>>>(a);
-  else train_scan_kernel<false><<<g, dim3(kScanThreads), 0, s>>>(a);
-  return hipGetLastError();
+  const int64_t groups = lists + (a.n * units * a.blocks + kScanWaves - 1) / kScanWaves;
+  for (int64_t at = 0; at < groups; at += most) {
+    const dim3 g(static_cast<unsigned>(std::min(groups - at, most)));
+    if (backward) train_scan_kernel<true><<<g, dim3(kScanThreads), 0, s>>>(a, static_cast<int>(at));
+    else train_scan_kernel<false><<<g, dim3(kScanThreads), 0, s>>>(a, static_cast<int>(at));
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_train(const TrainLaunch& a, hipStream_t s) {
