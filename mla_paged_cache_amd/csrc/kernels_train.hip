@@ -120,7 +120,7 @@ __device__ void list_keys(const TrainLaunch& a, int r, int e, uint32_t (*totals)
     for (int k = threadIdx.x; k < a.n_pad; k += kScanThreads) {
       const int d = min(death[k], a.n_pad);
       before += d > k && d > after;
-      sees += max(d - k, 0);
+      sees += d > k ? d - k : 0;   // (a death time may lie 2^31 before its key)
     }
     for (int x = 32; x >= 1; x >>= 1) {
       before += __shfl_xor(before, x);
