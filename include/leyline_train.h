@@ -11,7 +11,9 @@
  * Values are bf16; sums, softmax statistics and gradients' sums are float32, and each
  * result is rounded to bf16 once.  For the matrix instructions the softmax weights and
  * the scores' gradients are rounded to bf16 as well (2^-9 of each on average, of the
- * order of the results' own rounding).
+ * order of the results' own rounding; in dq a score gradient's rounding counts with the
+ * key's distance from the query's weighted mean key, so that what the keys have in
+ * common adds nothing to it).
  *
  * What a query does not see never reaches its result or the gradients of others,
  * whatever it holds.  The same call gives the same bits.

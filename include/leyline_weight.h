@@ -56,7 +56,9 @@ typedef struct {
  *   weights[s][j] = decay * weights[s][j] + sum_t sum_h exp(s_thj - lse[t][h])
  * over the tokens t of sequence s that see row j.  (A step that goes through several
  * layers decays in the first one, if at all.)  The sum over a token's rows is the
- * number of heads.  A token and head whose lse is -inf sees nothing and adds nothing.
+ * number of heads (a score and its lse are float32: their roundings, 2^-24 of each, are
+ * the weights' relative errors).  A token and head whose lse is -inf sees nothing and
+ * adds nothing.
  * Rows past a sequence's last one, and other sequences', are left as they were; a
  * sequence without tokens in the step decays too.  Scores and sums are float32, in a
  * fixed order: the same call on the same plan gives the same bits.  May be captured as

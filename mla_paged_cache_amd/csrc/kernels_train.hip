@@ -250,10 +250,11 @@ __global__ __launch_bounds__(kScanThreads) void train_scan_kernel(TrainLaunch a,
 // The running maximum is only a reference: it moves when a score (in base 2) exceeds it
 // by more than 8, so weights stay below 2^8 and most tiles scale nothing.
 //
-// Bound by the matrix and the vector instructions of the same waves, of which registers
-// hold two a SIMD (one where heads are 256 wide): 2 x 8192 tokens, 8 KV heads, 32 of 128,
-// cut every 2048 and capped, 1.03 ms: 660 TFLOP/s of the pairs that are seen; 8192 tokens
-// uncut 690 to 800 (490 where heads are 256 wide).  Tiles of 64 keys, 32 where heads are
+// Bound by the matrix and the vector instructions of the same waves (30% and 62% of the
+// time), of which registers hold two a SIMD (one where heads are 256 wide): 2 x 8192 tokens,
+// 8 KV heads, 32 of 128, cut every 2048 and capped, 1.00 ms, the call with its scan 1.02:
+// 670 TFLOP/s of the pairs that are seen; 8192 tokens
+// uncut 650 to 840 (500 where heads are 256 wide).  Tiles of 64 keys, 32 where heads are
 // wider than 128, for two stages and two workgroups in LDS.
 template <int DK, int DV, int BN, int WAVES, bool CAP>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK > 192 ? 1 : 2))) void train_kernel(TrainLaunch a) {

@@ -102,8 +102,9 @@ __device__ void train_dkv_row(const TrainLaunch& a, int r, int k, int kvh, int l
 // GLDS: dO lies in LDS, where the registers of two waves a SIMD hold no more (keys are
 // then taken 32 at a time, so that two workgroups fit).
 // Bound by its registers: two waves a SIMD, one where heads are wider than 128 (2 x 4096
-// tokens, 8 KV heads, 32 of 128, cut every 1024: 430 us; 4001 tokens of 16 heads of 192 /
-// 128, capped: 304 us).  One wave a SIMD for heads of 128, 64 keys at a time: 8% slower.
+// tokens, 8 KV heads, 32 of 128, cut every 1024: 394 us, matrix units busy 41% and vector
+// units 45% of the time; 4001 tokens of 16 heads of 192 / 128, capped: 273 us, 30% and
+// 42%).  One wave a SIMD for heads of 128, 64 keys at a time: the whole call 8% slower.
 // With w = p (under a cap p times its slope), rounded to w~, and ds from delta and rounded
 // to ds~, what delta lacks is L = sum p (dp - delta), and
 //   dq = sum ds~ k - (sum ds~ - sum ds + L sum w) / sum w~ * sum w~ k;
@@ -279,9 +280,10 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
 // LDS, of which a wave takes 32: S = Q K^T and dP = dO V^T with a lane per key, then
 // dV^T += dO^T P and dK^T += Q^T dS, dO^T and Q^T from the transposing LDS reads.  In the
 // end the QW waves of the same keys add up.
-// Matrix units 44% busy where two waves share a SIMD (2 x 4096 tokens, 8 KV heads, 32 of
-// 128, cut every 1024: 570 us), 25% where registers hold one, whose exponentials nothing
-// covers (4001 tokens of 16 heads of 192 / 128, capped: 350 us).
+// Matrix units busy 39% and vector units 55% of the time where two waves share a SIMD (2 x
+// 4096 tokens, 8 KV heads, 32 of 128, cut every 1024: 561 us), 25% and 44% where registers
+// hold one, whose exponentials nothing covers (4001 tokens of 16 heads of 192 / 128, capped:
+// 310 us).
 template <int DK, int DV, int QW, bool VLDS>
 struct KeyShape {
   static constexpr int KW = kTrainTile / 32, WAVES = KW * QW, BN = 32 * QW;

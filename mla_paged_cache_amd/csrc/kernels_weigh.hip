@@ -26,11 +26,11 @@ constexpr int weigh_keys(int d) { return kWeighRows * (d < 128 ? d : 128) * 2; }
 // workgroup's waves share: S = Q K^T with a lane per cached row, so that the sum over
 // query rows and heads stays in one register of the lane and one owner.  Single tokens
 // are bound by reading the keys (the next head's are asked for before this one's are
-// multiplied): 64 tokens over up to 16384 rows of 8 heads of 128 256 us, 5.25 TB/s.  Chunks
+// multiplied): 64 tokens over up to 16384 rows of 8 heads of 128 249 us, 5.4 TB/s.  Chunks
 // are bound by the vector instructions of scores to weights, 27 for each matrix instruction
-// with a cap: 3 x up to 1501 tokens over 8191 rows, 32 heads of 128, 482 us (matrix units
-// 21% busy); without a cap and MLA, whose rows are longer, 657 TFLOP/s.  Larger grids take
-// several tiles a workgroup.
+// with a cap: 3 x up to 1501 tokens over 8191 rows, 32 heads of 128, 470 us (vector units
+// busy 69%, matrix units 21% of the time); without a cap and MLA, whose rows are longer, 657
+// TFLOP/s.  Larger grids take several tiles a workgroup.
 template <bool MLA, int DP, int KB, bool CAP>
 __global__ __launch_bounds__(64 * kWeighWaves) __attribute__((amdgpu_waves_per_eu(!MLA && KB == 1 && DP <= 128 ? 3 : 2))) void weigh_kernel(WeighLaunch a) {
   constexpr int D = MLA ? kRowElems : DP, KK = D / 16, KEYS = 32 * KB * kWeighWaves;
