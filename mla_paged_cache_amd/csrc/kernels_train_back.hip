@@ -102,8 +102,8 @@ __device__ void train_dkv_row(const TrainLaunch& a, int r, int k, int kvh, int l
 // GLDS: dO lies in LDS, where the registers of two waves a SIMD hold no more (keys are
 // then taken 32 at a time, so that two workgroups fit).
 // Bound by its registers: two waves a SIMD, one where heads are wider than 128 (2 x 4096
-// tokens, 8 KV heads, 32 of 128, cut every 1024: 394 us, matrix units busy 41% and vector
-// units 45% of the time; 4001 tokens of 16 heads of 192 / 128, capped: 273 us, 30% and
+// tokens, 8 KV heads, 32 of 128, cut every 1024: 376 us, matrix units busy 43% and vector
+// units 47% of the time; 4001 tokens of 16 heads of 192 / 128, capped: 274 us, 30% and
 // 42%).  One wave a SIMD for heads of 128, 64 keys at a time: the whole call 8% slower.
 // With w = p (under a cap p times its slope), rounded to w~, and ds from delta and rounded
 // to ds~, what delta lacks is L = sum p (dp - delta), and
@@ -230,7 +230,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
         s[i] = p, dp[i] = t;
       }
       // (sums here and now: the compiler otherwise leaves them to the loop's end, and keeps what they add until then)
-      asm volatile("" : "+v"(lacks), "+v"(w_sum), "+v"(ds_sum));
+      asm volatile("" : "+v"(lacks));
+      if constexpr (CAP) asm volatile("" : "+v"(w_sum), "+v"(ds_sum));
       const bf16x8 ds[2] = {operand(dp, 0), operand(dp, 1)}, w[2] = {operand(s, 0), operand(s, 1)};
 #pragma unroll
       for (int x = 0; x < 2; ++x) ds_rounded = sum8(ds[x], ds_rounded), w_rounded = sum8(w[x], w_rounded);
@@ -281,7 +282,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK >
 // dV^T += dO^T P and dK^T += Q^T dS, dO^T and Q^T from the transposing LDS reads.  In the
 // end the QW waves of the same keys add up.
 // Matrix units busy 39% and vector units 55% of the time where two waves share a SIMD (2 x
-// 4096 tokens, 8 KV heads, 32 of 128, cut every 1024: 561 us), 25% and 44% where registers
+// 4096 tokens, 8 KV heads, 32 of 128, cut every 1024: 559 us), 25% and 44% where registers
 // hold one, whose exponentials nothing covers (4001 tokens of 16 heads of 192 / 128, capped:
 // 310 us).
 template <int DK, int DV, int QW, bool VLDS>
