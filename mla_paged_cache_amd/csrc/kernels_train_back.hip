@@ -13,8 +13,8 @@
 // takes the query's weighted mean key, sum_k p k, off its keys: sum_k ds k is the same for
 // the ds of the formula, whose sum is 0 (under a cap only what the sum is off by is taken
 // off), and neither an error of delta nor what ds is rounded by then counts with what the
-// keys share, or with the one key that holds the weight.  ds and p are rounded to bf16 for the products after them, half a step (2^-8) of
-// each.
+// keys share, or with the one key that holds the weight.  ds and p are rounded to bf16 for
+// the products after them, half a step (2^-8) of each.
 #include "train_common.h"
 
 namespace ll {
